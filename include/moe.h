@@ -110,6 +110,14 @@ typedef struct moe_config {
  * on long K but the slower weight gradient at this layer's per-expert K. */
 #define MOE_FLAG_WGRAD_PAIR 2
 
+/* Quantised input. With this flag moe_forward and moe_dispatch take MX(x) as
+ * the workspace already holds it (views XQ, XQ_SF with zero padding rows, and
+ * XQ_SFC: what moe_add_rmsnorm writes when it is given these views) instead of
+ * quantising x themselves. The results are the bytes of a call without the flag
+ * whenever the views hold MX of the same x. moe_forward then does not read x,
+ * which moe_route and moe_backward still do. */
+#define MOE_FLAG_X_QUANTIZED 4
+
 /* Bytes of workspace the layer needs for this shape (schedule, saved
  * activations for backward, ring buffers, staging). */
 MOE_API int moe_workspace_size(const moe_config_t* cfg, size_t* bytes);
@@ -392,6 +400,96 @@ MOE_API int moe_expert_gemm_nvfp4_push(const moe_config_t* cfg, int N, int K, co
  * ((r/128)*(K/128) + kb/4)*512, byte (r%32)*16 + (r/32%4)*4 + kb%4.
  * rows, K multiples of 128. */
 MOE_API int moe_scales_to_tiled(const void* canon, int rows, int K, void* tiled, moe_stream_t stream);
+
+/* Residual add + RMSNorm in front of the layer, with the MX quantisation the
+ * experts read.
+ *   h = x + residual, rstd = (mean(h^2) + eps)^(-1/2) per row, y = h rstd gamma.
+ *   x, residual, h, y: bf16 [T][d]; gamma: bf16 [d]; rstd: fp32 [T].
+ *   residual may be NULL (h = x); h and rstd may be NULL (not written). h may be
+ *   x or residual. The sum, the statistics and y are fp32 until their one
+ *   rounding to bf16 at the store: y comes from the unrounded sum.
+ *   codes (optional): E4M3 codes of MX(y) along d, blocks of 32 (moe_quantize_mxfp8
+ *   of the bf16 y, the same bytes), with its scales in one or both of
+ *   scales [T][d/32] and scales_tiled (the layout of moe_scales_to_tiled; codes
+ *   and scales_tiled then have ceil128(T) rows, those past T written as zero).
+ * T >= 0; d a multiple of 8 up to MOE_NORM_MAX_D, of 32 with codes and of 128
+ * with scales_tiled; eps >= 0. bf16 tensors and codes on 16-byte boundaries.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_ARCH, MOE_ERR_CUDA. */
+#define MOE_NORM_MAX_D 16384
+MOE_API int moe_add_rmsnorm(int T, int d, const void* x, const void* residual, const void* gamma, float eps, void* h,
+                            void* y, float* rstd, void* codes, void* scales, void* scales_tiled, moe_stream_t stream);
+
+/* Gradient of moe_add_rmsnorm. With g = dy gamma and xhat = h rstd,
+ *   dx = rstd (g - xhat mean(g xhat)) + dres   (the gradient of x and of residual alike),
+ *   dgamma = sum over rows of dy xhat.
+ *   dy, dres, h, dx: bf16 [T][d]; gamma: bf16 [d]; rstd: fp32 [T], as saved by the
+ *   forward call; dgamma: fp32 [d]. dres is the gradient that reaches h on the
+ *   residual path, or NULL. dx may be dy, dres or h. dgamma is written, not
+ *   added to (zero when T = 0), in a fixed summation order.
+ *   ws: moe_add_rmsnorm_backward_workspace bytes, no initial value needed.
+ * Sizes, alignment and errors as for moe_add_rmsnorm. */
+MOE_API int moe_add_rmsnorm_backward_workspace(int T, int d, size_t* bytes);
+MOE_API int moe_add_rmsnorm_backward(int T, int d, const void* dy, const void* dres, const void* h, const void* gamma,
+                                     const float* rstd, void* dx, float* dgamma, void* ws, moe_stream_t stream);
+
+/* Latent attention over a paged cache.
+ * A cached token is one bf16 row [latent | rope] that all heads share: its key is
+ * the whole row and its value the first `latent` columns (the absorbed form: the
+ * caller multiplies q by the key up-projection before, and the output by the
+ * value up-projection after).
+ *   cache       bf16 [num_pages][page_size][latent + rope]
+ *   block_table int32 [batch][max_pages]: token j of sequence b lives in row
+ *               j % page_size of page block_table[b][j / page_size]. Entries past a
+ *               sequence's pages are never read. Pages may be shared.
+ * batch >= 0; heads 1..128; latent 128, 256, 384 or 512; rope a multiple of 8 up to
+ * 64; page_size a multiple of 8; num_pages * page_size and max_pages * page_size
+ * below 2^31; softmax_scale > 0 and finite. */
+typedef struct moe_mla_config {
+  int batch, heads, latent, rope, page_size, num_pages, max_pages;
+  float softmax_scale;
+} moe_mla_config_t;
+
+/* Workspace of the two calls below: a status word and the pieces of sequences
+ * that the work split cuts (it depends on latent only, about 45 MB at 512). Its
+ * first 16 bytes have to be zero before the first call (moe_mla_status clears them too). */
+MOE_API int moe_mla_workspace_size(const moe_mla_config_t* cfg, size_t* bytes);
+
+/* Write n new tokens into the cache. Token i (row kv + i * ld_kv, latent + rope
+ * bf16 values) goes to position pos[i] of sequence seq[i]:
+ *   latent part: RMSNorm with weight gamma [latent] (bf16) and eps; copied when
+ *     gamma is NULL;
+ *   rope part: columns (2i, 2i+1) rotated by the position's angle i,
+ *     (x cos - y sin, x sin + y cos), with cos_sin fp32 [max_pos][rope] holding
+ *     rope/2 cosines, then rope/2 sines a position; copied when cos_sin is NULL.
+ * Both in fp32, rounded to bf16 once. A token with pos < 0 is skipped (padding).
+ * A sequence, position or page out of range writes nothing for that token and
+ * sets the status to MOE_ERR_BOUNDS. Two tokens of one call must not share a place.
+ * ld_kv a multiple of 8; kv, gamma, cos_sin, cache, ws on 16-byte boundaries. */
+MOE_API int moe_mla_append(const moe_mla_config_t* cfg, int n, const void* kv, int ld_kv, const void* gamma, float eps,
+                           const float* cos_sin, int max_pos, const int32_t* seq, const int32_t* pos,
+                           const int32_t* block_table, void* cache, void* ws, moe_stream_t stream);
+
+/* Attention of one new token a sequence over its cached tokens.
+ *   q: bf16, element (b, h, c) at b * q_stride_b + h * q_stride_h + c, c < latent + rope
+ *      (strides in elements, multiples of 8).
+ *   seq_lens int32 [batch] (device): tokens of each sequence, the new one included.
+ *   out bf16 [batch][heads][latent] = sum_j p_j k_j[0:latent], p = softmax over
+ *      j < seq_lens[b] of softmax_scale q . k_j.
+ *   lse fp32 [batch][heads] (or NULL): log sum_j exp(softmax_scale q . k_j).
+ * A sequence of length 0 gets zeros and lse = -inf, and so does a row whose scores
+ * are all -inf. Cache rows past a sequence's length may hold anything, NaN included.
+ * Products take bf16 operands (P is rounded to bf16, and normalised by the sum of
+ * the rounded values) and accumulate in fp32; statistics are fp32.
+ * A length outside [0, max_pages * page_size] is clamped and a page out of range
+ * read as zeros; both set the status to MOE_ERR_BOUNDS. Lengths are read on the
+ * device only, so a captured call replays with the lengths of the time. Calls that
+ * share a workspace must be ordered by the caller. */
+MOE_API int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_t q_stride_b, int64_t q_stride_h,
+                           const void* cache, const int32_t* block_table, const int32_t* seq_lens, void* out,
+                           float* lse, void* ws, moe_stream_t stream);
+
+/* moe_status for the workspace of the latent-attention calls. */
+MOE_API int moe_mla_status(const moe_mla_config_t* cfg, void* ws, int* code, int* site, int clear, moe_stream_t stream);
 
 /* Measurement hooks (process-wide, for benchmarks; not part of the layer).
  * moe_profile_enable(1): every kernel launch of the library is bracketed by a

@@ -49,6 +49,12 @@ class MoeConfig(ctypes.Structure):
                  "n_mover_warps")]
 
 
+class MlaConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in
+                ("batch", "heads", "latent", "rope", "page_size", "num_pages", "max_pages")] + \
+               [("softmax_scale", ctypes.c_float)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, name: str, code: int):
         super().__init__("%s failed with MOE error %d" % (name, code))
@@ -58,6 +64,7 @@ class MoeError(RuntimeError):
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _CFG = ctypes.POINTER(MoeConfig)
+_MLA = ctypes.POINTER(MlaConfig)
 _SZ = ctypes.POINTER(ctypes.c_size_t)
 
 _SIGS = {
@@ -81,6 +88,13 @@ _SIGS = {
     "moe_expert_gemm_nvfp4": [_CFG, _I, _I, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P],
     "moe_expert_gemm_nvfp4_push": [_CFG, _I, _I, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P],
     "moe_scales_to_tiled": [_P, _I, _I, _P, _P],
+    "moe_add_rmsnorm": [_I, _I, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P, _P],
+    "moe_add_rmsnorm_backward_workspace": [_I, _I, _SZ],
+    "moe_add_rmsnorm_backward": [_I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P],
+    "moe_mla_workspace_size": [_MLA, _SZ],
+    "moe_mla_append": [_MLA, _I, _P, _I, _P, ctypes.c_float, _P, _I, _P, _P, _P, _P, _P, _P],
+    "moe_mla_decode": [_MLA, _P, ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P],
+    "moe_mla_status": [_MLA, _P, ctypes.POINTER(_I), ctypes.POINTER(_I), _I, _P],
     "moe_profile_enable": [_I],
     "moe_profile_read": [ctypes.c_void_p, _I, ctypes.POINTER(_I)],
     "moe_profile_trace": [ctypes.c_void_p, _I, ctypes.POINTER(_I)],
@@ -113,6 +127,8 @@ def _p(x):
 
 MOE_FLAG_LAP_LAUNCHES = 1   # one mover launch + one GEMM launch per ring lap instead of one launch for all laps
 MOE_FLAG_WGRAD_PAIR = 2     # weight gradients on CTA pairs (256-row tiles) instead of single-CTA 128 x 256 tiles
+MOE_FLAG_X_QUANTIZED = 4    # moe_forward / moe_dispatch take MX(x) from the workspace instead of quantising x
+MOE_NORM_MAX_D = 16384
 
 
 def config(T, d, E, k, n_groups=1, topk_groups=1, I=128, n_shared=0, capacity=0, flags=0,
@@ -224,6 +240,53 @@ def moe_gemm_nvfp4(M, N, K, a, a_sf, b, b_sf, alpha, c, stream=0):
 
 def moe_scales_to_tiled(canon, rows, K, tiled, stream=0):
     _check("moe_scales_to_tiled", _lib.moe_scales_to_tiled(_p(canon), rows, K, _p(tiled), _p(stream)))
+
+
+def moe_add_rmsnorm(T, d, x, residual, gamma, eps, h, y, rstd=0, codes=0, scales=0, scales_tiled=0, stream=0):
+    _check("moe_add_rmsnorm",
+           _lib.moe_add_rmsnorm(T, d, _p(x), _p(residual), _p(gamma), float(eps), _p(h), _p(y), _p(rstd), _p(codes),
+                                _p(scales), _p(scales_tiled), _p(stream)))
+
+
+def moe_add_rmsnorm_backward_workspace(T, d) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_add_rmsnorm_backward_workspace", _lib.moe_add_rmsnorm_backward_workspace(T, d, ctypes.byref(n)))
+    return n.value
+
+
+def moe_add_rmsnorm_backward(T, d, dy, dres, h, gamma, rstd, dx, dgamma, ws, stream=0):
+    _check("moe_add_rmsnorm_backward",
+           _lib.moe_add_rmsnorm_backward(T, d, _p(dy), _p(dres), _p(h), _p(gamma), _p(rstd), _p(dx), _p(dgamma), _p(ws),
+                                         _p(stream)))
+
+
+def mla_config(batch, heads, latent=512, rope=64, page_size=64, num_pages=1, max_pages=1, softmax_scale=1.0) -> MlaConfig:
+    return MlaConfig(batch, heads, latent, rope, page_size, num_pages, max_pages, softmax_scale)
+
+
+def moe_mla_workspace_size(cfg: MlaConfig) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_mla_workspace_size", _lib.moe_mla_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def moe_mla_append(cfg, n, kv, ld_kv, gamma, eps, cos_sin, max_pos, seq, pos, block_table, cache, ws, stream=0):
+    _check("moe_mla_append",
+           _lib.moe_mla_append(ctypes.byref(cfg), n, _p(kv), ld_kv, _p(gamma), float(eps), _p(cos_sin), max_pos, _p(seq),
+                               _p(pos), _p(block_table), _p(cache), _p(ws), _p(stream)))
+
+
+def moe_mla_decode(cfg, q, q_stride_b, q_stride_h, cache, block_table, seq_lens, out, lse, ws, stream=0):
+    _check("moe_mla_decode",
+           _lib.moe_mla_decode(ctypes.byref(cfg), _p(q), q_stride_b, q_stride_h, _p(cache), _p(block_table), _p(seq_lens),
+                               _p(out), _p(lse), _p(ws), _p(stream)))
+
+
+def moe_mla_status(cfg, ws, clear=True, stream=0):
+    code, site = ctypes.c_int(), ctypes.c_int()
+    _check("moe_mla_status", _lib.moe_mla_status(ctypes.byref(cfg), _p(ws), ctypes.byref(code), ctypes.byref(site),
+                                                 1 if clear else 0, _p(stream)))
+    return code.value, site.value
 
 
 def moe_profile_enable(enable=True):

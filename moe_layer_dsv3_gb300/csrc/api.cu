@@ -51,6 +51,16 @@ bool arch_ok() {
   return v == 1;
 }
 
+int read_status(void* status, int* code, int* site, int clear, cudaStream_t s) {
+  int h[2] = {0, 0};
+  if (cudaMemcpyAsync(h, status, sizeof(h), cudaMemcpyDeviceToHost, s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return MOE_ERR_CUDA;
+  *code = h[0];
+  *site = h[1];
+  if (clear && cudaMemsetAsync(status, 0, 16, s) != cudaSuccess) return MOE_ERR_CUDA;
+  return MOE_OK;
+}
+
 namespace {
 
 inline cudaStream_t S(moe_stream_t s) { return static_cast<cudaStream_t>(s); }
@@ -101,6 +111,18 @@ inline bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) 
 template <typename... P>
 inline bool all_al16(const P*... p) { return (al16(p) && ...); }
 
+// MX(x) along d into the workspace, rows past T zero.
+void quantize_x(const Layout& L, const void* x, void* ws, cudaStream_t s) {
+  const Dims& m = L.m;
+  uint8_t* xq = ws_ptr<uint8_t>(L, ws, MOE_WS_XQ);
+  uint8_t* xq_sf = ws_ptr<uint8_t>(L, ws, MOE_WS_XQ_SF);
+  if (m.Tpad > m.T) {
+    note(cudaMemsetAsync(xq + m.T * m.d, 0, (m.Tpad - m.T) * m.d, s));
+    note(cudaMemsetAsync(xq_sf + (m.T / 128) * 128 * (m.d / 32), 0, (m.Tpad - m.T / 128 * 128) * (m.d / 32), s));
+  }
+  launch_quant_rows(x, m.T, m.d, m.d, xq, xq_sf, true, 0, s, ws_ptr<uint8_t>(L, ws, MOE_WS_XQ_SFC));
+}
+
 // Counters of an all-laps ring launch, zeroed on the stream before it.
 RingMovers ring_movers(const Layout& L, void* ws, cudaStream_t s) {
   RingMovers mv{};
@@ -127,7 +149,7 @@ int validate(const moe_config_t* c) {
   if (c->n_groups > 1 && (c->E / c->n_groups < 2 || c->k > c->topk_groups * (c->E / c->n_groups)))
     return MOE_ERR_INVALID_ARG;
   if (c->capacity < 0 || c->capacity % 128) return MOE_ERR_INVALID_ARG;
-  if (c->flags & ~(MOE_FLAG_LAP_LAUNCHES | MOE_FLAG_WGRAD_PAIR)) return MOE_ERR_INVALID_ARG;
+  if (c->flags & ~(MOE_FLAG_LAP_LAUNCHES | MOE_FLAG_WGRAD_PAIR | MOE_FLAG_X_QUANTIZED)) return MOE_ERR_INVALID_ARG;
   if (c->n_mover_warps != 0 && c->n_mover_warps != 1 && c->n_mover_warps != 2 && c->n_mover_warps != 4)
     return MOE_ERR_INVALID_ARG;
   const int64_t Ap = static_cast<int64_t>(c->T) * (c->k + c->n_shared);
@@ -373,13 +395,7 @@ int moe_dispatch(const moe_config_t* cfg, const void* x, void* ws, moe_stream_t 
   const Dims& m = L.m;
   if (m.T == 0) return MOE_OK;
   cudaStream_t s = S(stream);
-  uint8_t* xq = ws_ptr<uint8_t>(L, ws, MOE_WS_XQ);
-  uint8_t* xq_sf = ws_ptr<uint8_t>(L, ws, MOE_WS_XQ_SF);
-  if (m.Tpad > m.T) {
-    note(cudaMemsetAsync(xq + m.T * m.d, 0, (m.Tpad - m.T) * m.d, s));
-    note(cudaMemsetAsync(xq_sf + (m.T / 128) * 128 * (m.d / 32), 0, (m.Tpad - m.T / 128 * 128) * (m.d / 32), s));
-  }
-  launch_quant_rows(x, m.T, m.d, m.d, xq, xq_sf, true, 0, s, ws_ptr<uint8_t>(L, ws, MOE_WS_XQ_SFC));
+  if (!(cfg->flags & MOE_FLAG_X_QUANTIZED)) quantize_x(L, x, ws, s);
   launch_dispatch_all(m, L, ws, s);
   return call.status();
 }
@@ -399,11 +415,7 @@ int moe_forward(const moe_config_t* cfg, const void* x, const void* wq, const fl
   void* wqm = const_cast<void*>(wq);
   uint8_t* xq = ws_ptr<uint8_t>(L, ws, MOE_WS_XQ);
   uint8_t* xq_sf = ws_ptr<uint8_t>(L, ws, MOE_WS_XQ_SF);
-  if (m.Tpad > m.T) {
-    note(cudaMemsetAsync(xq + m.T * m.d, 0, (m.Tpad - m.T) * m.d, s));
-    note(cudaMemsetAsync(xq_sf + (m.T / 128) * 128 * (m.d / 32), 0, (m.Tpad - m.T / 128 * 128) * (m.d / 32), s));
-  }
-  launch_quant_rows(x, m.T, m.d, m.d, xq, xq_sf, true, 0, s, ws_ptr<uint8_t>(L, ws, MOE_WS_XQ_SFC));
+  if (!(cfg->flags & MOE_FLAG_X_QUANTIZED)) quantize_x(L, x, ws, s);
   int* counts = ws_ptr<int>(L, ws, MOE_WS_COUNTS);
   int* poff = ws_ptr<int>(L, ws, MOE_WS_POFF);
   int* lap_tiles = ws_ptr<int>(L, ws, MOE_WS_LAPTILES);
@@ -663,14 +675,7 @@ int moe_status(const moe_config_t* cfg, void* ws, int* code, int* site, int clea
   if (int r = validate(cfg)) return r;
   if (!ws || !code || !site) return MOE_ERR_INVALID_ARG;
   const Layout L = make_layout(cfg);
-  int h[2] = {0, 0};
-  int* st = ws_ptr<int>(L, ws, MOE_WS_STATUS);
-  if (cudaMemcpyAsync(h, st, sizeof(h), cudaMemcpyDeviceToHost, S(stream)) != cudaSuccess) return MOE_ERR_CUDA;
-  if (cudaStreamSynchronize(S(stream)) != cudaSuccess) return MOE_ERR_CUDA;
-  *code = h[0];
-  *site = h[1];
-  if (clear && cudaMemsetAsync(st, 0, 16, S(stream)) != cudaSuccess) return MOE_ERR_CUDA;
-  return MOE_OK;
+  return read_status(ws_ptr<int>(L, ws, MOE_WS_STATUS), code, site, clear, S(stream));
 }
 
 }  // extern "C"

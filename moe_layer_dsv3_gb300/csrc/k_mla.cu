@@ -1,0 +1,1028 @@
+// Latent attention over a paged cache: the write of new tokens and the
+// attention of one new token a sequence (absorbed form).
+//
+// The cache holds one row a token, [latent | rope], shared by all heads: keys
+// are whole rows, values their first `latent` columns.
+//
+//   s_j = scale q . k_j   (j < len),   out = sum_j softmax(s)_j k_j[0 : latent]
+//
+// One cached token costs 2 (latent + rope) bytes of HBM and, with H heads,
+// 2 H (2 latent + rope) products: at 512 + 64 columns and 128 heads that is
+// 242 flop/byte, where HBM and the tensor pipe are both close to their
+// limits; with fewer heads HBM alone bounds the kernel. So the cache is read
+// once per group of up to 64 heads, straight into the shared memory that both
+// products read.
+//
+// Both products run transposed, with cached tokens (then latent columns) as
+// the 128- or 64-row operand and the heads as the narrow one: a few heads then
+// cost little, and the output of 64 heads takes half of TMEM.
+//   S^T [64 tokens x N heads]   = K [64 x (latent + rope)] . Q [N x (latent + rope)]^T
+//   O^T [latent x N heads]     += V^T [latent x 64] . P [N x 64]^T,  V^T read from the
+//                                 same K tile as an MN-major operand
+// N = the group's heads, rounded up to 16.
+//
+// Work is split by tiles of 64 tokens: the tiles of all sequences, one after
+// another, are cut into equal contiguous ranges, one per worker (CTA; with two
+// head groups, one worker per group). A sequence inside one range is finished
+// there; one that is cut leaves a partial (unnormalised O, maximum, sum) per
+// piece in the workspace, and the join kernel adds the pieces in order. Every
+// worker finds its range from seq_lens on the device, so the host never reads
+// lengths and the call can be captured in a graph.
+#include <cudaTypedefs.h>
+
+#include "gemm.cuh"
+#include "prof.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kTile = 64;                 // cached tokens per tile
+constexpr int kMaxHeadsCta = 64;          // heads per CTA
+constexpr int kLatSlot = kTile * 256;     // 128 latent columns of a tile: two boxes of [64 tokens][128 bytes]
+constexpr int kRopeSlot = kTile * 128;    // the rope columns (64, zero-filled past `rope`)
+constexpr int kMaxLatSlots = 12;
+constexpr int kMaxRopeSlots = 3;
+constexpr int kBarBytes = 512;
+constexpr int kSmemMax = 232448;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// A tile's scores may exceed the running reference by this many powers of two
+// before O is rescaled: P and the sums stay far inside fp32 and bf16 range, and
+// their relative precision does not depend on the reference.
+constexpr float kSlack = 10.0f;
+
+struct MlaArgs {
+  int B, H, latent, rope, page, num_pages, max_pages;
+  int G, hg;                 // head groups, heads per group
+  int nm;                    // latent / 128
+  int nlat, nrope;           // ring slots
+  int W;                     // workers per head group
+  int piece;                 // tokens per TMA box: a power of two that divides the page
+  float scale2;              // scale * log2(e)
+  const int32_t* table;
+  const int32_t* lens;
+  __nv_bfloat16* out;
+  float* lse;                // or null
+  int* status;
+  int4* join;                // [W]: per worker that ends a cut sequence {b, first slot, first worker, pieces}
+  float* part_o;             // [2 W G][64][latent]
+  float* part_m;             // [2 W G][64] reference (log2 units)
+  float* part_l;             // [2 W G][64] sum of P as rounded for the product
+  float* part_e;             // [2 W G][64] sum of P in fp32 (for the lse)
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Valid cached tokens of sequence b: lengths outside [0, capacity] are clamped (and reported once).
+__device__ __forceinline__ int seq_len(const MlaArgs& a, int b, bool report) {
+  const int n = __ldg(a.lens + b);
+  const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page;
+  if (n < 0 || n > cap) {
+    if (report) report_error(a.status, kErrBounds, 60);
+    return n < 0 ? 0 : static_cast<int>(cap);
+  }
+  return n;
+}
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+
+// Range of tiles of worker w of W over `total` tiles, and the worker that owns tile t.
+__device__ __forceinline__ int range_begin(int total, int w, int W) {
+  return static_cast<int>(static_cast<int64_t>(total) * w / W);
+}
+__device__ __forceinline__ int owner_of(int total, int t, int W) {
+  return static_cast<int>((static_cast<int64_t>(t + 1) * W - 1) / total);
+}
+
+// Work of one worker: contiguous pieces of sequences, walked the same way by every role.
+struct Walk {
+  int b, t, left;            // next sequence, its next tile, tiles left in the range
+  int len, nt;               // current piece's sequence: tokens, tiles
+  int t0, n;                 // current piece: first tile, tiles
+  bool first;                // the worker's first piece
+  __device__ __forceinline__ bool next(const MlaArgs& a, bool& started) {
+    if (left <= 0) return false;
+    while (true) {
+      if (b >= a.B) return false;
+      len = seq_len(a, b, false);
+      nt = tiles_of(len);
+      if (t < nt) break;
+      ++b;
+      t = 0;
+    }
+    first = !started;
+    started = true;
+    t0 = t;
+    n = left < nt - t ? left : nt - t;
+    left -= n;
+    return true;
+  }
+  __device__ __forceinline__ void done() { ++b; t = 0; }
+};
+
+// TMEM loads. 16 lanes x 8 fp32 columns per step: register 4 i + {0, 1} is
+// (lane / 4, 8 i + 2 (lane % 4) + {0, 1}), register 4 i + {2, 3} the row 8 below.
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Store four transposed 8 x 8 blocks of 16-bit values: lane l gives the address
+// of row l % 8 of block l / 8.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1),
+               "r"(r2), "r"(r3)
+               : "memory");
+}
+
+// 3-D tiled load (q: columns, heads, sequences).
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Barrier over the 128 softmax threads that also gives the OR of their flags.
+__device__ __forceinline__ bool barrier_or(int id, bool flag) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(flag)), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// Ring position: slot index and the parity of its current use.
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step(int n) {
+    if (++slot == n) { slot = 0; phase ^= 1u; }
+  }
+};
+
+struct Smem {
+  uint64_t latf[kMaxLatSlots], late[kMaxLatSlots];     // latent slots: filled / free
+  uint64_t ropef[kMaxRopeSlots], ropee[kMaxRopeSlots];
+  uint64_t qf, qe;                                      // Q of the piece: filled / free
+  uint64_t sf[2], se[2];                                // S^T buffers: products done / read
+  uint64_t pf, pe;                                      // P: written / its product done
+  uint64_t of, oe;                                      // O: all products of the piece done / read
+  uint32_t tmem;
+  int scan[6];
+  int start_b, start_t;
+};
+static_assert(sizeof(Smem) <= kBarBytes, "control block");
+
+}  // namespace
+
+// Threads: warp 0 loads (TMA), warp 1 issues the MMAs, warps 2-5 do the softmax
+// and the epilogue (TMEM lane quarter warp % 4).
+template <int N>
+__global__ void __launch_bounds__(192, 1)
+    mla_decode_kernel(const __grid_constant__ CUtensorMap tma_k, const __grid_constant__ CUtensorMap tma_q,
+                      const __grid_constant__ MlaArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int nm = a.nm, nchunk = 2 * nm + 1;            // 64-column chunks of a row: latent, then rope
+  uint8_t* lat = smem;
+  uint8_t* ropes = lat + a.nlat * kLatSlot;
+  uint8_t* sq = ropes + a.nrope * kRopeSlot;           // [nchunk][N][128 bytes]
+  uint8_t* sp = sq + nchunk * N * 128;                 // [N][128 bytes]: P, 64 tokens a head
+  Smem& c = *reinterpret_cast<Smem*>(sp + N * 128);
+  float* smax = reinterpret_cast<float*>(sp + N * 128 + kBarBytes);   // [4][64]
+  float* fac = smax + 4 * kMaxHeadsCta;                               // [64]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = blockIdx.x % a.G, w = blockIdx.x / a.G;
+  constexpr int kSCol = 4 * N;                         // S^T buffers above O^T (latent / 128 <= 4 tiles of N columns)
+
+  if (tid == 0) {
+    for (int i = 0; i < a.nlat; ++i) {
+      mbar_init(&c.latf[i], 1);
+      mbar_init(&c.late[i], 1);
+    }
+    for (int i = 0; i < a.nrope; ++i) {
+      mbar_init(&c.ropef[i], 1);
+      mbar_init(&c.ropee[i], 1);
+    }
+    mbar_init(&c.qf, 1);
+    mbar_init(&c.qe, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.sf[i], 1);
+      mbar_init(&c.se[i], 128);
+    }
+    mbar_init(&c.pf, 128);
+    mbar_init(&c.pe, 1);
+    mbar_init(&c.of, 1);
+    mbar_init(&c.oe, 128);
+    fence_barrier_init();
+    fence_proxy_async();
+    tma_prefetch(&tma_k);
+    tma_prefetch(&tma_q);
+  }
+  if (warp == 1) {
+    tmem_alloc(&c.tmem, 512);
+    tmem_relinquish();
+  }
+  // Range of this worker: prefix sums of the sequences' tiles, a run of
+  // sequences per thread, then the thread whose run holds the first tile finds it.
+  const int per = (a.B + 191) / 192;
+  const int b0 = tid * per < a.B ? tid * per : a.B;
+  const int b1 = b0 + per < a.B ? b0 + per : a.B;
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += tiles_of(seq_len(a, b, blockIdx.x == 0));
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) c.scan[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    if (i < warp) before += c.scan[i];
+    total += c.scan[i];
+  }
+  const int W = a.W < total ? a.W : (total > 0 ? total : 1);   // workers that get tiles
+  const int f0 = w < W ? range_begin(total, w, W) : total;
+  const int f1 = w < W ? range_begin(total, w + 1, W) : total;
+  {
+    int at = before + incl - mine;
+    if (f0 >= at && f0 < at + mine)
+      for (int b = b0; b < b1; ++b) {
+        const int n = tiles_of(seq_len(a, b, false));
+        if (f0 < at + n) {
+          c.start_b = b;
+          c.start_t = f0 - at;
+          break;
+        }
+        at += n;
+      }
+  }
+  __syncthreads();
+  const uint32_t tmem = c.tmem;
+  Walk wk;
+  wk.b = c.start_b;
+  wk.t = c.start_t;
+  wk.left = f1 - f0;
+  bool started = false, ok = true;
+
+  if (warp == 0) {
+    Ring lr, rr;
+    uint32_t qphase = 0;
+    int issued_lat = 0, issued_rope = 0, issued_q = 0;
+    const int pieces = kTile / a.piece;
+    const int64_t oob = static_cast<int64_t>(a.num_pages) * a.page;   // a row past the cache: reads zeros
+    const int h0 = g * a.hg;
+    while (ok && wk.next(a, started)) {
+      // Q of this sequence and head group, once the previous piece's products have read the last one.
+      if (lane == 0) {
+        ok = mbar_wait(&c.qe, qphase ^ 1u, a.status, 61);
+        if (ok) {
+          mbar_arrive_expect_tx(&c.qf, nchunk * N * 128);
+          for (int k = 0; k < nchunk; ++k) tma_load_3d(sq + k * N * 128, &tma_q, k * 64, h0, wk.b, &c.qf);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      qphase ^= 1u;
+      ++issued_q;
+      // Row of this lane's piece of tile t: the page is read one tile ahead of its loads.
+      const int32_t* table = a.table + static_cast<int64_t>(wk.b) * a.max_pages;
+      auto page_of = [&](int t) {
+        const int tok = t * kTile + lane * a.piece;
+        return (lane < pieces && t < wk.nt && tok < wk.len) ? __ldg(table + tok / a.page) : -1;
+      };
+      int page = page_of(wk.t0);
+      for (int t = wk.t0; t < wk.t0 + wk.n && ok; ++t) {
+        const int tok = t * kTile + lane * a.piece;
+        const bool live = lane < pieces && tok < wk.len;
+        const int live_pieces = __popc(__ballot_sync(0xffffffffu, live));
+        int row = 0;
+        if (live) {
+          if (page < 0 || page >= a.num_pages) {
+            report_error(a.status, kErrBounds, 62);
+            row = static_cast<int>(oob);
+          } else {
+            row = page * a.page + tok % a.page;
+          }
+        }
+        page = page_of(t + 1);
+        for (int s = -1; s < nm && ok; ++s) {            // rope chunk first, then 128 latent columns a slot
+          const bool rope = s < 0;
+          Ring& r = rope ? rr : lr;
+          uint64_t* full = rope ? &c.ropef[r.slot] : &c.latf[r.slot];
+          uint64_t* empty = rope ? &c.ropee[r.slot] : &c.late[r.slot];
+          uint8_t* dst = rope ? ropes + r.slot * kRopeSlot : lat + r.slot * kLatSlot;
+          if (lane == 0) {
+            ok = mbar_wait(empty, r.phase ^ 1u, a.status, 63);
+            if (ok) mbar_arrive_expect_tx(full, live_pieces * a.piece * (rope ? 128 : 256));
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          if (live) {
+            tma_load_2d(dst + lane * a.piece * 128, &tma_k, rope ? a.latent : s * 128, row, full);
+            if (!rope) tma_load_2d(dst + kTile * 128 + lane * a.piece * 128, &tma_k, s * 128 + 64, row, full);
+          }
+          r.step(rope ? a.nrope : a.nlat);
+          if (rope) ++issued_rope; else ++issued_lat;
+        }
+      }
+      wk.done();
+    }
+    // Every copy this CTA started has landed before its shared memory is released.
+    if (lane == 0) {
+      for (int i = 0, n = issued_lat < a.nlat ? issued_lat : a.nlat; i < n; ++i) {
+        if (--lr.slot < 0) { lr.slot = a.nlat - 1; lr.phase ^= 1u; }
+        mbar_wait(&c.latf[lr.slot], lr.phase, a.status, 64);
+      }
+      for (int i = 0, n = issued_rope < a.nrope ? issued_rope : a.nrope; i < n; ++i) {
+        if (--rr.slot < 0) { rr.slot = a.nrope - 1; rr.phase ^= 1u; }
+        mbar_wait(&c.ropef[rr.slot], rr.phase, a.status, 64);
+      }
+      if (issued_q > 0) mbar_wait(&c.qf, qphase ^ 1u, a.status, 64);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16(64, N);
+      constexpr uint32_t idesc_o = idesc_bf16(128, N) | (1u << 15);   // A (V^T) is MN-major
+      Ring lr, rr, pvr;       // pvr: latent ring as the second product walks it
+      uint32_t qphase = 0, pphase = 0, ophase = 0;
+      int sbuf = 0;
+      uint32_t sphase = 0;
+      // One tile behind S^T: the pending O^T product of the previous tile.
+      bool pending = false, pend_first = false, pend_last = false;
+      auto pv = [&]() -> bool {
+        if (!mbar_wait(&c.pf, pphase, a.status, 70)) return false;
+        pphase ^= 1u;
+        if (pend_first) {     // the previous piece's O has been read
+          if (!mbar_wait(&c.oe, ophase ^ 1u, a.status, 71)) return false;
+          ophase ^= 1u;
+        }
+        tc_fence_after();
+        const uint32_t bp = smem_u32(sp);
+        for (int m = 0; m < nm; ++m) {
+          const uint32_t av = smem_u32(lat + pvr.slot * kLatSlot);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            tc_mma_bf16(tmem + m * N, smem_desc(av + kk * 2048, kTile * 128, 1024, 2), desc_kmajor_sw128(bp + kk * 32),
+                        idesc_o, !(pend_first && kk == 0));
+          tc_commit(&c.late[pvr.slot]);
+          pvr.step(a.nlat);
+        }
+        tc_commit(&c.pe);
+        if (pend_last) tc_commit(&c.of);
+        return true;
+      };
+      while (ok && wk.next(a, started)) {
+        ok = mbar_wait(&c.qf, qphase, a.status, 72);
+        qphase ^= 1u;
+        for (int i = 0; i < wk.n && ok; ++i) {
+          ok = mbar_wait(&c.se[sbuf], sphase ^ 1u, a.status, 73) && mbar_wait(&c.ropef[rr.slot], rr.phase, a.status, 74);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t d = tmem + kSCol + sbuf * N;
+          const uint32_t qb = smem_u32(sq);
+          const uint32_t ar = smem_u32(ropes + rr.slot * kRopeSlot);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_bf16(d, desc_kmajor_sw128(ar + kk * 32), desc_kmajor_sw128(qb + (nchunk - 1) * N * 128 + kk * 32),
+                        idesc_s, kk != 0);
+          tc_commit(&c.ropee[rr.slot]);
+          rr.step(a.nrope);
+          for (int m = 0; m < nm; ++m) {
+            if (!(ok = mbar_wait(&c.latf[lr.slot], lr.phase, a.status, 75))) break;
+            tc_fence_after();
+            const uint32_t al = smem_u32(lat + lr.slot * kLatSlot);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc_mma_bf16(d, desc_kmajor_sw128(al + (kk >> 2) * (kTile * 128) + (kk & 3) * 32),
+                          desc_kmajor_sw128(qb + (2 * m + (kk >> 2)) * N * 128 + (kk & 3) * 32), idesc_s, 1);
+            lr.step(a.nlat);
+          }
+          if (!ok) break;
+          tc_commit(&c.sf[sbuf]);
+          if (i == wk.n - 1) tc_commit(&c.qe);
+          sbuf ^= 1;
+          if (sbuf == 0) sphase ^= 1u;
+          if (pending) ok = pv();
+          pending = true;
+          pend_first = i == 0;
+          pend_last = i == wk.n - 1;
+        }
+        wk.done();
+      }
+      if (ok && pending) pv();
+    }
+  } else {
+    const int q = warp & 3;
+    const int st = tid - 64;                               // softmax thread
+    const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
+    constexpr int NP = N / 8;                              // 8-head column blocks
+    uint32_t pphase = 0, ophase = 0, sphase = 0;
+    int sbuf = 0;
+    Ring lr;                                               // latent ring position of the current tile
+    const int head0 = g * a.hg;                            // first head of the group
+    const int nh = a.H - head0 < a.hg ? a.H - head0 : a.hg;
+    bool any_tile = false;                                 // a product into O has been issued before this tile
+    // After a wait that gave up, these threads stop waiting but keep walking: all 128 then
+    // meet at every barrier, and the kernel ends.
+    auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+      if (ok) ok = mbar_wait(bar, parity, a.status, site);
+    };
+    while (wk.next(a, started)) {
+      // Heads 8 i + 2 (lane % 4) + e of this thread; rows q * 16 + lane / 4 and + 8 of a tile.
+      float mref[NP][2], l[NP][2], le[NP][2];
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mref[i][e] = -INFINITY;
+          l[i][e] = 0.0f;
+          le[i][e] = 0.0f;
+        }
+      for (int ti = 0; ti < wk.n; ++ti) {
+        const int valid = wk.len - (wk.t0 + ti) * kTile;   // tokens of the tile (>= 64: all)
+        wait(&c.sf[sbuf], sphase, 80);
+        tc_fence_after();
+        uint32_t r[4 * NP];
+#pragma unroll
+        for (int i = 0; i < NP; i += 2) tmem_ld_16x256b_x2(tmem + tlane + kSCol + sbuf * N + 8 * i, r + 4 * i);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4 * NP; ++i) reg_fence(r[i]);
+        tc_fence_before();
+        mbar_arrive(&c.se[sbuf]);
+        sbuf ^= 1;
+        if (sbuf == 0) sphase ^= 1u;
+        const int row = q * 16 + (lane >> 2);
+        float s[NP][4];
+        float over = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[i][e] = __uint_as_float(r[4 * i + e]) * a.scale2;
+            if (row + 8 * (e >> 1) >= valid) s[i][e] = -INFINITY;
+            over = fmaxf(over, s[i][e] - mref[i][e & 1]);   // +inf in a piece's first tile (or NaN: -inf - -inf)
+          }
+        // O is rescaled only when some score passes its head's reference by kSlack; always in the first tile.
+        const bool grow = barrier_or(2, ti == 0 || over > kSlack);
+        float corr[NP][2];
+        if (grow) {
+#pragma unroll
+          for (int i = 0; i < NP; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float m = fmaxf(s[i][e], s[i][e + 2]);
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+              if (lane < 4) smax[q * kMaxHeadsCta + 8 * i + 2 * lane + e] = m;
+            }
+          named_barrier(3, 128);
+#pragma unroll
+          for (int i = 0; i < NP; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int h = 8 * i + 2 * (lane & 3) + e;
+              float m = fmaxf(fmaxf(smax[h], smax[kMaxHeadsCta + h]),
+                              fmaxf(smax[2 * kMaxHeadsCta + h], smax[3 * kMaxHeadsCta + h]));
+              m = fmaxf(m, mref[i][e]);
+              corr[i][e] = mref[i][e] == -INFINITY ? 0.0f : ex2(mref[i][e] - m);
+              mref[i][e] = m;
+              l[i][e] *= corr[i][e];
+              le[i][e] *= corr[i][e];
+              if (q == 0 && lane < 4) fac[h] = corr[i][e];
+            }
+        }
+        uint32_t p[NP][2];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // a head that has seen only -inf keeps a zero reference, so its P is 0 and not NaN
+            const float m = mref[i][e & 1] == -INFINITY ? 0.0f : mref[i][e & 1];
+            x[e] = ex2(s[i][e] - m);
+            le[i][e & 1] += x[e];
+          }
+          p[i][0] = pack_bf16x2(x[0], x[1]);
+          p[i][1] = pack_bf16x2(x[2], x[3]);
+          // P enters the product rounded to bf16; the same rounded values are summed for its normalisation
+          l[i][0] += __uint_as_float(p[i][0] << 16) + __uint_as_float(p[i][1] << 16);
+          l[i][1] += __uint_as_float(p[i][0] & 0xFFFF0000u) + __uint_as_float(p[i][1] & 0xFFFF0000u);
+        }
+        // The previous tile's product is done: P is free and O stands still.
+        if (any_tile) {
+          wait(&c.pe, pphase, 81);
+          pphase ^= 1u;
+        }
+        any_tile = true;
+        if (grow) {
+          named_barrier(3, 128);                           // fac is written
+          if (ti > 0) {
+            tc_fence_after();
+            for (int m = 0; m < nm; ++m)
+#pragma unroll
+              for (int hc = 0; hc < N; hc += 16) {
+                uint32_t o[16];
+                const uint32_t at = tmem + tlane + m * N + hc;
+                tmem_ld_32x32b_x16(at, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  reg_fence(o[j]);
+                  o[j] = __float_as_uint(__uint_as_float(o[j]) * fac[hc + j]);
+                }
+                tmem_st_32x32b_x16(at, o);
+              }
+            tmem_wait_st();
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NP; i += 2) {
+          const int h = 8 * (i + (lane >> 4)) + (lane & 7);
+          const int ch = 2 * q + ((lane >> 3) & 1);
+          stmatrix_x4_trans(smem_u32(sp) + h * 128 + ((ch ^ (h & 7)) << 4), p[i][0], p[i][1], p[i + 1][0], p[i + 1][1]);
+        }
+        if (valid < kTile) {
+          // Rows past the sequence's end hold whatever the page held (NaN included): their P is 0, and they
+          // have to be 0 themselves for the product. Only a sequence's last tile is partial.
+          Ring z = lr;
+          for (int m = 0; m < nm; ++m) {
+            wait(&c.latf[z.slot], z.phase, 82);
+            uint4* v = reinterpret_cast<uint4*>(lat + z.slot * kLatSlot);
+            for (int i = st; i < 2 * (kTile - valid) * 8; i += 128) {
+              const int half = i / ((kTile - valid) * 8), k = i - half * ((kTile - valid) * 8);
+              v[half * kTile * 8 + valid * 8 + k] = make_uint4(0, 0, 0, 0);
+            }
+            z.step(a.nlat);
+          }
+        }
+        for (int m = 0; m < nm; ++m) lr.step(a.nlat);
+        fence_proxy_async();
+        tc_fence_before();
+        mbar_arrive(&c.pf);
+      }
+      // ---- epilogue of the piece
+      // Sums over the tile rows: lanes with the same lane % 4, then the four warps.
+      float tot[2][NP][2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        named_barrier(3, 128);                             // smax is free
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = k ? le[i][e] : l[i][e];
+            v += __shfl_xor_sync(0xffffffffu, v, 4);
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            v += __shfl_xor_sync(0xffffffffu, v, 16);
+            if (lane < 4) smax[q * kMaxHeadsCta + 8 * i + 2 * lane + e] = v;
+          }
+        named_barrier(3, 128);
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int h = 8 * i + 2 * (lane & 3) + e;
+            tot[k][i][e] = (smax[h] + smax[kMaxHeadsCta + h]) + (smax[2 * kMaxHeadsCta + h] + smax[3 * kMaxHeadsCta + h]);
+          }
+      }
+      const bool whole = wk.n == wk.nt;
+      const int slot = 2 * static_cast<int>(blockIdx.x) + (wk.first ? 0 : 1);
+      if (q == 0 && lane < 4) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int h = 8 * i + 2 * lane + e;
+            if (whole) {
+              fac[h] = tot[0][i][e] == 0.0f ? 0.0f : 1.0f / tot[0][i][e];
+              if (a.lse != nullptr && h < nh)
+                a.lse[static_cast<int64_t>(wk.b) * a.H + head0 + h] =
+                    tot[1][i][e] == 0.0f ? -INFINITY : (mref[i][e] + log2f(tot[1][i][e])) * kLn2;
+            } else {
+              a.part_m[slot * kMaxHeadsCta + h] = mref[i][e];
+              a.part_l[slot * kMaxHeadsCta + h] = tot[0][i][e];
+              a.part_e[slot * kMaxHeadsCta + h] = tot[1][i][e];
+            }
+          }
+      }
+      named_barrier(3, 128);
+      wait(&c.of, ophase, 83);
+      ophase ^= 1u;
+      tc_fence_after();
+      if (whole) {
+        __nv_bfloat16* out = a.out + (static_cast<int64_t>(wk.b) * a.H + head0) * a.latent;
+        for (int m = 0; m < nm; ++m) {
+          const int dv = m * 128 + q * 32 + lane;
+#pragma unroll
+          for (int hc = 0; hc < N; hc += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(tmem + tlane + m * N + hc, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              reg_fence(o[j]);
+              reg_fence(o[j + 1]);
+              const float v0 = __uint_as_float(o[j]) * fac[hc + j], v1 = __uint_as_float(o[j + 1]) * fac[hc + j + 1];
+              // neighbouring lanes swap, so that each stores two columns of one head
+              const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v0 : v1, 1);
+              const int h = hc + j + (lane & 1);
+              const uint32_t pk = (lane & 1) ? pack_bf16x2(got, v1) : pack_bf16x2(v0, got);
+              if (h < nh) *reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(h) * a.latent + (dv & ~1)) = pk;
+            }
+          }
+        }
+      } else {
+        float* out = a.part_o + static_cast<int64_t>(slot) * kMaxHeadsCta * a.latent;
+        for (int m = 0; m < nm; ++m) {
+          const int dv = m * 128 + q * 32 + lane;
+#pragma unroll
+          for (int hc = 0; hc < N; hc += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(tmem + tlane + m * N + hc, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              reg_fence(o[j]);
+              if (hc + j < nh) out[(hc + j) * a.latent + dv] = __uint_as_float(o[j]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&c.oe);
+      wk.done();
+    }
+    // The worker that ends a cut sequence names its pieces for the join.
+    if (st == 0 && g == 0) {
+      int4 j = make_int4(0, 0, 0, 0);
+      if (f1 > f0) {
+        // The first piece of the range is the only one that can end a sequence begun by another worker.
+        const int n0 = tiles_of(seq_len(a, c.start_b, false));
+        const int s0 = f0 - c.start_t;                     // the sequence's first tile in the common count
+        if (c.start_t > 0 && s0 + n0 <= f1) {
+          const int w0 = owner_of(total, s0, W);
+          // it opened w0's range, or came after another piece there
+          j = make_int4(c.start_b, range_begin(total, w0, W) == s0 ? 0 : 1, w0, w - w0 + 1);
+        }
+      }
+      a.join[w] = j;
+    }
+    // Sequences without tokens: zero rows, lse = -inf.
+    for (int b = w; b < a.B; b += a.W) {
+      if (seq_len(a, b, false) > 0) continue;
+      __nv_bfloat16* out = a.out + (static_cast<int64_t>(b) * a.H + head0) * a.latent;
+      for (int i = st; i < nh * a.latent / 8; i += 128) reinterpret_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse != nullptr)
+        for (int i = st; i < nh; i += 128) a.lse[static_cast<int64_t>(b) * a.H + head0 + i] = -INFINITY;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of the sequences that the work split cut: block (w, head),
+// for the sequence that worker w ended. Pieces are added in order. Latent /4
+// threads, four columns each.
+__global__ void mla_join_kernel(const __grid_constant__ MlaArgs a) {
+  const int4 j = a.join[blockIdx.x];
+  if (j.w == 0) return;
+  const int head = blockIdx.y, g = head / a.hg, h = head - g * a.hg;
+  auto slot_of = [&](int i) { return 2 * ((j.z + i) * a.G + g) + (i == 0 ? j.y : 0); };
+  float m = -INFINITY;
+  for (int i = 0; i < j.w; ++i) m = fmaxf(m, a.part_m[slot_of(i) * kMaxHeadsCta + h]);
+  const float mr = m == -INFINITY ? 0.0f : m;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float l = 0.0f, le = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < j.w; ++i) {
+    const int at = slot_of(i) * kMaxHeadsCta + h;
+    const float f = ex2(a.part_m[at] - mr);
+    const float4 v = reinterpret_cast<const float4*>(a.part_o + static_cast<int64_t>(at) * a.latent)[threadIdx.x];
+    l = fmaf(f, a.part_l[at], l);
+    le = fmaf(f, a.part_e[at], le);
+    o.x = fmaf(f, v.x, o.x);
+    o.y = fmaf(f, v.y, o.y);
+    o.z = fmaf(f, v.z, o.z);
+    o.w = fmaf(f, v.w, o.w);
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int64_t row = static_cast<int64_t>(j.x) * a.H + head;
+  *reinterpret_cast<uint2*>(a.out + row * a.latent + threadIdx.x * 4) =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (a.lse != nullptr && threadIdx.x == 0) a.lse[row] = le == 0.0f ? -INFINITY : (mr + log2f(le)) * kLn2;
+}
+
+// New tokens into the cache: one warp a token. The latent part is normalised
+// (gamma given) in fp32 and rounded once; neighbouring rope columns (2 i, 2 i + 1)
+// are rotated by the position's angle i (cos_sin given).
+struct AppendArgs {
+  int n, B, latent, rope, page, num_pages, max_pages, ld, max_pos;
+  const __nv_bfloat16* kv;
+  const __nv_bfloat16* gamma;    // or null
+  float eps;
+  const float* cos_sin;          // [max_pos][rope]: cos, then sin; or null
+  const int32_t* seq;
+  const int32_t* pos;
+  const int32_t* table;
+  __nv_bfloat16* cache;
+  int* status;
+};
+
+__global__ void __launch_bounds__(256) mla_append_kernel(const __grid_constant__ AppendArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (i >= a.n) return;
+  const __nv_bfloat16* src = a.kv + i * a.ld;
+  const int nlat = a.latent >> 3, nrope = a.rope >> 3;
+  // the row's loads do not wait for its place
+  uint4 c[2], u = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    c[k] = lane + 32 * k < nlat ? ld_global_u4(src + (lane + 32 * k) * 8) : make_uint4(0, 0, 0, 0);
+  if (lane < nrope) u = ld_global_u4(src + a.latent + lane * 8);
+  const int p = a.pos[i], b = a.seq[i];
+  if (p < 0) return;                                       // padding
+  if (b < 0 || b >= a.B || p >= static_cast<int64_t>(a.max_pages) * a.page ||
+      (a.cos_sin != nullptr && p >= a.max_pos)) {
+    if (lane == 0) report_error(a.status, kErrBounds, 65);
+    return;
+  }
+  const int page = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + p / a.page);
+  if (page < 0 || page >= a.num_pages) {
+    if (lane == 0) report_error(a.status, kErrBounds, 66);
+    return;
+  }
+  __nv_bfloat16* dst = a.cache + (static_cast<int64_t>(page) * a.page + p % a.page) * (a.latent + a.rope);
+  if (a.gamma != nullptr) {
+    float v[2][8], ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      unpack_bf16x8(c[k], v[k]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(v[k][e], v[k][e], ss);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float rstd = rsqrtf(ss / static_cast<float>(a.latent) + a.eps);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (lane + 32 * k < nlat) {
+        float g[8];
+        unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(a.gamma) + lane + 32 * k), g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = v[k][e] * rstd * g[e];
+        c[k] = pack_bf16x8(g);
+      }
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (lane + 32 * k < nlat) reinterpret_cast<uint4*>(dst)[lane + 32 * k] = c[k];
+  if (lane < nrope) {
+    if (a.cos_sin != nullptr) {
+      const float* cs = a.cos_sin + static_cast<int64_t>(p) * a.rope + lane * 4;
+      const float4 co = __ldg(reinterpret_cast<const float4*>(cs));
+      const float4 si = __ldg(reinterpret_cast<const float4*>(cs + a.rope / 2));
+      const float cc[4] = {co.x, co.y, co.z, co.w}, sn[4] = {si.x, si.y, si.z, si.w};
+      float v[8];
+      unpack_bf16x8(u, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = v[2 * e], y = v[2 * e + 1];
+        v[2 * e] = x * cc[e] - y * sn[e];
+        v[2 * e + 1] = x * sn[e] + y * cc[e];
+      }
+      u = pack_bf16x8(v);
+    }
+    reinterpret_cast<uint4*>(dst + a.latent)[lane] = u;
+  }
+}
+
+namespace {
+
+// Cache as [rows][latent + rope], box 64 columns x `piece` rows, 128-byte swizzle.
+bool make_tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int cols, int piece) {
+  return make_tmap_strided(m, base, {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), 1},
+                           {static_cast<uint64_t>(cols) * 2, 0}, {64, static_cast<uint32_t>(piece), 1}, 2);
+}
+
+int validate_mla(const moe_mla_config_t* c) {
+  if (c == nullptr) return MOE_ERR_INVALID_ARG;
+  if (c->batch < 0 || c->heads < 1 || c->heads > 128) return MOE_ERR_INVALID_ARG;
+  if (c->latent < 128 || c->latent > 512 || c->latent % 128) return MOE_ERR_INVALID_ARG;
+  if (c->rope < 8 || c->rope > 64 || c->rope % 8) return MOE_ERR_INVALID_ARG;
+  if (c->page_size < 8 || c->page_size % 8 || c->num_pages < 1 || c->max_pages < 1) return MOE_ERR_INVALID_ARG;
+  if (!(c->softmax_scale > 0.0f) || c->softmax_scale > 3.0e38f) return MOE_ERR_INVALID_ARG;
+  const int64_t lim = (1LL << 31) - 1;
+  const int64_t cap = static_cast<int64_t>(c->max_pages) * c->page_size;
+  // row coordinates and token positions are 32-bit, and so is the count of tiles of all sequences
+  if (static_cast<int64_t>(c->num_pages) * c->page_size >= lim || cap >= lim) return MOE_ERR_INVALID_ARG;
+  if (c->batch > 0 && ceil_div(cap, kTile) > lim / c->batch) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+struct MlaLayout {
+  size_t status, join, m, l, e, o, total;
+};
+MlaLayout mla_layout(const moe_mla_config_t* c) {
+  MlaLayout L{};
+  const size_t slots = 2 * static_cast<size_t>(kMaxSms);
+  size_t cur = 0;
+  auto add = [&](size_t n) {
+    const size_t at = cur;
+    cur += (n + 255) / 256 * 256;
+    return at;
+  };
+  L.status = add(16);
+  L.join = add(sizeof(int4) * kMaxSms);
+  L.m = add(sizeof(float) * slots * kMaxHeadsCta);
+  L.l = add(sizeof(float) * slots * kMaxHeadsCta);
+  L.e = add(sizeof(float) * slots * kMaxHeadsCta);
+  L.o = add(sizeof(float) * slots * kMaxHeadsCta * c->latent);
+  L.total = cur;
+  return L;
+}
+
+template <int N>
+int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tq, int sms, cudaStream_t s) {
+  static DevOnce once;
+  if (!once.ready([] {
+        return cudaFuncSetAttribute(mla_decode_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+      }))
+    return MOE_ERR_CUDA;
+  const int fixed = 1024 + kBarBytes + (4 + 1) * kMaxHeadsCta * 4 + (2 * a.nm + 1) * N * 128 + N * 128;
+  a.nrope = N <= 32 ? 3 : 2;
+  a.nlat = (kSmemMax - fixed - a.nrope * kRopeSlot) / kLatSlot;
+  if (a.nlat > kMaxLatSlots) a.nlat = kMaxLatSlots;
+  const int smem = fixed + a.nrope * kRopeSlot + a.nlat * kLatSlot;
+  launch_kernel("mla_decode", mla_decode_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(192), smem, s, tk, tq, a);
+  return MOE_OK;
+}
+
+inline bool mis(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_mla_workspace_size(const moe_mla_config_t* cfg, size_t* bytes) {
+  if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+  if (int r = validate_mla(cfg)) return r;
+  *bytes = mla_layout(cfg).total;
+  return MOE_OK;
+}
+
+extern "C" int moe_mla_append(const moe_mla_config_t* cfg, int n, const void* kv, int ld_kv, const void* gamma,
+                              float eps, const float* cos_sin, int max_pos, const int32_t* seq, const int32_t* pos,
+                              const int32_t* block_table, void* cache, void* ws, moe_stream_t stream) {
+  if (int r = validate_mla(cfg)) return r;
+  if (n < 0 || ld_kv < cfg->latent + cfg->rope || ld_kv % 8 || cache == nullptr || ws == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (n > 0 && (kv == nullptr || seq == nullptr || pos == nullptr || block_table == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (gamma != nullptr && !(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  if (cos_sin != nullptr && max_pos < 1) return MOE_ERR_INVALID_ARG;
+  if (mis(kv, 16) || mis(gamma, 16) || mis(cos_sin, 16) || mis(cache, 16) || mis(ws, 16) || mis(seq, 4) || mis(pos, 4) ||
+      mis(block_table, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (!arch_ok()) return MOE_ERR_UNSUPPORTED_ARCH;
+  CallScope call;
+  if (n == 0) return MOE_OK;
+  AppendArgs a{};
+  a.n = n;
+  a.B = cfg->batch;
+  a.latent = cfg->latent;
+  a.rope = cfg->rope;
+  a.page = cfg->page_size;
+  a.num_pages = cfg->num_pages;
+  a.max_pages = cfg->max_pages;
+  a.ld = ld_kv;
+  a.max_pos = max_pos;
+  a.kv = static_cast<const __nv_bfloat16*>(kv);
+  a.gamma = static_cast<const __nv_bfloat16*>(gamma);
+  a.eps = eps;
+  a.cos_sin = cos_sin;
+  a.seq = seq;
+  a.pos = pos;
+  a.table = block_table;
+  a.cache = static_cast<__nv_bfloat16*>(cache);
+  a.status = reinterpret_cast<int*>(static_cast<char*>(ws) + mla_layout(cfg).status);
+  launch_kernel("mla_append", mla_append_kernel, dim3(static_cast<unsigned>(ceil_div(n, 8))), dim3(256), 0,
+                static_cast<cudaStream_t>(stream), a);
+  return call.status();
+}
+
+extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_t q_stride_b, int64_t q_stride_h,
+                              const void* cache, const int32_t* block_table, const int32_t* seq_lens, void* out,
+                              float* lse, void* ws, moe_stream_t stream) {
+  if (int r = validate_mla(cfg)) return r;
+  const int row = cfg->latent + cfg->rope;
+  if (cache == nullptr || ws == nullptr) return MOE_ERR_INVALID_ARG;
+  if (cfg->batch > 0 && (q == nullptr || block_table == nullptr || seq_lens == nullptr || out == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  // strides in elements; a TMA dimension's pitch is below 2^40 bytes
+  if (q_stride_h < row || q_stride_b < row || q_stride_h % 8 || q_stride_b % 8 || q_stride_h >= (1LL << 38) ||
+      q_stride_b >= (1LL << 38))
+    return MOE_ERR_INVALID_ARG;
+  if (mis(q, 16) || mis(cache, 16) || mis(out, 16) || mis(ws, 16) || mis(lse, 4) || mis(block_table, 4) || mis(seq_lens, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (!arch_ok()) return MOE_ERR_UNSUPPORTED_ARCH;
+  CallScope call;
+  if (cfg->batch == 0) return MOE_OK;
+  if (!get_encode()) return MOE_ERR_CUDA;
+  const MlaLayout L = mla_layout(cfg);
+  char* base = static_cast<char*>(ws);
+  MlaArgs a{};
+  a.B = cfg->batch;
+  a.H = cfg->heads;
+  a.latent = cfg->latent;
+  a.rope = cfg->rope;
+  a.page = cfg->page_size;
+  a.num_pages = cfg->num_pages;
+  a.max_pages = cfg->max_pages;
+  a.G = static_cast<int>(ceil_div(cfg->heads, kMaxHeadsCta));
+  a.hg = static_cast<int>(ceil_div(cfg->heads, a.G));
+  a.nm = cfg->latent / 128;
+  const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
+  a.W = sms / a.G;
+  a.piece = cfg->page_size & -cfg->page_size;
+  if (a.piece > kTile) a.piece = kTile;
+  a.scale2 = cfg->softmax_scale * kLog2e;
+  a.table = block_table;
+  a.lens = seq_lens;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.status = reinterpret_cast<int*>(base + L.status);
+  a.join = reinterpret_cast<int4*>(base + L.join);
+  a.part_m = reinterpret_cast<float*>(base + L.m);
+  a.part_l = reinterpret_cast<float*>(base + L.l);
+  a.part_e = reinterpret_cast<float*>(base + L.e);
+  a.part_o = reinterpret_cast<float*>(base + L.o);
+  const int N = static_cast<int>(round_up(a.hg, 16));
+  CUtensorMap tk, tq;
+  if (!make_tmap_rows(&tk, cache, static_cast<int64_t>(cfg->num_pages) * cfg->page_size, row, a.piece)) return MOE_ERR_CUDA;
+  if (!make_tmap_strided(&tq, q,
+                         {static_cast<uint64_t>(row), static_cast<uint64_t>(cfg->heads), static_cast<uint64_t>(cfg->batch)},
+                         {static_cast<uint64_t>(q_stride_h) * 2, static_cast<uint64_t>(q_stride_b) * 2},
+                         {64, static_cast<uint32_t>(N), 1}, 3))
+    return MOE_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int r;
+  switch (N) {
+    case 16: r = run_decode<16>(a, tk, tq, sms, s); break;
+    case 32: r = run_decode<32>(a, tk, tq, sms, s); break;
+    case 48: r = run_decode<48>(a, tk, tq, sms, s); break;
+    default: r = run_decode<64>(a, tk, tq, sms, s); break;
+  }
+  if (r) return r;
+  if (int e = call.status()) return e;
+  launch_kernel("mla_join", mla_join_kernel, dim3(static_cast<unsigned>(a.W), static_cast<unsigned>(a.H)),
+                dim3(static_cast<unsigned>(a.latent / 4)), 0, s, a);
+  return call.status();
+}
+
+extern "C" int moe_mla_status(const moe_mla_config_t* cfg, void* ws, int* code, int* site, int clear,
+                              moe_stream_t stream) {
+  if (int r = validate_mla(cfg)) return r;
+  if (!ws || !code || !site) return MOE_ERR_INVALID_ARG;
+  return read_status(static_cast<char*>(ws) + mla_layout(cfg).status, code, site, clear, static_cast<cudaStream_t>(stream));
+}

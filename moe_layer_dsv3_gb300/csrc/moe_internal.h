@@ -4,6 +4,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "../../include/moe.h"
 
 namespace moe {
@@ -76,12 +78,36 @@ inline T* wq_ptr(const WLayout& L, void* wq, int which) {
 
 // Per-device caches are indexed by the device ordinal, below this bound.
 constexpr int kMaxDev = 64;
+// SMs that a workspace is sized for; a grid that leaves one partial result per
+// CTA is no larger.
+constexpr int kMaxSms = 160;
 // Current device ordinal, or -1 when it cannot be read or is past kMaxDev.
 int current_device();
 // SM count of the current device (cached per device).
 int num_sms();
 // Current device is compute capability 10.3 (GB300) (cached per device).
 bool arch_ok();
+
+// One-time set-up of a kernel on each device (attributes belong to the current device).
+class DevOnce {
+ public:
+  // True when `f` (returning a cudaError_t) has succeeded on the current device, now or before.
+  template <typename F>
+  bool ready(F f) {
+    const int dev = current_device();
+    if (dev < 0) return false;
+    std::lock_guard<std::mutex> lk(mu_);
+    if (state_[dev] == 0) state_[dev] = f() == cudaSuccess ? 1 : 2;
+    return state_[dev] == 1;
+  }
+
+ private:
+  std::mutex mu_;
+  int state_[kMaxDev] = {};
+};
+
+// Copies a status word pair to the host on `s`, waits for it, and clears it when asked to (MOE_* code).
+int read_status(void* status, int* code, int* site, int clear, cudaStream_t s);
 
 // ---------------------------------------------------------------- call errors
 // An entry point collects the return codes of its own kernel launches and
