@@ -37,6 +37,7 @@ namespace moe {
 
 namespace {
 
+constexpr int kThreads = 224;
 constexpr int kTile = 64;                 // cached tokens per tile
 constexpr int kMaxHeadsCta = 64;          // heads per CTA
 constexpr int kLatSlot = kTile * 256;     // 128 latent columns of a tile: two boxes of [64 tokens][128 bytes]
@@ -164,6 +165,23 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int
       : "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// mbar_wait by a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int site) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, site));
+}
+
 // Barrier over the 128 softmax threads that also gives the OR of their flags.
 __device__ __forceinline__ bool barrier_or(int id, bool flag) {
   uint32_t r;
@@ -195,17 +213,17 @@ struct Smem {
   uint64_t pf, pe;                                      // P: written / its product done
   uint64_t of, oe;                                      // O: all products of the piece done / read
   uint32_t tmem;
-  int scan[6];
+  int scan[kThreads / 32];
   int start_b, start_t;
 };
 static_assert(sizeof(Smem) <= kBarBytes, "control block");
 
 }  // namespace
 
-// Threads: warp 0 loads (TMA), warp 1 issues the MMAs, warps 2-5 do the softmax
-// and the epilogue (TMEM lane quarter warp % 4).
+// Threads: warp 0 loads (TMA), warps 1 and 6 issue the MMAs of S^T and O^T, warps
+// 2-5 do the softmax and the epilogue (TMEM lane quarter warp % 4).
 template <int N>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     mla_decode_kernel(const __grid_constant__ CUtensorMap tma_k, const __grid_constant__ CUtensorMap tma_q,
                       const __grid_constant__ MlaArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -252,7 +270,7 @@ __global__ void __launch_bounds__(192, 1)
   }
   // Range of this worker: prefix sums of the sequences' tiles, a run of
   // sequences per thread, then the thread whose run holds the first tile finds it.
-  const int per = (a.B + 191) / 192;
+  const int per = (a.B + kThreads - 1) / kThreads;
   const int b0 = tid * per < a.B ? tid * per : a.B;
   const int b1 = b0 + per < a.B ? b0 + per : a.B;
   int mine = 0;
@@ -269,7 +287,7 @@ __global__ void __launch_bounds__(192, 1)
   tc_fence_after();
   int before = 0, total = 0;
 #pragma unroll
-  for (int i = 0; i < 6; ++i) {
+  for (int i = 0; i < kThreads / 32; ++i) {
     if (i < warp) before += c.scan[i];
     total += c.scan[i];
   }
@@ -373,76 +391,93 @@ __global__ void __launch_bounds__(192, 1)
       if (issued_q > 0) mbar_wait(&c.qf, qphase ^ 1u, a.status, 64);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16(64, N);
-      constexpr uint32_t idesc_o = idesc_bf16(128, N) | (1u << 15);   // A (V^T) is MN-major
-      Ring lr, rr, pvr;       // pvr: latent ring as the second product walks it
-      uint32_t qphase = 0, pphase = 0, ophase = 0;
-      int sbuf = 0;
-      uint32_t sphase = 0;
-      // One tile behind S^T: the pending O^T product of the previous tile.
-      bool pending = false, pend_first = false, pend_last = false;
-      auto pv = [&]() -> bool {
-        if (!mbar_wait(&c.pf, pphase, a.status, 70)) return false;
-        pphase ^= 1u;
-        if (pend_first) {     // the previous piece's O has been read
-          if (!mbar_wait(&c.oe, ophase ^ 1u, a.status, 71)) return false;
-          ophase ^= 1u;
-        }
+    // Issues S^T. The whole warp walks the tiles and waits, and one elected lane
+    // issues; with every wait's result and every length taken warp-wide, the
+    // descriptors stay in uniform registers. That counts: an MMA of these sizes
+    // takes 23 to 48 clocks, and issuing one from a divergent branch took 100.
+    constexpr uint32_t idesc_s = idesc_bf16(64, N);
+    constexpr uint32_t kLatStep = kLatSlot >> 4, kRopeStep = kRopeSlot >> 4;   // descriptor address units
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + kSCol;
+    const uint64_t dq0 = desc_kmajor_sw128(smem_u32(sq)), dl0 = desc_kmajor_sw128(smem_u32(lat));
+    const uint64_t dr0 = desc_kmajor_sw128(smem_u32(ropes));
+    Ring lr, rr;
+    uint32_t qphase = 0, sbuf = 0, sphase = 0;
+    while (ok && wk.next(a, started)) {
+      const int n = __shfl_sync(0xffffffffu, wk.n, 0);
+      ok = warp_wait(&c.qf, qphase, a.status, 72);
+      qphase ^= 1u;
+      for (int i = 0; i < n && ok; ++i) {
+        ok = warp_wait(&c.se[sbuf], sphase ^ 1u, a.status, 73) && warp_wait(&c.ropef[rr.slot], rr.phase, a.status, 74);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t bp = smem_u32(sp);
-        for (int m = 0; m < nm; ++m) {
-          const uint32_t av = smem_u32(lat + pvr.slot * kLatSlot);
+        const uint32_t d = tm + sbuf * N;
+        if (elect_one()) {
+          const uint64_t dr = dr0 + rr.slot * kRopeStep, dqr = dq0 + (nchunk - 1) * (N * 8);
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            tc_mma_bf16(tmem + m * N, smem_desc(av + kk * 2048, kTile * 128, 1024, 2), desc_kmajor_sw128(bp + kk * 32),
-                        idesc_o, !(pend_first && kk == 0));
-          tc_commit(&c.late[pvr.slot]);
-          pvr.step(a.nlat);
-        }
-        tc_commit(&c.pe);
-        if (pend_last) tc_commit(&c.of);
-        return true;
-      };
-      while (ok && wk.next(a, started)) {
-        ok = mbar_wait(&c.qf, qphase, a.status, 72);
-        qphase ^= 1u;
-        for (int i = 0; i < wk.n && ok; ++i) {
-          ok = mbar_wait(&c.se[sbuf], sphase ^ 1u, a.status, 73) && mbar_wait(&c.ropef[rr.slot], rr.phase, a.status, 74);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem + kSCol + sbuf * N;
-          const uint32_t qb = smem_u32(sq);
-          const uint32_t ar = smem_u32(ropes + rr.slot * kRopeSlot);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_bf16(d, desc_kmajor_sw128(ar + kk * 32), desc_kmajor_sw128(qb + (nchunk - 1) * N * 128 + kk * 32),
-                        idesc_s, kk != 0);
+          for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, dr + kk * 2, dqr + kk * 2, idesc_s, kk != 0);
           tc_commit(&c.ropee[rr.slot]);
-          rr.step(a.nrope);
-          for (int m = 0; m < nm; ++m) {
-            if (!(ok = mbar_wait(&c.latf[lr.slot], lr.phase, a.status, 75))) break;
-            tc_fence_after();
-            const uint32_t al = smem_u32(lat + lr.slot * kLatSlot);
+        }
+        __syncwarp();
+        rr.step(a.nrope);
+        for (int m = 0; m < nm && ok; ++m) {
+          ok = warp_wait(&c.latf[lr.slot], lr.phase, a.status, 75);
+          tc_fence_after();
+          if (ok && elect_one()) {
+            const uint64_t dl = dl0 + lr.slot * kLatStep, dqm = dq0 + m * (2 * N * 8);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              tc_mma_bf16(d, desc_kmajor_sw128(al + (kk >> 2) * (kTile * 128) + (kk & 3) * 32),
-                          desc_kmajor_sw128(qb + (2 * m + (kk >> 2)) * N * 128 + (kk & 3) * 32), idesc_s, 1);
-            lr.step(a.nlat);
+              tc_mma_bf16(d, dl + (kk >> 2) * (kTile * 8) + (kk & 3) * 2, dqm + (kk >> 2) * (N * 8) + (kk & 3) * 2,
+                          idesc_s, 1);
           }
-          if (!ok) break;
-          tc_commit(&c.sf[sbuf]);
-          if (i == wk.n - 1) tc_commit(&c.qe);
-          sbuf ^= 1;
-          if (sbuf == 0) sphase ^= 1u;
-          if (pending) ok = pv();
-          pending = true;
-          pend_first = i == 0;
-          pend_last = i == wk.n - 1;
+          __syncwarp();
+          lr.step(a.nlat);
         }
-        wk.done();
+        if (!ok) break;
+        if (elect_one()) {
+          tc_commit(&c.sf[sbuf]);
+          if (i == n - 1) tc_commit(&c.qe);
+        }
+        __syncwarp();
+        sbuf ^= 1;
+        if (sbuf == 0) sphase ^= 1u;
       }
-      if (ok && pending) pv();
+      wk.done();
+    }
+  } else if (warp == 6) {
+    // Issues O^T, in a warp of its own: it then never waits behind the next tile's data.
+    constexpr uint32_t idesc_o = idesc_bf16(128, N) | (1u << 15);   // A (V^T) is MN-major
+    constexpr uint32_t kLatStep = kLatSlot >> 4;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t dp0 = desc_kmajor_sw128(smem_u32(sp)), dv0 = smem_desc(smem_u32(lat), kTile * 128, 1024, 2);
+    Ring lr;
+    uint32_t pphase = 0, ophase = 0;
+    while (ok && wk.next(a, started)) {
+      const int n = __shfl_sync(0xffffffffu, wk.n, 0);
+      ok = warp_wait(&c.oe, ophase ^ 1u, a.status, 71);             // the previous piece's O has been read
+      ophase ^= 1u;
+      for (int i = 0; i < n && ok; ++i) {
+        ok = warp_wait(&c.pf, pphase, a.status, 70);                // P is written, so the tile's data is there
+        if (!ok) break;
+        pphase ^= 1u;
+        tc_fence_after();
+        for (int m = 0; m < nm; ++m) {
+          if (elect_one()) {
+            const uint64_t dv = dv0 + lr.slot * kLatStep;
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              tc_mma_bf16(tm + m * N, dv + kk * 128, dp0 + kk * 2, idesc_o, i > 0 || kk > 0);
+            tc_commit(&c.late[lr.slot]);
+          }
+          __syncwarp();
+          lr.step(a.nlat);
+        }
+        if (elect_one()) {
+          tc_commit(&c.pe);
+          if (i == n - 1) tc_commit(&c.of);
+        }
+        __syncwarp();
+      }
+      wk.done();
     }
   } else {
     const int q = warp & 3;
@@ -893,7 +928,7 @@ int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tq, int sms,
   a.nlat = (kSmemMax - fixed - a.nrope * kRopeSlot) / kLatSlot;
   if (a.nlat > kMaxLatSlots) a.nlat = kMaxLatSlots;
   const int smem = fixed + a.nrope * kRopeSlot + a.nlat * kLatSlot;
-  launch_kernel("mla_decode", mla_decode_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(192), smem, s, tk, tq, a);
+  launch_kernel("mla_decode", mla_decode_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(kThreads), smem, s, tk, tq, a);
   return MOE_OK;
 }
 
