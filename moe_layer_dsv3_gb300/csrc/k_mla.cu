@@ -52,6 +52,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // before O is rescaled: P and the sums stay far inside fp32 and bf16 range, and
 // their relative precision does not depend on the reference.
 constexpr float kSlack = 10.0f;
+// Reference of a head that has met no score above it: any such score is far past kSlack, and P of -inf is 0.
+constexpr float kNoRef = -3.0e38f;
 
 struct MlaArgs {
   int B, H, latent, rope, page, num_pages, max_pages;
@@ -107,6 +109,7 @@ struct Walk {
   bool first;                // the worker's first piece
   __device__ __forceinline__ bool next(const MlaArgs& a, bool& started) {
     if (left <= 0) return false;
+#pragma unroll 1
     while (true) {
       if (b >= a.B) return false;
       len = seq_len(a, b, false);
@@ -176,10 +179,24 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// mbar_wait by a whole warp: the same answer in every lane.
+// mbar_wait in few instructions. Seven warps run five different loops here, and
+// with mbar_wait's unrolled polls at every wait the kernel was 150 KB of code:
+// its instruction-cache misses set the pace of every warp.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int* status, int site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      report_error(status, kErrTimeout, site);
+      return false;
+    }
+  return true;
+}
+
+// bar_wait by a whole warp: the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int site) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, site));
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, status, site));
 }
 
 // Barrier over the 128 softmax threads that also gives the OR of their flags.
@@ -224,8 +241,8 @@ static_assert(sizeof(Smem) <= kBarBytes, "control block");
 // 2-5 do the softmax and the epilogue (TMEM lane quarter warp % 4).
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1)
-    mla_decode_kernel(const __grid_constant__ CUtensorMap tma_k, const __grid_constant__ CUtensorMap tma_q,
-                      const __grid_constant__ MlaArgs a) {
+    mla_decode_kernel(const __grid_constant__ CUtensorMap tma_k, const __grid_constant__ CUtensorMap tma_r,
+                      const __grid_constant__ CUtensorMap tma_q, const __grid_constant__ MlaArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nm = a.nm, nchunk = 2 * nm + 1;            // 64-column chunks of a row: latent, then rope
@@ -262,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
     fence_proxy_async();
     tma_prefetch(&tma_k);
+    tma_prefetch(&tma_r);
     tma_prefetch(&tma_q);
   }
   if (warp == 1) {
@@ -274,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int b0 = tid * per < a.B ? tid * per : a.B;
   const int b1 = b0 + per < a.B ? b0 + per : a.B;
   int mine = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) mine += tiles_of(seq_len(a, b, blockIdx.x == 0));
   int incl = mine;
 #pragma unroll
@@ -297,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     int at = before + incl - mine;
     if (f0 >= at && f0 < at + mine)
+#pragma unroll 1
       for (int b = b0; b < b1; ++b) {
         const int n = tiles_of(seq_len(a, b, false));
         if (f0 < at + n) {
@@ -316,79 +336,97 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool started = false, ok = true;
 
   if (warp == 0) {
+    // Loads. Like the MMA warps, the whole warp walks and one elected lane issues
+    // from warp-uniform registers (a box took about 250 clocks to issue from a
+    // divergent lane, and this warp then set the pace).
     Ring lr, rr;
     uint32_t qphase = 0;
     int issued_lat = 0, issued_rope = 0, issued_q = 0;
     const int pieces = kTile / a.piece;
-    const int64_t oob = static_cast<int64_t>(a.num_pages) * a.page;   // a row past the cache: reads zeros
+    const int oob = a.num_pages * a.page;               // a row past the cache: reads zeros
     const int h0 = g * a.hg;
     while (ok && wk.next(a, started)) {
-      // Q of this sequence and head group, once the previous piece's products have read the last one.
-      if (lane == 0) {
-        ok = mbar_wait(&c.qe, qphase ^ 1u, a.status, 61);
-        if (ok) {
-          mbar_arrive_expect_tx(&c.qf, nchunk * N * 128);
-          for (int k = 0; k < nchunk; ++k) tma_load_3d(sq + k * N * 128, &tma_q, k * 64, h0, wk.b, &c.qf);
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      qphase ^= 1u;
-      ++issued_q;
-      // Row of this lane's piece of tile t: the page is read one tile ahead of its loads.
-      const int32_t* table = a.table + static_cast<int64_t>(wk.b) * a.max_pages;
+      const int b = __shfl_sync(0xffffffffu, wk.b, 0), len = __shfl_sync(0xffffffffu, wk.len, 0);
+      const int t0 = __shfl_sync(0xffffffffu, wk.t0, 0), t1 = t0 + __shfl_sync(0xffffffffu, wk.n, 0);
+      // Lane p: page of piece p of tile t, and its first row. Pages are read a tile ahead of their use.
+      const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
       auto page_of = [&](int t) {
         const int tok = t * kTile + lane * a.piece;
-        return (lane < pieces && t < wk.nt && tok < wk.len) ? __ldg(table + tok / a.page) : -1;
+        return (lane < pieces && t < t1 && tok < len) ? __ldg(table + tok / a.page) : 0;
       };
-      int page = page_of(wk.t0);
-      for (int t = wk.t0; t < wk.t0 + wk.n && ok; ++t) {
+      auto row_of = [&](int t, int page) {
         const int tok = t * kTile + lane * a.piece;
-        const bool live = lane < pieces && tok < wk.len;
-        const int live_pieces = __popc(__ballot_sync(0xffffffffu, live));
-        int row = 0;
-        if (live) {
-          if (page < 0 || page >= a.num_pages) {
-            report_error(a.status, kErrBounds, 62);
-            row = static_cast<int>(oob);
-          } else {
-            row = page * a.page + tok % a.page;
-          }
-        }
-        page = page_of(t + 1);
-        for (int s = -1; s < nm && ok; ++s) {            // rope chunk first, then 128 latent columns a slot
+        if (page >= 0 && page < a.num_pages) return page * a.page + tok % a.page;
+        report_error(a.status, kErrBounds, 62);
+        return oob;
+      };
+      int page = page_of(t0);
+      // Q of this sequence and head group, once the previous piece's products have read the last one.
+      ok = warp_wait(&c.qe, qphase ^ 1u, a.status, 61);
+      if (!ok) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&c.qf, nchunk * N * 128);
+#pragma unroll 1
+        for (int k = 0; k < nchunk; ++k) tma_load_3d(sq + k * N * 128, &tma_q, k * 64, h0, b, &c.qf);
+      }
+      __syncwarp();
+      qphase ^= 1u;
+      ++issued_q;
+      int row = row_of(t0, page);
+      page = page_of(t0 + 1);
+#pragma unroll 1
+      for (int t = t0; t < t1 && ok; ++t) {
+        const int left = len - t * kTile;
+        const int live = left >= kTile ? pieces : (left + a.piece - 1) / a.piece;   // pieces with tokens
+#pragma unroll 1
+        for (int s = -1; s < nm && ok; ++s) {            // rope columns first, then 128 latent columns a slot
           const bool rope = s < 0;
-          Ring& r = rope ? rr : lr;
-          uint64_t* full = rope ? &c.ropef[r.slot] : &c.latf[r.slot];
-          uint64_t* empty = rope ? &c.ropee[r.slot] : &c.late[r.slot];
-          uint8_t* dst = rope ? ropes + r.slot * kRopeSlot : lat + r.slot * kLatSlot;
-          if (lane == 0) {
-            ok = mbar_wait(empty, r.phase ^ 1u, a.status, 63);
-            if (ok) mbar_arrive_expect_tx(full, live_pieces * a.piece * (rope ? 128 : 256));
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
+          uint64_t* full = rope ? &c.ropef[rr.slot] : &c.latf[lr.slot];
+          ok = warp_wait(rope ? &c.ropee[rr.slot] : &c.late[lr.slot], (rope ? rr.phase : lr.phase) ^ 1u, a.status, 63);
           if (!ok) break;
-          if (live) {
-            tma_load_2d(dst + lane * a.piece * 128, &tma_k, rope ? a.latent : s * 128, row, full);
-            if (!rope) tma_load_2d(dst + kTile * 128 + lane * a.piece * 128, &tma_k, s * 128 + 64, row, full);
+          uint8_t* dst = rope ? ropes + rr.slot * kRopeSlot : lat + lr.slot * kLatSlot;
+          if (elect_one()) mbar_arrive_expect_tx(full, live * a.piece * (rope ? 128 : 256));
+          __syncwarp();
+#pragma unroll 1
+          for (int p = 0; p < live; ++p) {
+            const int y = __shfl_sync(0xffffffffu, row, p);
+            if (elect_one()) {
+              uint8_t* d = dst + p * a.piece * 128;
+              if (rope) {
+                tma_load_2d(d, &tma_r, a.latent, y, full);
+              } else {
+                tma_load_3d(d, &tma_k, 0, y, 2 * s, full);   // both 64-column halves when the piece is a whole tile
+                if (pieces > 1) tma_load_3d(d + kTile * 128, &tma_k, 0, y, 2 * s + 1, full);
+              }
+            }
+            __syncwarp();
           }
-          r.step(rope ? a.nrope : a.nlat);
-          if (rope) ++issued_rope; else ++issued_lat;
+          if (rope) {
+            rr.step(a.nrope);
+            ++issued_rope;
+          } else {
+            lr.step(a.nlat);
+            ++issued_lat;
+          }
         }
+        row = row_of(t + 1, page);
+        page = page_of(t + 2);
       }
       wk.done();
     }
     // Every copy this CTA started has landed before its shared memory is released.
     if (lane == 0) {
+#pragma unroll 1
       for (int i = 0, n = issued_lat < a.nlat ? issued_lat : a.nlat; i < n; ++i) {
         if (--lr.slot < 0) { lr.slot = a.nlat - 1; lr.phase ^= 1u; }
-        mbar_wait(&c.latf[lr.slot], lr.phase, a.status, 64);
+        bar_wait(&c.latf[lr.slot], lr.phase, a.status, 64);
       }
+#pragma unroll 1
       for (int i = 0, n = issued_rope < a.nrope ? issued_rope : a.nrope; i < n; ++i) {
         if (--rr.slot < 0) { rr.slot = a.nrope - 1; rr.phase ^= 1u; }
-        mbar_wait(&c.ropef[rr.slot], rr.phase, a.status, 64);
+        bar_wait(&c.ropef[rr.slot], rr.phase, a.status, 64);
       }
-      if (issued_q > 0) mbar_wait(&c.qf, qphase ^ 1u, a.status, 64);
+      if (issued_q > 0) bar_wait(&c.qf, qphase ^ 1u, a.status, 64);
     }
   } else if (warp == 1) {
     // Issues S^T. The whole warp walks the tiles and waits, and one elected lane
@@ -406,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = __shfl_sync(0xffffffffu, wk.n, 0);
       ok = warp_wait(&c.qf, qphase, a.status, 72);
       qphase ^= 1u;
+#pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
         ok = warp_wait(&c.se[sbuf], sphase ^ 1u, a.status, 73) && warp_wait(&c.ropef[rr.slot], rr.phase, a.status, 74);
         if (!ok) break;
@@ -419,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         rr.step(a.nrope);
+#pragma unroll 1
         for (int m = 0; m < nm && ok; ++m) {
           ok = warp_wait(&c.latf[lr.slot], lr.phase, a.status, 75);
           tc_fence_after();
@@ -455,11 +495,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = __shfl_sync(0xffffffffu, wk.n, 0);
       ok = warp_wait(&c.oe, ophase ^ 1u, a.status, 71);             // the previous piece's O has been read
       ophase ^= 1u;
+#pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
         ok = warp_wait(&c.pf, pphase, a.status, 70);                // P is written, so the tile's data is there
         if (!ok) break;
         pphase ^= 1u;
         tc_fence_after();
+#pragma unroll 1
         for (int m = 0; m < nm; ++m) {
           if (elect_one()) {
             const uint64_t dv = dv0 + lr.slot * kLatStep;
@@ -493,19 +535,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // After a wait that gave up, these threads stop waiting but keep walking: all 128 then
     // meet at every barrier, and the kernel ends.
     auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
-      if (ok) ok = mbar_wait(bar, parity, a.status, site);
+      if (ok) ok = bar_wait(bar, parity, a.status, site);
     };
     while (wk.next(a, started)) {
       // Heads 8 i + 2 (lane % 4) + e of this thread; rows q * 16 + lane / 4 and + 8 of a tile.
-      float mref[NP][2], l[NP][2], le[NP][2];
+      float ref[NP][2], l[NP][2], le[NP][2];
 #pragma unroll
       for (int i = 0; i < NP; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mref[i][e] = -INFINITY;
+          ref[i][e] = kNoRef;
           l[i][e] = 0.0f;
           le[i][e] = 0.0f;
         }
+#pragma unroll 1
       for (int ti = 0; ti < wk.n; ++ti) {
         const int valid = wk.len - (wk.t0 + ti) * kTile;   // tokens of the tile (>= 64: all)
         wait(&c.sf[sbuf], sphase, 80);
@@ -520,30 +563,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&c.se[sbuf]);
         sbuf ^= 1;
         if (sbuf == 0) sphase ^= 1u;
-        const int row = q * 16 + (lane >> 2);
-        float s[NP][4];
-        float over = -INFINITY;
+        if (valid < kTile) {
+          const int row = q * 16 + (lane >> 2);
+#pragma unroll
+          for (int i = 0; i < 4 * NP; ++i)
+            if (row + 8 * ((i >> 1) & 1) >= valid) r[i] = __float_as_uint(-INFINITY);
+        }
+        // Scores above their head's reference, in powers of two. O is rescaled only when one of the tile
+        // passes kSlack, as in a piece's first tile.
+        float y[NP][4], over = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NP; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[i][e] = __uint_as_float(r[4 * i + e]) * a.scale2;
-            if (row + 8 * (e >> 1) >= valid) s[i][e] = -INFINITY;
-            over = fmaxf(over, s[i][e] - mref[i][e & 1]);   // +inf in a piece's first tile (or NaN: -inf - -inf)
+            y[i][e] = fmaf(__uint_as_float(r[4 * i + e]), a.scale2, -ref[i][e & 1]);
+            over = fmaxf(over, y[i][e]);
           }
-        // O is rescaled only when some score passes its head's reference by kSlack; always in the first tile.
-        const bool grow = barrier_or(2, ti == 0 || over > kSlack);
-        float corr[NP][2];
+        const bool grow = barrier_or(2, over > kSlack);
         if (grow) {
 #pragma unroll
           for (int i = 0; i < NP; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float m = fmaxf(s[i][e], s[i][e + 2]);
+              float m = fmaxf(__uint_as_float(r[4 * i + e]), __uint_as_float(r[4 * i + e + 2]));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-              if (lane < 4) smax[q * kMaxHeadsCta + 8 * i + 2 * lane + e] = m;
+              if (lane < 4) smax[q * kMaxHeadsCta + 8 * i + 2 * lane + e] = m * a.scale2;
             }
           named_barrier(3, 128);
 #pragma unroll
@@ -551,29 +597,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int h = 8 * i + 2 * (lane & 3) + e;
-              float m = fmaxf(fmaxf(smax[h], smax[kMaxHeadsCta + h]),
-                              fmaxf(smax[2 * kMaxHeadsCta + h], smax[3 * kMaxHeadsCta + h]));
-              m = fmaxf(m, mref[i][e]);
-              corr[i][e] = mref[i][e] == -INFINITY ? 0.0f : ex2(mref[i][e] - m);
-              mref[i][e] = m;
-              l[i][e] *= corr[i][e];
-              le[i][e] *= corr[i][e];
-              if (q == 0 && lane < 4) fac[h] = corr[i][e];
+              const float m = fmaxf(fmaxf(fmaxf(smax[h], smax[kMaxHeadsCta + h]),
+                                          fmaxf(smax[2 * kMaxHeadsCta + h], smax[3 * kMaxHeadsCta + h])),
+                                    ref[i][e]);
+              const float corr = ex2(ref[i][e] - m);       // 0 from kNoRef to a score
+              l[i][e] *= corr;
+              le[i][e] *= corr;
+              ref[i][e] = m;
+              if (q == 0 && lane < 4) fac[h] = corr;
+              y[i][e] = fmaf(__uint_as_float(r[4 * i + e]), a.scale2, -m);
+              y[i][e + 2] = fmaf(__uint_as_float(r[4 * i + e + 2]), a.scale2, -m);
             }
         }
         uint32_t p[NP][2];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-          float x[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            // a head that has seen only -inf keeps a zero reference, so its P is 0 and not NaN
-            const float m = mref[i][e & 1] == -INFINITY ? 0.0f : mref[i][e & 1];
-            x[e] = ex2(s[i][e] - m);
-            le[i][e & 1] += x[e];
+            y[i][e] = ex2(y[i][e]);
+            le[i][e & 1] += y[i][e];
           }
-          p[i][0] = pack_bf16x2(x[0], x[1]);
-          p[i][1] = pack_bf16x2(x[2], x[3]);
+          p[i][0] = pack_bf16x2(y[i][0], y[i][1]);
+          p[i][1] = pack_bf16x2(y[i][2], y[i][3]);
           // P enters the product rounded to bf16; the same rounded values are summed for its normalisation
           l[i][0] += __uint_as_float(p[i][0] << 16) + __uint_as_float(p[i][1] << 16);
           l[i][1] += __uint_as_float(p[i][0] & 0xFFFF0000u) + __uint_as_float(p[i][1] & 0xFFFF0000u);
@@ -588,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           named_barrier(3, 128);                           // fac is written
           if (ti > 0) {
             tc_fence_after();
+#pragma unroll 1
             for (int m = 0; m < nm; ++m)
 #pragma unroll
               for (int hc = 0; hc < N; hc += 16) {
@@ -615,9 +661,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Rows past the sequence's end hold whatever the page held (NaN included): their P is 0, and they
           // have to be 0 themselves for the product. Only a sequence's last tile is partial.
           Ring z = lr;
+#pragma unroll 1
           for (int m = 0; m < nm; ++m) {
             wait(&c.latf[z.slot], z.phase, 82);
             uint4* v = reinterpret_cast<uint4*>(lat + z.slot * kLatSlot);
+#pragma unroll 1
             for (int i = st; i < 2 * (kTile - valid) * 8; i += 128) {
               const int half = i / ((kTile - valid) * 8), k = i - half * ((kTile - valid) * 8);
               v[half * kTile * 8 + valid * 8 + k] = make_uint4(0, 0, 0, 0);
@@ -667,9 +715,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               fac[h] = tot[0][i][e] == 0.0f ? 0.0f : 1.0f / tot[0][i][e];
               if (a.lse != nullptr && h < nh)
                 a.lse[static_cast<int64_t>(wk.b) * a.H + head0 + h] =
-                    tot[1][i][e] == 0.0f ? -INFINITY : (mref[i][e] + log2f(tot[1][i][e])) * kLn2;
+                    tot[1][i][e] == 0.0f ? -INFINITY : (ref[i][e] + log2f(tot[1][i][e])) * kLn2;
             } else {
-              a.part_m[slot * kMaxHeadsCta + h] = mref[i][e];
+              a.part_m[slot * kMaxHeadsCta + h] = ref[i][e];
               a.part_l[slot * kMaxHeadsCta + h] = tot[0][i][e];
               a.part_e[slot * kMaxHeadsCta + h] = tot[1][i][e];
             }
@@ -681,6 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (whole) {
         __nv_bfloat16* out = a.out + (static_cast<int64_t>(wk.b) * a.H + head0) * a.latent;
+#pragma unroll 1
         for (int m = 0; m < nm; ++m) {
           const int dv = m * 128 + q * 32 + lane;
 #pragma unroll
@@ -703,6 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         float* out = a.part_o + static_cast<int64_t>(slot) * kMaxHeadsCta * a.latent;
+#pragma unroll 1
         for (int m = 0; m < nm; ++m) {
           const int dv = m * 128 + q * 32 + lane;
 #pragma unroll
@@ -738,11 +788,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       a.join[w] = j;
     }
     // Sequences without tokens: zero rows, lse = -inf.
+#pragma unroll 1
     for (int b = w; b < a.B; b += a.W) {
       if (seq_len(a, b, false) > 0) continue;
       __nv_bfloat16* out = a.out + (static_cast<int64_t>(b) * a.H + head0) * a.latent;
+#pragma unroll 1
       for (int i = st; i < nh * a.latent / 8; i += 128) reinterpret_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
       if (a.lse != nullptr)
+#pragma unroll 1
         for (int i = st; i < nh; i += 128) a.lse[static_cast<int64_t>(b) * a.H + head0 + i] = -INFINITY;
     }
   }
@@ -873,10 +926,18 @@ __global__ void __launch_bounds__(256) mla_append_kernel(const __grid_constant__
 
 namespace {
 
-// Cache as [rows][latent + rope], box 64 columns x `piece` rows, 128-byte swizzle.
-bool make_tmap_rows(CUtensorMap* m, const void* base, int64_t rows, int cols, int piece) {
-  return make_tmap_strided(m, base, {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), 1},
-                           {static_cast<uint64_t>(cols) * 2, 0}, {64, static_cast<uint32_t>(piece), 1}, 2);
+// The cache's latent columns as [latent / 64][rows][64]: a box is `piece` rows of one 64-column chunk, or of two
+// when the piece is a whole tile (a slot is two chunks of 64 rows).
+bool make_tmap_latent(CUtensorMap* m, const void* base, int64_t rows, const moe_mla_config_t* c, int piece) {
+  const uint64_t pitch = static_cast<uint64_t>(c->latent + c->rope) * 2;
+  return make_tmap_strided(m, base, {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(c->latent / 64)}, {pitch, 128},
+                           {64, static_cast<uint32_t>(piece), piece == kTile ? 2u : 1u}, 3);
+}
+// Whole cache rows; the rope columns are one box of 64, zero past the row's end.
+bool make_tmap_rope(CUtensorMap* m, const void* base, int64_t rows, const moe_mla_config_t* c, int piece) {
+  const uint64_t cols = static_cast<uint64_t>(c->latent + c->rope);
+  return make_tmap_strided(m, base, {cols, static_cast<uint64_t>(rows), 1}, {cols * 2, 0},
+                           {64, static_cast<uint32_t>(piece), 1}, 2);
 }
 
 int validate_mla(const moe_mla_config_t* c) {
@@ -917,7 +978,7 @@ MlaLayout mla_layout(const moe_mla_config_t* c) {
 }
 
 template <int N>
-int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tq, int sms, cudaStream_t s) {
+int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CUtensorMap& tq, cudaStream_t s) {
   static DevOnce once;
   if (!once.ready([] {
         return cudaFuncSetAttribute(mla_decode_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
@@ -928,7 +989,8 @@ int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tq, int sms,
   a.nlat = (kSmemMax - fixed - a.nrope * kRopeSlot) / kLatSlot;
   if (a.nlat > kMaxLatSlots) a.nlat = kMaxLatSlots;
   const int smem = fixed + a.nrope * kRopeSlot + a.nlat * kLatSlot;
-  launch_kernel("mla_decode", mla_decode_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(kThreads), smem, s, tk, tq, a);
+  launch_kernel("mla_decode", mla_decode_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(kThreads), smem, s, tk, tr, tq,
+                a);
   return MOE_OK;
 }
 
@@ -1033,8 +1095,10 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
   a.part_e = reinterpret_cast<float*>(base + L.e);
   a.part_o = reinterpret_cast<float*>(base + L.o);
   const int N = static_cast<int>(round_up(a.hg, 16));
-  CUtensorMap tk, tq;
-  if (!make_tmap_rows(&tk, cache, static_cast<int64_t>(cfg->num_pages) * cfg->page_size, row, a.piece)) return MOE_ERR_CUDA;
+  CUtensorMap tk, tr, tq;
+  const int64_t rows = static_cast<int64_t>(cfg->num_pages) * cfg->page_size;
+  if (!make_tmap_latent(&tk, cache, rows, cfg, a.piece) || !make_tmap_rope(&tr, cache, rows, cfg, a.piece))
+    return MOE_ERR_CUDA;
   if (!make_tmap_strided(&tq, q,
                          {static_cast<uint64_t>(row), static_cast<uint64_t>(cfg->heads), static_cast<uint64_t>(cfg->batch)},
                          {static_cast<uint64_t>(q_stride_h) * 2, static_cast<uint64_t>(q_stride_b) * 2},
@@ -1043,10 +1107,10 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int r;
   switch (N) {
-    case 16: r = run_decode<16>(a, tk, tq, sms, s); break;
-    case 32: r = run_decode<32>(a, tk, tq, sms, s); break;
-    case 48: r = run_decode<48>(a, tk, tq, sms, s); break;
-    default: r = run_decode<64>(a, tk, tq, sms, s); break;
+    case 16: r = run_decode<16>(a, tk, tr, tq, s); break;
+    case 32: r = run_decode<32>(a, tk, tr, tq, s); break;
+    case 48: r = run_decode<48>(a, tk, tr, tq, s); break;
+    default: r = run_decode<64>(a, tk, tr, tq, s); break;
   }
   if (r) return r;
   if (int e = call.status()) return e;
