@@ -40,8 +40,7 @@ namespace {
 constexpr int kThreads = 224;
 constexpr int kTile = 64;                 // cached tokens per tile
 constexpr int kMaxHeadsCta = 64;          // heads per CTA
-constexpr int kLatSlot = kTile * 256;     // 128 latent columns of a tile: two boxes of [64 tokens][128 bytes]
-constexpr int kRopeSlot = kTile * 128;    // the rope columns (64, zero-filled past `rope`)
+constexpr int kChunk = kTile * 128;       // 64 columns of a tile: [64 tokens][128 bytes]
 constexpr int kMaxLatSlots = 12;
 constexpr int kMaxRopeSlots = 3;
 constexpr int kBarBytes = 512;
@@ -58,8 +57,8 @@ constexpr float kNoRef = -3.0e38f;
 struct MlaArgs {
   int B, H, latent, rope, page, num_pages, max_pages;
   int G, hg;                 // head groups, heads per group
-  int nm;                    // latent / 128
-  int nlat, nrope;           // ring slots
+  int nm, um, nu;            // latent / 128; 128-column tiles per ring slot; slots per token tile
+  int nlat, nrope;           // ring slots: latent, rope
   int W;                     // workers per head group
   int piece;                 // tokens per TMA box: a power of two that divides the page
   float scale2;              // scale * log2(e)
@@ -224,7 +223,7 @@ struct Ring {
 
 struct Smem {
   uint64_t latf[kMaxLatSlots], late[kMaxLatSlots];     // latent slots: filled / free
-  uint64_t ropef[kMaxRopeSlots], ropee[kMaxRopeSlots];
+  uint64_t ropee[kMaxRopeSlots];                       // (a tile's rope columns arrive with its first latent slot)
   uint64_t qf, qe;                                      // Q of the piece: filled / free
   uint64_t sf[2], se[2];                                // S^T buffers: products done / read
   uint64_t pf, pe;                                      // P: written / its product done
@@ -247,8 +246,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nm = a.nm, nchunk = 2 * nm + 1;            // 64-column chunks of a row: latent, then rope
   uint8_t* lat = smem;
-  uint8_t* ropes = lat + a.nlat * kLatSlot;
-  uint8_t* sq = ropes + a.nrope * kRopeSlot;           // [nchunk][N][128 bytes]
+  const int slot_bytes = a.um * 2 * kChunk;
+  uint8_t* ropes = lat + a.nlat * slot_bytes;
+  uint8_t* sq = ropes + a.nrope * kChunk;           // [nchunk][N][128 bytes]
   uint8_t* sp = sq + nchunk * N * 128;                 // [N][128 bytes]: P, 64 tokens a head
   Smem& c = *reinterpret_cast<Smem*>(sp + N * 128);
   float* smax = reinterpret_cast<float*>(sp + N * 128 + kBarBytes);   // [4][64]
@@ -262,10 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c.latf[i], 1);
       mbar_init(&c.late[i], 1);
     }
-    for (int i = 0; i < a.nrope; ++i) {
-      mbar_init(&c.ropef[i], 1);
-      mbar_init(&c.ropee[i], 1);
-    }
+    for (int i = 0; i < a.nrope; ++i) mbar_init(&c.ropee[i], 1);
     mbar_init(&c.qf, 1);
     mbar_init(&c.qe, 1);
     for (int i = 0; i < 2; ++i) {
@@ -341,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // divergent lane, and this warp then set the pace).
     Ring lr, rr;
     uint32_t qphase = 0;
-    int issued_lat = 0, issued_rope = 0, issued_q = 0;
+    int issued = 0, issued_q = 0;
     const int pieces = kTile / a.piece;
     const int oob = a.num_pages * a.page;               // a row past the cache: reads zeros
     const int h0 = g * a.hg;
@@ -378,37 +375,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = t0; t < t1 && ok; ++t) {
         const int left = len - t * kTile;
         const int live = left >= kTile ? pieces : (left + a.piece - 1) / a.piece;   // pieces with tokens
+        const int y = __shfl_sync(0xffffffffu, row, 0);
 #pragma unroll 1
-        for (int s = -1; s < nm && ok; ++s) {            // rope columns first, then 128 latent columns a slot
-          const bool rope = s < 0;
-          uint64_t* full = rope ? &c.ropef[rr.slot] : &c.latf[lr.slot];
-          ok = warp_wait(rope ? &c.ropee[rr.slot] : &c.late[lr.slot], (rope ? rr.phase : lr.phase) ^ 1u, a.status, 63);
+        for (int u = 0; u < a.nu && ok; ++u) {           // a slot of latent columns, the rope columns with the first
+          if (u == 0) ok = warp_wait(&c.ropee[rr.slot], rr.phase ^ 1u, a.status, 63);
+          ok = ok && warp_wait(&c.late[lr.slot], lr.phase ^ 1u, a.status, 63);
           if (!ok) break;
-          uint8_t* dst = rope ? ropes + rr.slot * kRopeSlot : lat + lr.slot * kLatSlot;
-          if (elect_one()) mbar_arrive_expect_tx(full, live * a.piece * (rope ? 128 : 256));
-          __syncwarp();
-#pragma unroll 1
-          for (int p = 0; p < live; ++p) {
-            const int y = __shfl_sync(0xffffffffu, row, p);
-            if (elect_one()) {
-              uint8_t* d = dst + p * a.piece * 128;
-              if (rope) {
-                tma_load_2d(d, &tma_r, a.latent, y, full);
-              } else {
-                tma_load_3d(d, &tma_k, 0, y, 2 * s, full);   // both 64-column halves when the piece is a whole tile
-                if (pieces > 1) tma_load_3d(d + kTile * 128, &tma_k, 0, y, 2 * s + 1, full);
-              }
+          uint64_t* full = &c.latf[lr.slot];
+          uint8_t* dst = lat + lr.slot * slot_bytes;
+          uint8_t* rdst = ropes + rr.slot * kChunk;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(full, live * a.piece * 128 * (2 * a.um + (u == 0 ? 1 : 0)));
+            if (pieces == 1) {                           // one box for all chunks of the slot
+              tma_load_3d(dst, &tma_k, 0, y, 2 * a.um * u, full);
+              if (u == 0) tma_load_2d(rdst, &tma_r, a.latent, y, full);
             }
-            __syncwarp();
           }
-          if (rope) {
-            rr.step(a.nrope);
-            ++issued_rope;
-          } else {
-            lr.step(a.nlat);
-            ++issued_lat;
+          __syncwarp();
+          if (pieces > 1 && lane < live) {               // a box per piece and chunk
+#pragma unroll 1
+            for (int k = 0; k < 2 * a.um; ++k)
+              tma_load_3d(dst + k * kChunk + lane * a.piece * 128, &tma_k, 0, row, 2 * a.um * u + k, full);
+            if (u == 0) tma_load_2d(rdst + lane * a.piece * 128, &tma_r, a.latent, row, full);
           }
+          __syncwarp();
+          lr.step(a.nlat);
+          ++issued;
         }
+        rr.step(a.nrope);
         row = row_of(t + 1, page);
         page = page_of(t + 2);
       }
@@ -417,14 +411,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Every copy this CTA started has landed before its shared memory is released.
     if (lane == 0) {
 #pragma unroll 1
-      for (int i = 0, n = issued_lat < a.nlat ? issued_lat : a.nlat; i < n; ++i) {
+      for (int i = 0, n = issued < a.nlat ? issued : a.nlat; i < n; ++i) {
         if (--lr.slot < 0) { lr.slot = a.nlat - 1; lr.phase ^= 1u; }
         bar_wait(&c.latf[lr.slot], lr.phase, a.status, 64);
-      }
-#pragma unroll 1
-      for (int i = 0, n = issued_rope < a.nrope ? issued_rope : a.nrope; i < n; ++i) {
-        if (--rr.slot < 0) { rr.slot = a.nrope - 1; rr.phase ^= 1u; }
-        bar_wait(&c.ropef[rr.slot], rr.phase, a.status, 64);
       }
       if (issued_q > 0) bar_wait(&c.qf, qphase ^ 1u, a.status, 64);
     }
@@ -434,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // descriptors stay in uniform registers. That counts: an MMA of these sizes
     // takes 23 to 48 clocks, and issuing one from a divergent branch took 100.
     constexpr uint32_t idesc_s = idesc_bf16(64, N);
-    constexpr uint32_t kLatStep = kLatSlot >> 4, kRopeStep = kRopeSlot >> 4;   // descriptor address units
+    constexpr uint32_t kChunkStep = kChunk >> 4;          // descriptor address units
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + kSCol;
     const uint64_t dq0 = desc_kmajor_sw128(smem_u32(sq)), dl0 = desc_kmajor_sw128(smem_u32(lat));
     const uint64_t dr0 = desc_kmajor_sw128(smem_u32(ropes));
@@ -446,38 +435,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       qphase ^= 1u;
 #pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
-        ok = warp_wait(&c.se[sbuf], sphase ^ 1u, a.status, 73) && warp_wait(&c.ropef[rr.slot], rr.phase, a.status, 74);
-        if (!ok) break;
-        tc_fence_after();
+        ok = warp_wait(&c.se[sbuf], sphase ^ 1u, a.status, 73);
         const uint32_t d = tm + sbuf * N;
-        if (elect_one()) {
-          const uint64_t dr = dr0 + rr.slot * kRopeStep, dqr = dq0 + (nchunk - 1) * (N * 8);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, dr + kk * 2, dqr + kk * 2, idesc_s, kk != 0);
-          tc_commit(&c.ropee[rr.slot]);
-        }
-        __syncwarp();
-        rr.step(a.nrope);
 #pragma unroll 1
-        for (int m = 0; m < nm && ok; ++m) {
+        for (int u = 0; u < a.nu && ok; ++u) {
           ok = warp_wait(&c.latf[lr.slot], lr.phase, a.status, 75);
           tc_fence_after();
           if (ok && elect_one()) {
-            const uint64_t dl = dl0 + lr.slot * kLatStep, dqm = dq0 + m * (2 * N * 8);
+            if (u == 0) {
+              const uint64_t dr = dr0 + rr.slot * kChunkStep, dqr = dq0 + (nchunk - 1) * (N * 8);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc_mma_bf16(d, dl + (kk >> 2) * (kTile * 8) + (kk & 3) * 2, dqm + (kk >> 2) * (N * 8) + (kk & 3) * 2,
-                          idesc_s, 1);
+              for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, dr + kk * 2, dqr + kk * 2, idesc_s, kk != 0);
+              tc_commit(&c.ropee[rr.slot]);
+            }
+            uint64_t dl = dl0 + lr.slot * (a.um * 2 * kChunkStep), dqm = dq0 + u * a.um * (2 * N * 8);
+#pragma unroll 1
+            for (int m = 0; m < a.um; ++m, dl += 2 * kChunkStep, dqm += 2 * N * 8)
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_bf16(d, dl + (kk >> 2) * kChunkStep + (kk & 3) * 2, dqm + (kk >> 2) * (N * 8) + (kk & 3) * 2,
+                            idesc_s, 1);
+            if (u == a.nu - 1) {
+              tc_commit(&c.sf[sbuf]);
+              if (i == n - 1) tc_commit(&c.qe);
+            }
           }
           __syncwarp();
           lr.step(a.nlat);
         }
         if (!ok) break;
-        if (elect_one()) {
-          tc_commit(&c.sf[sbuf]);
-          if (i == n - 1) tc_commit(&c.qe);
-        }
-        __syncwarp();
+        rr.step(a.nrope);
         sbuf ^= 1;
         if (sbuf == 0) sphase ^= 1u;
       }
@@ -486,9 +473,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 6) {
     // Issues O^T, in a warp of its own: it then never waits behind the next tile's data.
     constexpr uint32_t idesc_o = idesc_bf16(128, N) | (1u << 15);   // A (V^T) is MN-major
-    constexpr uint32_t kLatStep = kLatSlot >> 4;
+    constexpr uint32_t kChunkStep = kChunk >> 4;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t dp0 = desc_kmajor_sw128(smem_u32(sp)), dv0 = smem_desc(smem_u32(lat), kTile * 128, 1024, 2);
+    const uint64_t dp0 = desc_kmajor_sw128(smem_u32(sp)), dv0 = smem_desc(smem_u32(lat), kChunk, 1024, 2);
     Ring lr;
     uint32_t pphase = 0, ophase = 0;
     while (ok && wk.next(a, started)) {
@@ -501,23 +488,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         pphase ^= 1u;
         tc_fence_after();
-#pragma unroll 1
-        for (int m = 0; m < nm; ++m) {
-          if (elect_one()) {
-            const uint64_t dv = dv0 + lr.slot * kLatStep;
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              tc_mma_bf16(tm + m * N, dv + kk * 128, dp0 + kk * 2, idesc_o, i > 0 || kk > 0);
-            tc_commit(&c.late[lr.slot]);
-          }
-          __syncwarp();
-          lr.step(a.nlat);
-        }
         if (elect_one()) {
+          uint32_t d = tm;
+          int slot = lr.slot;
+#pragma unroll 1
+          for (int u = 0; u < a.nu; ++u) {
+            uint64_t dv = dv0 + slot * (a.um * 2 * kChunkStep);
+#pragma unroll 1
+            for (int m = 0; m < a.um; ++m, dv += 2 * kChunkStep, d += N)
+#pragma unroll
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                tc_mma_bf16(d, dv + kk * 128, dp0 + kk * 2, idesc_o, i > 0 || kk > 0);
+            tc_commit(&c.late[slot]);
+            if (++slot == a.nlat) slot = 0;
+          }
           tc_commit(&c.pe);
           if (i == n - 1) tc_commit(&c.of);
         }
         __syncwarp();
+        for (int u = 0; u < a.nu; ++u) lr.step(a.nlat);
       }
       wk.done();
     }
@@ -661,19 +650,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           // Rows past the sequence's end hold whatever the page held (NaN included): their P is 0, and they
           // have to be 0 themselves for the product. Only a sequence's last tile is partial.
           Ring z = lr;
+          const int per = (kTile - valid) * 8;             // 16-byte words to clear in a chunk
 #pragma unroll 1
-          for (int m = 0; m < nm; ++m) {
+          for (int u = 0; u < a.nu; ++u) {
             wait(&c.latf[z.slot], z.phase, 82);
-            uint4* v = reinterpret_cast<uint4*>(lat + z.slot * kLatSlot);
+            uint4* v = reinterpret_cast<uint4*>(lat + z.slot * slot_bytes) + valid * 8;
 #pragma unroll 1
-            for (int i = st; i < 2 * (kTile - valid) * 8; i += 128) {
-              const int half = i / ((kTile - valid) * 8), k = i - half * ((kTile - valid) * 8);
-              v[half * kTile * 8 + valid * 8 + k] = make_uint4(0, 0, 0, 0);
-            }
+            for (int i = st; i < 2 * a.um * per; i += 128) v[i / per * (kChunk / 16) + i % per] = make_uint4(0, 0, 0, 0);
             z.step(a.nlat);
           }
         }
-        for (int m = 0; m < nm; ++m) lr.step(a.nlat);
+        for (int u = 0; u < a.nu; ++u) lr.step(a.nlat);
         fence_proxy_async();
         tc_fence_before();
         mbar_arrive(&c.pf);
@@ -926,12 +913,12 @@ __global__ void __launch_bounds__(256) mla_append_kernel(const __grid_constant__
 
 namespace {
 
-// The cache's latent columns as [latent / 64][rows][64]: a box is `piece` rows of one 64-column chunk, or of two
-// when the piece is a whole tile (a slot is two chunks of 64 rows).
-bool make_tmap_latent(CUtensorMap* m, const void* base, int64_t rows, const moe_mla_config_t* c, int piece) {
+// The cache's latent columns as [latent / 64][rows][64]: a box is `piece` rows of one 64-column chunk, or of all
+// `chunks` of a ring slot when the piece is a whole tile (a slot is that many chunks of 64 rows).
+bool make_tmap_latent(CUtensorMap* m, const void* base, int64_t rows, const moe_mla_config_t* c, int piece, int chunks) {
   const uint64_t pitch = static_cast<uint64_t>(c->latent + c->rope) * 2;
   return make_tmap_strided(m, base, {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(c->latent / 64)}, {pitch, 128},
-                           {64, static_cast<uint32_t>(piece), piece == kTile ? 2u : 1u}, 3);
+                           {64, static_cast<uint32_t>(piece), piece == kTile ? static_cast<uint32_t>(chunks) : 1u}, 3);
 }
 // Whole cache rows; the rope columns are one box of 64, zero past the row's end.
 bool make_tmap_rope(CUtensorMap* m, const void* base, int64_t rows, const moe_mla_config_t* c, int piece) {
@@ -986,9 +973,10 @@ int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CU
     return MOE_ERR_CUDA;
   const int fixed = 1024 + kBarBytes + (4 + 1) * kMaxHeadsCta * 4 + (2 * a.nm + 1) * N * 128 + N * 128;
   a.nrope = N <= 32 ? 3 : 2;
-  a.nlat = (kSmemMax - fixed - a.nrope * kRopeSlot) / kLatSlot;
+  const int slot_bytes = a.um * 2 * kChunk;
+  a.nlat = (kSmemMax - fixed - a.nrope * kChunk) / slot_bytes;
   if (a.nlat > kMaxLatSlots) a.nlat = kMaxLatSlots;
-  const int smem = fixed + a.nrope * kRopeSlot + a.nlat * kLatSlot;
+  const int smem = fixed + a.nrope * kChunk + a.nlat * slot_bytes;
   launch_kernel("mla_decode", mla_decode_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(kThreads), smem, s, tk, tr, tq,
                 a);
   return MOE_OK;
@@ -1079,6 +1067,8 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
   a.G = static_cast<int>(ceil_div(cfg->heads, kMaxHeadsCta));
   a.hg = static_cast<int>(ceil_div(cfg->heads, a.G));
   a.nm = cfg->latent / 128;
+  a.um = a.nm % 2 ? 1 : 2;
+  a.nu = a.nm / a.um;
   const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
   a.W = sms / a.G;
   a.piece = cfg->page_size & -cfg->page_size;
@@ -1097,7 +1087,7 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
   const int N = static_cast<int>(round_up(a.hg, 16));
   CUtensorMap tk, tr, tq;
   const int64_t rows = static_cast<int64_t>(cfg->num_pages) * cfg->page_size;
-  if (!make_tmap_latent(&tk, cache, rows, cfg, a.piece) || !make_tmap_rope(&tr, cache, rows, cfg, a.piece))
+  if (!make_tmap_latent(&tk, cache, rows, cfg, a.piece, 2 * a.um) || !make_tmap_rope(&tr, cache, rows, cfg, a.piece))
     return MOE_ERR_CUDA;
   if (!make_tmap_strided(&tq, q,
                          {static_cast<uint64_t>(row), static_cast<uint64_t>(cfg->heads), static_cast<uint64_t>(cfg->batch)},
