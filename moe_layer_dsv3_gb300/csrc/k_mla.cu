@@ -13,13 +13,12 @@
 // once per group of up to 64 heads, straight into the shared memory that both
 // products read.
 //
-// Both products run transposed, with cached tokens (then latent columns) as
-// the 128- or 64-row operand and the heads as the narrow one: a few heads then
-// cost little, and the output of 64 heads takes half of TMEM.
-//   S^T [64 tokens x N heads]   = K [64 x (latent + rope)] . Q [N x (latent + rope)]^T
-//   O^T [latent x N heads]     += V^T [latent x 64] . P [N x 64]^T,  V^T read from the
-//                                 same K tile as an MN-major operand
-// N = the group's heads, rounded up to 16.
+//   S [64 heads x 64 tokens]   = Q . K^T    (rows past the group's heads are not used)
+//   O^T [latent x N heads]    += V^T . P^T   (N = the group's heads, rounded up to 16)
+// The second product runs transposed, with latent columns as its 128-row
+// operand and the heads as the narrow one: the output of 64 heads then takes
+// half of TMEM, a few heads cost little, and V^T is the K tile itself, read as
+// an MN-major operand.
 //
 // Work is split by tiles of 64 tokens: the tiles of all sequences, one after
 // another, are cut into equal contiguous ranges, one per worker (CTA; with two
@@ -129,10 +128,16 @@ struct Walk {
 
 // TMEM loads. 16 lanes x 8 fp32 columns per step: register 4 i + {0, 1} is
 // (lane / 4, 8 i + 2 (lane % 4) + {0, 1}), register 4 i + {2, 3} the row 8 below.
-__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -150,11 +155,10 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Store four transposed 8 x 8 blocks of 16-bit values: lane l gives the address
-// of row l % 8 of block l / 8.
-__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1),
-               "r"(r2), "r"(r3)
+// Store four 8 x 8 blocks of 16-bit values: lane l gives the address of row l % 8 of block l / 8.
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2),
+               "r"(r3)
                : "memory");
 }
 
@@ -225,7 +229,7 @@ struct Smem {
   uint64_t latf[kMaxLatSlots], late[kMaxLatSlots];     // latent slots: filled / free
   uint64_t ropee[kMaxRopeSlots];                       // (a tile's rope columns arrive with its first latent slot)
   uint64_t qf, qe;                                      // Q of the piece: filled / free
-  uint64_t sf[2], se[2];                                // S^T buffers: products done / read
+  uint64_t sf[2], se[2];                                // S buffers: products done / read
   uint64_t pf, pe;                                      // P: written / its product done
   uint64_t of, oe;                                      // O: all products of the piece done / read
   uint32_t tmem;
@@ -236,7 +240,7 @@ static_assert(sizeof(Smem) <= kBarBytes, "control block");
 
 }  // namespace
 
-// Threads: warp 0 loads (TMA), warps 1 and 6 issue the MMAs of S^T and O^T, warps
+// Threads: warp 0 loads (TMA), warps 1 and 6 issue the MMAs of S and O^T, warps
 // 2-5 do the softmax and the epilogue (TMEM lane quarter warp % 4).
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -245,17 +249,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nm = a.nm, nchunk = 2 * nm + 1;            // 64-column chunks of a row: latent, then rope
-  uint8_t* lat = smem;
   const int slot_bytes = a.um * 2 * kChunk;
-  uint8_t* ropes = lat + a.nlat * slot_bytes;
-  uint8_t* sq = ropes + a.nrope * kChunk;           // [nchunk][N][128 bytes]
+  uint8_t* sq = smem;                                  // [nchunk][N][128 bytes]; the product's 64 rows of a chunk
+                                                       // run on into what follows when N is less
   uint8_t* sp = sq + nchunk * N * 128;                 // [N][128 bytes]: P, 64 tokens a head
-  Smem& c = *reinterpret_cast<Smem*>(sp + N * 128);
-  float* smax = reinterpret_cast<float*>(sp + N * 128 + kBarBytes);   // [4][64]
-  float* fac = smax + 4 * kMaxHeadsCta;                               // [64]
+  uint8_t* lat = sp + N * 128;
+  uint8_t* ropes = lat + a.nlat * slot_bytes;
+  Smem& c = *reinterpret_cast<Smem*>(ropes + a.nrope * kChunk);
+  float* fac = reinterpret_cast<float*>(ropes + a.nrope * kChunk + kBarBytes);   // [64] a factor per head
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = blockIdx.x % a.G, w = blockIdx.x / a.G;
-  constexpr int kSCol = 4 * N;                         // S^T buffers above O^T (latent / 128 <= 4 tiles of N columns)
+  constexpr int kSCol = 4 * N;                         // S buffers above O^T (latent / 128 <= 4 tiles of N columns)
 
   if (tid == 0) {
     for (int i = 0; i < a.nlat; ++i) {
@@ -418,11 +422,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (issued_q > 0) bar_wait(&c.qf, qphase ^ 1u, a.status, 64);
     }
   } else if (warp == 1) {
-    // Issues S^T. The whole warp walks the tiles and waits, and one elected lane
+    // Issues S. The whole warp walks the tiles and waits, and one elected lane
     // issues; with every wait's result and every length taken warp-wide, the
     // descriptors stay in uniform registers. That counts: an MMA of these sizes
     // takes 23 to 48 clocks, and issuing one from a divergent branch took 100.
-    constexpr uint32_t idesc_s = idesc_bf16(64, N);
+    constexpr uint32_t idesc_s = idesc_bf16(64, kTile);
     constexpr uint32_t kChunkStep = kChunk >> 4;          // descriptor address units
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + kSCol;
     const uint64_t dq0 = desc_kmajor_sw128(smem_u32(sq)), dl0 = desc_kmajor_sw128(smem_u32(lat));
@@ -436,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
         ok = warp_wait(&c.se[sbuf], sphase ^ 1u, a.status, 73);
-        const uint32_t d = tm + sbuf * N;
+        const uint32_t d = tm + sbuf * kTile;
 #pragma unroll 1
         for (int u = 0; u < a.nu && ok; ++u) {
           ok = warp_wait(&c.latf[lr.slot], lr.phase, a.status, 75);
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (u == 0) {
               const uint64_t dr = dr0 + rr.slot * kChunkStep, dqr = dq0 + (nchunk - 1) * (N * 8);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, dr + kk * 2, dqr + kk * 2, idesc_s, kk != 0);
+              for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, dqr + kk * 2, dr + kk * 2, idesc_s, kk != 0);
               tc_commit(&c.ropee[rr.slot]);
             }
             uint64_t dl = dl0 + lr.slot * (a.um * 2 * kChunkStep), dqm = dq0 + u * a.um * (2 * N * 8);
@@ -453,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int m = 0; m < a.um; ++m, dl += 2 * kChunkStep, dqm += 2 * N * 8)
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
-                tc_mma_bf16(d, dl + (kk >> 2) * kChunkStep + (kk & 3) * 2, dqm + (kk >> 2) * (N * 8) + (kk & 3) * 2,
+                tc_mma_bf16(d, dqm + (kk >> 2) * (N * 8) + (kk & 3) * 2, dl + (kk >> 2) * kChunkStep + (kk & 3) * 2,
                             idesc_s, 1);
             if (u == a.nu - 1) {
               tc_commit(&c.sf[sbuf]);
@@ -514,12 +518,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;
     const int st = tid - 64;                               // softmax thread
     const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
-    constexpr int NP = N / 8;                              // 8-head column blocks
     uint32_t pphase = 0, ophase = 0, sphase = 0;
     int sbuf = 0;
     Ring lr;                                               // latent ring position of the current tile
     const int head0 = g * a.hg;                            // first head of the group
     const int nh = a.H - head0 < a.hg ? a.H - head0 : a.hg;
+    const bool active = 16 * q < N;                        // this warp's 16 rows of S hold heads
+    const int hr = 16 * q + (lane >> 2);                   // this thread's heads: rows hr and hr + 8 of S
     bool any_tile = false;                                 // a product into O has been issued before this tile
     // After a wait that gave up, these threads stop waiting but keep walking: all 128 then
     // meet at every barrier, and the kernel ends.
@@ -527,90 +532,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ok = bar_wait(bar, parity, a.status, site);
     };
     while (wk.next(a, started)) {
-      // Heads 8 i + 2 (lane % 4) + e of this thread; rows q * 16 + lane / 4 and + 8 of a tile.
-      float ref[NP][2], l[NP][2], le[NP][2];
-#pragma unroll
-      for (int i = 0; i < NP; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          ref[i][e] = kNoRef;
-          l[i][e] = 0.0f;
-          le[i][e] = 0.0f;
-        }
+      float ref[2] = {kNoRef, kNoRef}, l[2] = {0.0f, 0.0f}, le[2] = {0.0f, 0.0f};
 #pragma unroll 1
       for (int ti = 0; ti < wk.n; ++ti) {
         const int valid = wk.len - (wk.t0 + ti) * kTile;   // tokens of the tile (>= 64: all)
         wait(&c.sf[sbuf], sphase, 80);
-        tc_fence_after();
-        uint32_t r[4 * NP];
+        // Register 4 i + 2 r + e: head hr + 8 r, token 8 i + 2 (lane % 4) + e.
+        float y[32], over = -INFINITY;
+        uint32_t x[32];
+        if (active) {
+          tc_fence_after();
+          tmem_ld_16x256b_x8(tmem + tlane + kSCol + sbuf * kTile, x);
+          tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < NP; i += 2) tmem_ld_16x256b_x2(tmem + tlane + kSCol + sbuf * N + 8 * i, r + 4 * i);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 4 * NP; ++i) reg_fence(r[i]);
-        tc_fence_before();
+          for (int i = 0; i < 32; ++i) reg_fence(x[i]);
+          tc_fence_before();
+        }
         mbar_arrive(&c.se[sbuf]);
         sbuf ^= 1;
         if (sbuf == 0) sphase ^= 1u;
-        if (valid < kTile) {
-          const int row = q * 16 + (lane >> 2);
+        if (active) {
+          if (valid < kTile) {
+            const int col = 2 * (lane & 3);
 #pragma unroll
-          for (int i = 0; i < 4 * NP; ++i)
-            if (row + 8 * ((i >> 1) & 1) >= valid) r[i] = __float_as_uint(-INFINITY);
-        }
-        // Scores above their head's reference, in powers of two. O is rescaled only when one of the tile
-        // passes kSlack, as in a piece's first tile.
-        float y[NP][4], over = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[i][e] = fmaf(__uint_as_float(r[4 * i + e]), a.scale2, -ref[i][e & 1]);
-            over = fmaxf(over, y[i][e]);
+            for (int i = 0; i < 32; ++i)
+              if (8 * (i >> 2) + col + (i & 1) >= valid) x[i] = __float_as_uint(-INFINITY);
           }
+          // Scores above their head's reference, in powers of two.
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            y[i] = fmaf(__uint_as_float(x[i]), a.scale2, -ref[(i >> 1) & 1]);
+            over = fmaxf(over, y[i]);
+          }
+        }
+        // O is rescaled only when a score of the tile passes kSlack, as in a piece's first tile.
         const bool grow = barrier_or(2, over > kSlack);
-        if (grow) {
+        if (grow && active) {
 #pragma unroll
-          for (int i = 0; i < NP; ++i)
+          for (int k = 0; k < 2; ++k) {
+            float m = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float m = fmaxf(__uint_as_float(r[4 * i + e]), __uint_as_float(r[4 * i + e + 2]));
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-              if (lane < 4) smax[q * kMaxHeadsCta + 8 * i + 2 * lane + e] = m * a.scale2;
-            }
-          named_barrier(3, 128);
-#pragma unroll
-          for (int i = 0; i < NP; ++i)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int h = 8 * i + 2 * (lane & 3) + e;
-              const float m = fmaxf(fmaxf(fmaxf(smax[h], smax[kMaxHeadsCta + h]),
-                                          fmaxf(smax[2 * kMaxHeadsCta + h], smax[3 * kMaxHeadsCta + h])),
-                                    ref[i][e]);
-              const float corr = ex2(ref[i][e] - m);       // 0 from kNoRef to a score
-              l[i][e] *= corr;
-              le[i][e] *= corr;
-              ref[i][e] = m;
-              if (q == 0 && lane < 4) fac[h] = corr;
-              y[i][e] = fmaf(__uint_as_float(r[4 * i + e]), a.scale2, -m);
-              y[i][e + 2] = fmaf(__uint_as_float(r[4 * i + e + 2]), a.scale2, -m);
-            }
-        }
-        uint32_t p[NP][2];
-#pragma unroll
-        for (int i = 0; i < NP; ++i) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[i][e] = ex2(y[i][e]);
-            le[i][e & 1] += y[i][e];
+            for (int i = 0; i < 8; ++i)
+              m = fmaxf(m, fmaxf(__uint_as_float(x[4 * i + 2 * k]), __uint_as_float(x[4 * i + 2 * k + 1])));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            m = fmaxf(m * a.scale2, ref[k]);
+            const float corr = ex2(ref[k] - m);            // 0 from kNoRef to a score
+            l[k] *= corr;
+            le[k] *= corr;
+            ref[k] = m;
+            if ((lane & 3) == 0) fac[hr + 8 * k] = corr;
           }
-          p[i][0] = pack_bf16x2(y[i][0], y[i][1]);
-          p[i][1] = pack_bf16x2(y[i][2], y[i][3]);
-          // P enters the product rounded to bf16; the same rounded values are summed for its normalisation
-          l[i][0] += __uint_as_float(p[i][0] << 16) + __uint_as_float(p[i][1] << 16);
-          l[i][1] += __uint_as_float(p[i][0] & 0xFFFF0000u) + __uint_as_float(p[i][1] & 0xFFFF0000u);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(x[i]), a.scale2, -ref[(i >> 1) & 1]);
+        }
+        if (active) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int k = i & 1;
+            y[2 * i] = ex2(y[2 * i]);
+            y[2 * i + 1] = ex2(y[2 * i + 1]);
+            le[k] += y[2 * i] + y[2 * i + 1];
+            x[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+            // P enters the product rounded to bf16; the same rounded values are summed for its normalisation
+            l[k] += __uint_as_float(x[i] << 16) + __uint_as_float(x[i] & 0xFFFF0000u);
+          }
         }
         // The previous tile's product is done: P is free and O stands still.
         if (any_tile) {
@@ -624,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
 #pragma unroll 1
             for (int m = 0; m < nm; ++m)
-#pragma unroll
+#pragma unroll 1
               for (int hc = 0; hc < N; hc += 16) {
                 uint32_t o[16];
                 const uint32_t at = tmem + tlane + m * N + hc;
@@ -640,11 +626,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
           }
         }
+        if (active) {
+          const int h = 16 * q + (lane & 15);              // lanes 0-7, 8-15: rows of the first two blocks; 16-31: the next token block
 #pragma unroll
-        for (int i = 0; i < NP; i += 2) {
-          const int h = 8 * (i + (lane >> 4)) + (lane & 7);
-          const int ch = 2 * q + ((lane >> 3) & 1);
-          stmatrix_x4_trans(smem_u32(sp) + h * 128 + ((ch ^ (h & 7)) << 4), p[i][0], p[i][1], p[i + 1][0], p[i + 1][1]);
+          for (int i = 0; i < 8; i += 2) {
+            const int ch = i + (lane >> 4);
+            stmatrix_x4(smem_u32(sp) + h * 128 + ((ch ^ (h & 7)) << 4), x[2 * i], x[2 * i + 1], x[2 * i + 2], x[2 * i + 3]);
+          }
         }
         if (valid < kTile) {
           // Rows past the sequence's end hold whatever the page held (NaN included): their P is 0, and they
@@ -666,49 +654,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&c.pf);
       }
       // ---- epilogue of the piece
-      // Sums over the tile rows: lanes with the same lane % 4, then the four warps.
-      float tot[2][NP][2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        named_barrier(3, 128);                             // smax is free
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float v = k ? le[i][e] : l[i][e];
-            v += __shfl_xor_sync(0xffffffffu, v, 4);
-            v += __shfl_xor_sync(0xffffffffu, v, 8);
-            v += __shfl_xor_sync(0xffffffffu, v, 16);
-            if (lane < 4) smax[q * kMaxHeadsCta + 8 * i + 2 * lane + e] = v;
-          }
-        named_barrier(3, 128);
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int h = 8 * i + 2 * (lane & 3) + e;
-            tot[k][i][e] = (smax[h] + smax[kMaxHeadsCta + h]) + (smax[2 * kMaxHeadsCta + h] + smax[3 * kMaxHeadsCta + h]);
-          }
-      }
       const bool whole = wk.n == wk.nt;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (wk.first ? 0 : 1);
-      if (q == 0 && lane < 4) {
+      named_barrier(3, 128);                               // fac is free
+      if (active) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int h = 8 * i + 2 * lane + e;
+        for (int k = 0; k < 2; ++k) {
+          // a head's sums lie in the four lanes of its row
+          float v = l[k], ve = le[k];
+          v += __shfl_xor_sync(0xffffffffu, v, 1);
+          ve += __shfl_xor_sync(0xffffffffu, ve, 1);
+          v += __shfl_xor_sync(0xffffffffu, v, 2);
+          ve += __shfl_xor_sync(0xffffffffu, ve, 2);
+          const int h = hr + 8 * k;
+          if ((lane & 3) == 0) {
             if (whole) {
-              fac[h] = tot[0][i][e] == 0.0f ? 0.0f : 1.0f / tot[0][i][e];
+              fac[h] = v == 0.0f ? 0.0f : 1.0f / v;
               if (a.lse != nullptr && h < nh)
-                a.lse[static_cast<int64_t>(wk.b) * a.H + head0 + h] =
-                    tot[1][i][e] == 0.0f ? -INFINITY : (ref[i][e] + log2f(tot[1][i][e])) * kLn2;
+                a.lse[static_cast<int64_t>(wk.b) * a.H + head0 + h] = ve == 0.0f ? -INFINITY : (ref[k] + log2f(ve)) * kLn2;
             } else {
-              a.part_m[slot * kMaxHeadsCta + h] = ref[i][e];
-              a.part_l[slot * kMaxHeadsCta + h] = tot[0][i][e];
-              a.part_e[slot * kMaxHeadsCta + h] = tot[1][i][e];
+              a.part_m[slot * kMaxHeadsCta + h] = ref[k];
+              a.part_l[slot * kMaxHeadsCta + h] = v;
+              a.part_e[slot * kMaxHeadsCta + h] = ve;
             }
           }
+        }
       }
       named_barrier(3, 128);
       wait(&c.of, ophase, 83);
@@ -971,7 +941,7 @@ int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CU
         return cudaFuncSetAttribute(mla_decode_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
       }))
     return MOE_ERR_CUDA;
-  const int fixed = 1024 + kBarBytes + (4 + 1) * kMaxHeadsCta * 4 + (2 * a.nm + 1) * N * 128 + N * 128;
+  const int fixed = 1024 + kBarBytes + kMaxHeadsCta * 4 + (2 * a.nm + 1) * N * 128 + N * 128;
   a.nrope = N <= 32 ? 3 : 2;
   const int slot_bytes = a.um * 2 * kChunk;
   a.nlat = (kSmemMax - fixed - a.nrope * kChunk) / slot_bytes;
