@@ -58,9 +58,12 @@ struct MlaArgs {
   int G, hg;                 // head groups, heads per group
   int nm, um, nu;            // latent / 128; 128-column tiles per ring slot; slots per token tile
   int nlat, nrope;           // ring slots: latent, rope
+  int nts;                   // 64-column chunks of Q held in TMEM; the others stay in shared memory
   int W;                     // workers per head group
   int piece;                 // tokens per TMA box: a power of two that divides the page
   float scale2;              // scale * log2(e)
+  const __nv_bfloat16* q;
+  int64_t q_b, q_h;          // strides of q, in elements
   const int32_t* table;
   const int32_t* lens;
   __nv_bfloat16* out;
@@ -171,6 +174,28 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int
       : "memory");
 }
 
+// D[tmem] (+)= A[tmem] x B[smem]^T for bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -228,7 +253,7 @@ struct Ring {
 struct Smem {
   uint64_t latf[kMaxLatSlots], late[kMaxLatSlots];     // latent slots: filled / free
   uint64_t ropee[kMaxRopeSlots];                       // (a tile's rope columns arrive with its first latent slot)
-  uint64_t qf, qe;                                      // Q of the piece: filled / free
+  uint64_t qf, qe;                                      // Q of the piece: filled (both parts) / free
   uint64_t sf[2], se[2];                                // S buffers: products done / read
   uint64_t pf, pe;                                      // P: written / its product done
   uint64_t of, oe;                                      // O: all products of the piece done / read
@@ -237,6 +262,19 @@ struct Smem {
   int start_b, start_t;
 };
 static_assert(sizeof(Smem) <= kBarBytes, "control block");
+
+// TMEM columns: O^T (a block of N per 128 latent columns), the S buffers, then as
+// many chunks of Q (32 columns each) as fit. Q in TMEM leaves shared memory to
+// the ring, and the product then reads only the cached rows from there. 64 heads
+// leave room for one S buffer: the next product waits until the last scores are
+// in registers, while the other product runs.
+template <int N>
+struct Plan {
+  static constexpr int kBufs = N > 48 ? 1 : 2;
+  static constexpr int kS = 4 * N;
+  static constexpr int kQ = kS + kBufs * kTile;
+  static constexpr int kMaxTs = (512 - kQ) / 32 < 9 ? (512 - kQ) / 32 : 9;
+};
 
 }  // namespace
 
@@ -250,16 +288,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nm = a.nm, nchunk = 2 * nm + 1;            // 64-column chunks of a row: latent, then rope
   const int slot_bytes = a.um * 2 * kChunk;
-  uint8_t* sq = smem;                                  // [nchunk][N][128 bytes]; the product's 64 rows of a chunk
+  const int nss = nchunk - a.nts;                      // chunks of Q in shared memory
+  uint8_t* sq = smem;                                  // [nss][N][128 bytes]; the product's 64 rows of a chunk
                                                        // run on into what follows when N is less
-  uint8_t* sp = sq + nchunk * N * 128;                 // [N][128 bytes]: P, 64 tokens a head
+  uint8_t* sp = sq + nss * N * 128;                 // [N][128 bytes]: P, 64 tokens a head
   uint8_t* lat = sp + N * 128;
   uint8_t* ropes = lat + a.nlat * slot_bytes;
   Smem& c = *reinterpret_cast<Smem*>(ropes + a.nrope * kChunk);
   float* fac = reinterpret_cast<float*>(ropes + a.nrope * kChunk + kBarBytes);   // [64] a factor per head
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = blockIdx.x % a.G, w = blockIdx.x / a.G;
-  constexpr int kSCol = 4 * N;                         // S buffers above O^T (latent / 128 <= 4 tiles of N columns)
+  using P = Plan<N>;
 
   if (tid == 0) {
     for (int i = 0; i < a.nlat; ++i) {
@@ -267,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c.late[i], 1);
     }
     for (int i = 0; i < a.nrope; ++i) mbar_init(&c.ropee[i], 1);
-    mbar_init(&c.qf, 1);
+    mbar_init(&c.qf, 129);
     mbar_init(&c.qe, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.sf[i], 1);
@@ -366,9 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = warp_wait(&c.qe, qphase ^ 1u, a.status, 61);
       if (!ok) break;
       if (elect_one()) {
-        mbar_arrive_expect_tx(&c.qf, nchunk * N * 128);
+        mbar_arrive_expect_tx(&c.qf, nss * N * 128);
 #pragma unroll 1
-        for (int k = 0; k < nchunk; ++k) tma_load_3d(sq + k * N * 128, &tma_q, k * 64, h0, b, &c.qf);
+        for (int k = 0; k < nss; ++k) tma_load_3d(sq + k * N * 128, &tma_q, (a.nts + k) * 64, h0, b, &c.qf);
       }
       __syncwarp();
       qphase ^= 1u;
@@ -428,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // takes 23 to 48 clocks, and issuing one from a divergent branch took 100.
     constexpr uint32_t idesc_s = idesc_bf16(64, kTile);
     constexpr uint32_t kChunkStep = kChunk >> 4;          // descriptor address units
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0) + kSCol;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dq0 = desc_kmajor_sw128(smem_u32(sq)), dl0 = desc_kmajor_sw128(smem_u32(lat));
     const uint64_t dr0 = desc_kmajor_sw128(smem_u32(ropes));
     Ring lr, rr;
@@ -440,25 +479,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
         ok = warp_wait(&c.se[sbuf], sphase ^ 1u, a.status, 73);
-        const uint32_t d = tm + sbuf * kTile;
+        const uint32_t d = tm + P::kS + sbuf * kTile;
 #pragma unroll 1
         for (int u = 0; u < a.nu && ok; ++u) {
           ok = warp_wait(&c.latf[lr.slot], lr.phase, a.status, 75);
           tc_fence_after();
           if (ok && elect_one()) {
-            if (u == 0) {
-              const uint64_t dr = dr0 + rr.slot * kChunkStep, dqr = dq0 + (nchunk - 1) * (N * 8);
+            // one chunk of 64 columns: A from TMEM or shared memory
+            auto chunk = [&](int k, uint64_t dk, bool fresh) {
+              if (k < a.nts) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, dqr + kk * 2, dr + kk * 2, idesc_s, kk != 0);
+                for (int kk = 0; kk < 4; ++kk) tc_mma_bf16_ts(d, tm + P::kQ + k * 32 + kk * 8, dk + kk * 2, idesc_s, !fresh || kk > 0);
+              } else {
+                const uint64_t dq = dq0 + (k - a.nts) * (N * 8);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, dq + kk * 2, dk + kk * 2, idesc_s, !fresh || kk > 0);
+              }
+            };
+            const uint64_t dl = dl0 + lr.slot * (a.um * 2 * kChunkStep);
+#pragma unroll 1
+            for (int k = 0; k < 2 * a.um; ++k) chunk(u * a.um * 2 + k, dl + k * kChunkStep, u + k == 0);
+            if (u == 0) {
+              chunk(nchunk - 1, dr0 + rr.slot * kChunkStep, false);
               tc_commit(&c.ropee[rr.slot]);
             }
-            uint64_t dl = dl0 + lr.slot * (a.um * 2 * kChunkStep), dqm = dq0 + u * a.um * (2 * N * 8);
-#pragma unroll 1
-            for (int m = 0; m < a.um; ++m, dl += 2 * kChunkStep, dqm += 2 * N * 8)
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc_mma_bf16(d, dqm + (kk >> 2) * (N * 8) + (kk & 3) * 2, dl + (kk >> 2) * kChunkStep + (kk & 3) * 2,
-                            idesc_s, 1);
             if (u == a.nu - 1) {
               tc_commit(&c.sf[sbuf]);
               if (i == n - 1) tc_commit(&c.qe);
@@ -469,8 +513,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         rr.step(a.nrope);
-        sbuf ^= 1;
-        if (sbuf == 0) sphase ^= 1u;
+        if (++sbuf == P::kBufs) {
+          sbuf = 0;
+          sphase ^= 1u;
+        }
       }
       wk.done();
     }
@@ -531,6 +577,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
       if (ok) ok = bar_wait(bar, parity, a.status, site);
     };
+    // Chunks of Q that the TMEM plan holds: row 16 q + lane of the quarter's lanes 0-15, two values a
+    // column. Lanes l and l + 16 load half a row of a chunk each; lane l stores it whole.
+    auto q_to_tmem = [&](int b) {
+      if (active) {
+        const int h = 16 * q + (lane & 15);
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + b * a.q_b + (head0 + h) * a.q_h) + (lane >> 4) * 4;
+        constexpr int kAtOnce = P::kMaxTs < 5 ? P::kMaxTs : 5;
+#pragma unroll 1
+        for (int k0 = 0; k0 < a.nts; k0 += kAtOnce) {
+          uint4 v[kAtOnce][4];
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              v[k][j] = k0 + k < a.nts && h < nh ? ld_global_u4(src + (k0 + k) * 8 + j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            if (k0 + k >= a.nts) break;
+            uint32_t r[32];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t w[4] = {v[k][j].x, v[k][j].y, v[k][j].z, v[k][j].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                r[4 * j + e] = w[e];
+                r[16 + 4 * j + e] = __shfl_xor_sync(0xffffffffu, w[e], 16);
+              }
+            }
+            tmem_st_32x32b_x32(tmem + tlane + P::kQ + (k0 + k) * 32, r);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      mbar_arrive(&c.qf);
+    };
+    // One piece ahead: its Q goes in as soon as the last scores of the piece before are done.
+    Walk nx = wk;
+    bool nx_started = false;
+    bool more = nx.next(a, nx_started);
+    if (more) q_to_tmem(nx.b);
     while (wk.next(a, started)) {
       float ref[2] = {kNoRef, kNoRef}, l[2] = {0.0f, 0.0f}, le[2] = {0.0f, 0.0f};
 #pragma unroll 1
@@ -542,15 +629,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t x[32];
         if (active) {
           tc_fence_after();
-          tmem_ld_16x256b_x8(tmem + tlane + kSCol + sbuf * kTile, x);
+          tmem_ld_16x256b_x8(tmem + tlane + P::kS + sbuf * kTile, x);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) reg_fence(x[i]);
           tc_fence_before();
         }
         mbar_arrive(&c.se[sbuf]);
-        sbuf ^= 1;
-        if (sbuf == 0) sphase ^= 1u;
+        if (++sbuf == P::kBufs) {
+          sbuf = 0;
+          sphase ^= 1u;
+        }
         if (active) {
           if (valid < kTile) {
             const int col = 2 * (lane & 3);
@@ -653,7 +742,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(&c.pf);
       }
-      // ---- epilogue of the piece
+      // ---- epilogue of the piece, after the next one's Q
+      nx.done();
+      if (more && (more = nx.next(a, nx_started))) q_to_tmem(nx.b);
       const bool whole = wk.n == wk.nt;
       const int slot = 2 * static_cast<int>(blockIdx.x) + (wk.first ? 0 : 1);
       named_barrier(3, 128);                               // fac is free
@@ -941,7 +1032,10 @@ int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CU
         return cudaFuncSetAttribute(mla_decode_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
       }))
     return MOE_ERR_CUDA;
-  const int fixed = 1024 + kBarBytes + kMaxHeadsCta * 4 + (2 * a.nm + 1) * N * 128 + N * 128;
+  const int nchunk = 2 * a.nm + 1;
+  // a row past 64 * nchunk columns does not exist: a rope part under 64 columns is zero-filled by its TMA box only
+  a.nts = Plan<N>::kMaxTs < nchunk - 1 ? Plan<N>::kMaxTs : (a.rope == 64 && Plan<N>::kMaxTs >= nchunk ? nchunk : nchunk - 1);
+  const int fixed = 1024 + kBarBytes + kMaxHeadsCta * 4 + (nchunk - a.nts) * N * 128 + N * 128;
   a.nrope = N <= 32 ? 3 : 2;
   const int slot_bytes = a.um * 2 * kChunk;
   a.nlat = (kSmemMax - fixed - a.nrope * kChunk) / slot_bytes;
@@ -1044,6 +1138,9 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
   a.piece = cfg->page_size & -cfg->page_size;
   if (a.piece > kTile) a.piece = kTile;
   a.scale2 = cfg->softmax_scale * kLog2e;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_b = q_stride_b;
+  a.q_h = q_stride_h;
   a.table = block_table;
   a.lens = seq_lens;
   a.out = static_cast<__nv_bfloat16*>(out);
