@@ -70,7 +70,7 @@ struct MlaArgs {
   float* lse;                // or null
   int* status;
   int4* join;                // [W]: per worker that ends a cut sequence {b, first slot, first worker, pieces}
-  float* part_o;             // [2 W G][64][latent]
+  float* part_o;             // [2 W G][64 * latent], in the register order of the epilogue
   float* part_m;             // [2 W G][64] reference (log2 units)
   float* part_l;             // [2 W G][64] sum of P as rounded for the product
   float* part_e;             // [2 W G][64] sum of P in fp32 (for the lse)
@@ -142,6 +142,11 @@ __device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t* r) 
         "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -162,6 +167,12 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2),
                "r"(r3)
+               : "memory");
+}
+// The same, each block transposed.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1),
+               "r"(r2), "r"(r3)
                : "memory");
 }
 
@@ -368,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   }
   __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;");       // the join's blocks may be placed; they wait for this grid's end
   const uint32_t tmem = c.tmem;
   Walk wk;
   wk.b = c.start_b;
@@ -620,13 +632,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (more) q_to_tmem(nx.b);
     while (wk.next(a, started)) {
       float ref[2] = {kNoRef, kNoRef}, l[2] = {0.0f, 0.0f}, le[2] = {0.0f, 0.0f};
+      // P of the scores x, packed to bf16, and its row sums (this thread's part): as rounded for the product,
+      // which normalise the output, and in fp32 for the lse. Returns the largest score above its head's
+      // reference, in powers of two.
+      auto take = [&](const uint32_t* x, uint32_t* p, float* ls, float* les) {
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float rs[4] = {}, es[4] = {};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float r = -ref[i & 1];
+          const float y0 = fmaf(__uint_as_float(x[2 * i]), a.scale2, r), y1 = fmaf(__uint_as_float(x[2 * i + 1]), a.scale2, r);
+          top[i & 3] = fmaxf(top[i & 3], fmaxf(y0, y1));
+          const float p0 = ex2(y0), p1 = ex2(y1);
+          es[i & 3] += p0 + p1;
+          p[i] = pack_bf16x2(p0, p1);
+          rs[i & 3] += __uint_as_float(p[i] << 16) + __uint_as_float(p[i] & 0xFFFF0000u);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          ls[k] = rs[k] + rs[k + 2];
+          les[k] = es[k] + es[k + 2];
+        }
+        return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      };
 #pragma unroll 1
       for (int ti = 0; ti < wk.n; ++ti) {
         const int valid = wk.len - (wk.t0 + ti) * kTile;   // tokens of the tile (>= 64: all)
         wait(&c.sf[sbuf], sphase, 80);
         // Register 4 i + 2 r + e: head hr + 8 r, token 8 i + 2 (lane % 4) + e.
-        float y[32], over = -INFINITY;
-        uint32_t x[32];
+        float over = -INFINITY, ls[2] = {0.0f, 0.0f}, les[2] = {0.0f, 0.0f};
+        uint32_t x[32], p[16];
         if (active) {
           tc_fence_after();
           tmem_ld_16x256b_x8(tmem + tlane + P::kS + sbuf * kTile, x);
@@ -647,14 +682,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i)
               if (8 * (i >> 2) + col + (i & 1) >= valid) x[i] = __float_as_uint(-INFINITY);
           }
-          // Scores above their head's reference, in powers of two.
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            y[i] = fmaf(__uint_as_float(x[i]), a.scale2, -ref[(i >> 1) & 1]);
-            over = fmaxf(over, y[i]);
-          }
+          over = take(x, p, ls, les);
         }
-        // O is rescaled only when a score of the tile passes kSlack, as in a piece's first tile.
+        // O is rescaled only when a score of the tile passes kSlack, as in a piece's first tile; P above
+        // (formed before the warps meet here) is then formed again.
         const bool grow = barrier_or(2, over > kSlack);
         if (grow && active) {
 #pragma unroll
@@ -672,20 +703,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             ref[k] = m;
             if ((lane & 3) == 0) fac[hr + 8 * k] = corr;
           }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(x[i]), a.scale2, -ref[(i >> 1) & 1]);
+          take(x, p, ls, les);
         }
-        if (active) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int k = i & 1;
-            y[2 * i] = ex2(y[2 * i]);
-            y[2 * i + 1] = ex2(y[2 * i + 1]);
-            le[k] += y[2 * i] + y[2 * i + 1];
-            x[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
-            // P enters the product rounded to bf16; the same rounded values are summed for its normalisation
-            l[k] += __uint_as_float(x[i] << 16) + __uint_as_float(x[i] & 0xFFFF0000u);
-          }
+        for (int k = 0; k < 2; ++k) {
+          l[k] += ls[k];
+          le[k] += les[k];
         }
         // The previous tile's product is done: P is free and O stands still.
         if (any_tile) {
@@ -720,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             const int ch = i + (lane >> 4);
-            stmatrix_x4(smem_u32(sp) + h * 128 + ((ch ^ (h & 7)) << 4), x[2 * i], x[2 * i + 1], x[2 * i + 2], x[2 * i + 3]);
+            stmatrix_x4(smem_u32(sp) + h * 128 + ((ch ^ (h & 7)) << 4), p[2 * i], p[2 * i + 1], p[2 * i + 2], p[2 * i + 3]);
           }
         }
         if (valid < kTile) {
@@ -775,45 +798,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait(&c.of, ophase, 83);
       ophase ^= 1u;
       tc_fence_after();
-      if (whole) {
-        __nv_bfloat16* out = a.out + (static_cast<int64_t>(wk.b) * a.H + head0) * a.latent;
+      // O^T in blocks of 16 latent columns: register 4 i + 2 r + e is column lane / 4 + 8 r, head 8 i + 2 (lane % 4) + e.
+      constexpr int NP = N / 8;
+      float2 f[NP];
+      if (whole)
+#pragma unroll
+        for (int i = 0; i < NP; ++i) f[i] = reinterpret_cast<const float2*>(fac)[4 * i + (lane & 3)];
+      uint8_t* stage = sp + q * (N * 32);                  // [N heads][16 columns] of this warp, over P
+      __nv_bfloat16* out = a.out + (static_cast<int64_t>(wk.b) * a.H + head0) * a.latent;
+      float4* part = reinterpret_cast<float4*>(a.part_o + static_cast<int64_t>(slot) * kMaxHeadsCta * a.latent) + q * 32 + lane;
 #pragma unroll 1
-        for (int m = 0; m < nm; ++m) {
-          const int dv = m * 128 + q * 32 + lane;
+      for (int mh = 0; mh < 2 * nm; ++mh) {
+        uint32_t o[4 * NP];
 #pragma unroll
-          for (int hc = 0; hc < N; hc += 16) {
-            uint32_t o[16];
-            tmem_ld_32x32b_x16(tmem + tlane + m * N + hc, o);
-            tmem_wait_ld();
+        for (int i = 0; i < NP; i += 2)
+          tmem_ld_16x256b_x2(tmem + tlane + (static_cast<uint32_t>(mh & 1) << 20) + (mh >> 1) * N + 8 * i, o + 4 * i);
+        tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              reg_fence(o[j]);
-              reg_fence(o[j + 1]);
-              const float v0 = __uint_as_float(o[j]) * fac[hc + j], v1 = __uint_as_float(o[j + 1]) * fac[hc + j + 1];
-              // neighbouring lanes swap, so that each stores two columns of one head
-              const float got = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v0 : v1, 1);
-              const int h = hc + j + (lane & 1);
-              const uint32_t pk = (lane & 1) ? pack_bf16x2(got, v1) : pack_bf16x2(v0, got);
-              if (h < nh) *reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(h) * a.latent + (dv & ~1)) = pk;
-            }
+        for (int i = 0; i < 4 * NP; ++i) reg_fence(o[i]);
+        if (whole) {
+          // Normalised, rounded and turned through shared memory: two lanes then store 32 bytes of a head.
+#pragma unroll
+          for (int i = 0; i < NP; i += 2) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = pack_bf16x2(__uint_as_float(o[4 * i + 2 * k]) * f[i + (k >> 1)].x,
+                                 __uint_as_float(o[4 * i + 2 * k + 1]) * f[i + (k >> 1)].y);
+            const int h = 8 * (i + (lane >> 4)) + (lane & 7);
+            stmatrix_x4_trans(smem_u32(stage) + h * 32 + ((((lane >> 3) ^ (h >> 2)) & 1) << 4), w[0], w[1], w[2], w[3]);
           }
-        }
-      } else {
-        float* out = a.part_o + static_cast<int64_t>(slot) * kMaxHeadsCta * a.latent;
-#pragma unroll 1
-        for (int m = 0; m < nm; ++m) {
-          const int dv = m * 128 + q * 32 + lane;
+          __syncwarp();
 #pragma unroll
-          for (int hc = 0; hc < N; hc += 16) {
-            uint32_t o[16];
-            tmem_ld_32x32b_x16(tmem + tlane + m * N + hc, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              reg_fence(o[j]);
-              if (hc + j < nh) out[(hc + j) * a.latent + dv] = __uint_as_float(o[j]);
-            }
+          for (int k = 0; k < N / 16; ++k) {
+            const int h = 16 * k + (lane >> 1), ch = lane & 1;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + h * 32 + (((ch ^ (h >> 2)) & 1) << 4));
+            if (h < nh)
+              *reinterpret_cast<uint4*>(out + h * a.latent + (mh >> 1) * 128 + q * 32 + (mh & 1) * 16 + ch * 8) = v;
           }
+          __syncwarp();
+        } else {
+          // A partial keeps this register order: every store is 512 bytes in a row.
+#pragma unroll
+          for (int i = 0; i < NP; ++i)
+            part[(mh * NP + i) * 128] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                    __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
       }
       tc_fence_before();
@@ -855,36 +884,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the pieces of the sequences that the work split cut: block (w, head),
-// for the sequence that worker w ended. Pieces are added in order. Latent /4
-// threads, four columns each.
-__global__ void mla_join_kernel(const __grid_constant__ MlaArgs a) {
-  const int4 j = a.join[blockIdx.x];
+// Joins the pieces of the sequences that the work split cut, in their order.
+// Block (worker and head group, 8 heads and 128 latent columns) for the sequence
+// that the worker ended; a warp takes 32 columns, in the register order in which
+// the pieces were stored. Each block reads few bytes, so that many loads are in
+// flight and a long list of pieces costs a few rounds of latency.
+template <int N>
+__global__ void __launch_bounds__(128) mla_join_kernel(const __grid_constant__ MlaArgs a) {
+  constexpr int NP = N / 8;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the decode kernel's writes are visible
+  const int w = blockIdx.x / a.G, g = blockIdx.x - w * a.G;
+  const int4 j = a.join[w];
   if (j.w == 0) return;
-  const int head = blockIdx.y, g = head / a.hg, h = head - g * a.hg;
-  auto slot_of = [&](int i) { return 2 * ((j.z + i) * a.G + g) + (i == 0 ? j.y : 0); };
-  float m = -INFINITY;
-  for (int i = 0; i < j.w; ++i) m = fmaxf(m, a.part_m[slot_of(i) * kMaxHeadsCta + h]);
-  const float mr = m == -INFINITY ? 0.0f : m;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float l = 0.0f, le = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < j.w; ++i) {
-    const int at = slot_of(i) * kMaxHeadsCta + h;
-    const float f = ex2(a.part_m[at] - mr);
-    const float4 v = reinterpret_cast<const float4*>(a.part_o + static_cast<int64_t>(at) * a.latent)[threadIdx.x];
-    l = fmaf(f, a.part_l[at], l);
-    le = fmaf(f, a.part_e[at], le);
-    o.x = fmaf(f, v.x, o.x);
-    o.y = fmaf(f, v.y, o.y);
-    o.z = fmaf(f, v.z, o.z);
-    o.w = fmaf(f, v.w, o.w);
+  const int i = blockIdx.y % NP, m = blockIdx.y / NP, q = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = 8 * i + 2 * (lane & 3);                     // this thread's heads h, h + 1 of the group
+  auto slot_of = [&](int k) { return 2 * ((j.z + k) * a.G + g) + (k == 0 ? j.y : 0); };
+  auto pair = [&](const float* v, int k) { return *reinterpret_cast<const float2*>(v + slot_of(k) * kMaxHeadsCta + h); };
+  float2 top = make_float2(kNoRef, kNoRef);
+#pragma unroll 8
+  for (int k = 0; k < j.w; ++k) {
+    const float2 v = pair(a.part_m, k);
+    top = make_float2(fmaxf(top.x, v.x), fmaxf(top.y, v.y));
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t row = static_cast<int64_t>(j.x) * a.H + head;
-  *reinterpret_cast<uint2*>(a.out + row * a.latent + threadIdx.x * 4) =
-      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (a.lse != nullptr && threadIdx.x == 0) a.lse[row] = le == 0.0f ? -INFINITY : (mr + log2f(le)) * kLn2;
+  const float4* o = reinterpret_cast<const float4*>(a.part_o) + (2 * m * NP + i) * 128 + threadIdx.x;
+  float4 s0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s1 = s0;
+  float2 l = make_float2(0.0f, 0.0f), le = l;
+#pragma unroll 8
+  for (int k = 0; k < j.w; ++k) {
+    const float2 mk = pair(a.part_m, k), lk = pair(a.part_l, k), ek = pair(a.part_e, k);
+    const float4* p = o + static_cast<int64_t>(slot_of(k)) * (kMaxHeadsCta / 4) * a.latent;
+    const float4 v0 = p[0], v1 = p[NP * 128];
+    const float fx = ex2(mk.x - top.x), fy = ex2(mk.y - top.y);
+    l = make_float2(fmaf(fx, lk.x, l.x), fmaf(fy, lk.y, l.y));
+    le = make_float2(fmaf(fx, ek.x, le.x), fmaf(fy, ek.y, le.y));
+    s0 = make_float4(fmaf(fx, v0.x, s0.x), fmaf(fy, v0.y, s0.y), fmaf(fx, v0.z, s0.z), fmaf(fy, v0.w, s0.w));
+    s1 = make_float4(fmaf(fx, v1.x, s1.x), fmaf(fy, v1.y, s1.y), fmaf(fx, v1.z, s1.z), fmaf(fy, v1.w, s1.w));
+  }
+  const float ix = l.x == 0.0f ? 0.0f : 1.0f / l.x, iy = l.y == 0.0f ? 0.0f : 1.0f / l.y;
+  const int head0 = g * a.hg, nh = a.H - head0 < a.hg ? a.H - head0 : a.hg;
+  const int64_t row = static_cast<int64_t>(j.x) * a.H + head0 + h;
+  if (a.lse != nullptr && m == 0 && threadIdx.x < 4) {
+    if (h < nh) a.lse[row] = le.x == 0.0f ? -INFINITY : (top.x + log2f(le.x)) * kLn2;
+    if (h + 1 < nh) a.lse[row + 1] = le.y == 0.0f ? -INFINITY : (top.y + log2f(le.y)) * kLn2;
+  }
+  // Columns c + 8 k of head h (x) and h + 1 (y). Lanes of neighbouring columns swap: the even one
+  // then stores two columns of head h, the odd one of head h + 1.
+  const float x[4] = {s0.x * ix, s0.z * ix, s1.x * ix, s1.z * ix}, y[4] = {s0.y * iy, s0.w * iy, s1.y * iy, s1.w * iy};
+  const int odd = (lane >> 2) & 1;
+  __nv_bfloat16* out = a.out + (row + odd) * a.latent + m * 128 + q * 32 + ((lane >> 2) & ~1);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? x[k] : y[k], 4);
+    const uint32_t v = odd ? pack_bf16x2(got, y[k]) : pack_bf16x2(x[k], got);
+    if (h + odd < nh) *reinterpret_cast<uint32_t*>(out + 8 * k) = v;
+  }
 }
 
 // New tokens into the cache: one warp a token. The latent part is normalised
@@ -1043,6 +1096,10 @@ int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CU
   const int smem = fixed + a.nrope * kChunk + a.nlat * slot_bytes;
   launch_kernel("mla_decode", mla_decode_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(kThreads), smem, s, tk, tr, tq,
                 a);
+  if (int e = call_error() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA) return e;
+  // The join's blocks start while the last decode CTAs run and wait for their writes on the device.
+  launch_kernel_after("mla_join", mla_join_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G), static_cast<unsigned>(N / 8 * a.nm)),
+                      dim3(128), 0, s, a);
   return MOE_OK;
 }
 
@@ -1170,9 +1227,6 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
     default: r = run_decode<64>(a, tk, tr, tq, s); break;
   }
   if (r) return r;
-  if (int e = call.status()) return e;
-  launch_kernel("mla_join", mla_join_kernel, dim3(static_cast<unsigned>(a.W), static_cast<unsigned>(a.H)),
-                dim3(static_cast<unsigned>(a.latent / 4)), 0, s, a);
   return call.status();
 }
 

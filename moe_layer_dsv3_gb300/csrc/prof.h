@@ -38,4 +38,23 @@ inline void launch_kernel(const char* name, void (*kern)(Kp...), dim3 grid, dim3
   note(cudaLaunchKernelEx(&lc, kern, std::forward<Ar>(args)...));
 }
 
+// The same, for a kernel that orders itself after the stream's previous kernel
+// with griddepcontrol.wait: it may be placed while that one still runs.
+template <typename... Kp, typename... Ar>
+inline void launch_kernel_after(const char* name, void (*kern)(Kp...), dim3 grid, dim3 block, size_t smem,
+                                cudaStream_t s, Ar&&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = block;
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  Prof prof(name, s);
+  note(cudaLaunchKernelEx(&lc, kern, std::forward<Ar>(args)...));
+}
+
 }  // namespace moe
