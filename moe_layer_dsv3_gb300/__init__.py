@@ -122,7 +122,8 @@ def _check(name: str, rc: int) -> None:
 
 
 def _p(x):
-    return None if x is None or x == 0 else ctypes.c_void_p(int(x))
+    # an int: ctypes turns it into the pointer argument itself, without an object per argument
+    return None if x is None or x == 0 else int(x)
 
 
 MOE_FLAG_LAP_LAUNCHES = 1   # one mover launch + one GEMM launch per ring lap instead of one launch for all laps

@@ -36,7 +36,7 @@ class LatentAttention:
     def append(self, kv, cache, block_table, seq, pos, gamma=None, eps=1e-6, cos_sin=None, stream=0):
         """Write tokens kv [n][latent + rope] (rows may be pitched) at positions pos of sequences seq into the cache."""
         n, row = seq.numel(), self.latent + self.rope
-        if not kv.is_cuda or kv.dtype != torch.bfloat16 or tuple(kv.shape) != (n, row) or (n and kv.stride(1) != 1):
+        if not kv.is_cuda or kv.dtype is not torch.bfloat16 or kv.shape != (n, row) or (n and kv.stride(1) != 1):
             raise MoeError("kv: a CUDA bfloat16 tensor of shape (n, %d) with dense rows is wanted" % row,
                            MOE_ERR_INVALID_ARG)
         self._check_cache(cache, block_table)
@@ -57,7 +57,7 @@ class LatentAttention:
         out = self.out if out is None else out
         lse = self.lse if lse is None else lse
         row = self.latent + self.rope
-        if not q.is_cuda or q.dtype != torch.bfloat16 or tuple(q.shape) != (self.batch, self.heads, row) or \
+        if not q.is_cuda or q.dtype is not torch.bfloat16 or q.shape != (self.batch, self.heads, row) or \
                 (q.numel() and q.stride(2) != 1):
             raise MoeError("q: a CUDA bfloat16 tensor of shape %s with dense rows is wanted" %
                            ((self.batch, self.heads, row),), MOE_ERR_INVALID_ARG)

@@ -42,6 +42,7 @@ constexpr int kMaxHeadsCta = 64;          // heads per CTA
 constexpr int kChunk = kTile * 128;       // 64 columns of a tile: [64 tokens][128 bytes]
 constexpr int kMaxLatSlots = 12;
 constexpr int kMaxRopeSlots = 3;
+constexpr int kMinTiles = 3;
 constexpr int kBarBytes = 512;
 constexpr int kSmemMax = 232448;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -60,7 +61,8 @@ struct MlaArgs {
   int nlat, nrope;           // ring slots: latent, rope
   int nts;                   // 64-column chunks of Q held in TMEM; the others stay in shared memory
   int W;                     // workers per head group
-  int piece;                 // tokens per TMA box: a power of two that divides the page
+  int piece;                 // tokens per TMA box: a whole tile, or 8 where a page can end inside a tile
+  int chunk_step, row8_step; // bytes from one 64-column chunk of a slot to the next, and from 8 tokens to the next 8
   float scale2;              // scale * log2(e)
   const __nv_bfloat16* q;
   int64_t q_b, q_h;          // strides of q, in elements
@@ -106,6 +108,7 @@ __device__ __forceinline__ int owner_of(int total, int t, int W) {
 struct Walk {
   int b, t, left;            // next sequence, its next tile, tiles left in the range
   int len, nt;               // current piece's sequence: tokens, tiles
+  int ahead;                 // tokens of sequence b (read a piece early)
   int t0, n;                 // current piece: first tile, tiles
   bool first;                // the worker's first piece
   __device__ __forceinline__ bool next(const MlaArgs& a, bool& started) {
@@ -113,7 +116,8 @@ struct Walk {
 #pragma unroll 1
     while (true) {
       if (b >= a.B) return false;
-      len = seq_len(a, b, false);
+      len = ahead;
+      ahead = b + 1 < a.B ? seq_len(a, b + 1, false) : 0;
       nt = tiles_of(len);
       if (t < nt) break;
       ++b;
@@ -270,7 +274,7 @@ struct Smem {
   uint64_t of, oe;                                      // O: all products of the piece done / read
   uint32_t tmem;
   int scan[kThreads / 32];
-  int start_b, start_t;
+  int start_b, start_t, start_len;
 };
 static_assert(sizeof(Smem) <= kBarBytes, "control block");
 
@@ -337,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&c.tmem, 512);
     tmem_relinquish();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // inputs and workspace of the stream's earlier kernels
   // Range of this worker: prefix sums of the sequences' tiles, a run of
   // sequences per thread, then the thread whose run holds the first tile finds it.
   const int per = (a.B + kThreads - 1) / kThreads;
@@ -361,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (i < warp) before += c.scan[i];
     total += c.scan[i];
   }
-  const int W = a.W < total ? a.W : (total > 0 ? total : 1);   // workers that get tiles
+  const int most = (total + kMinTiles - 1) / kMinTiles;       // workers that get tiles
+  const int W = a.W < most ? a.W : (most > 0 ? most : 1);
   const int f0 = w < W ? range_begin(total, w, W) : total;
   const int f1 = w < W ? range_begin(total, w + 1, W) : total;
   {
@@ -369,10 +375,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (f0 >= at && f0 < at + mine)
 #pragma unroll 1
       for (int b = b0; b < b1; ++b) {
-        const int n = tiles_of(seq_len(a, b, false));
+        const int len = seq_len(a, b, false), n = tiles_of(len);
         if (f0 < at + n) {
           c.start_b = b;
           c.start_t = f0 - at;
+          c.start_len = len;
           break;
         }
         at += n;
@@ -384,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk wk;
   wk.b = c.start_b;
   wk.t = c.start_t;
+  wk.ahead = c.start_len;
   wk.left = f1 - f0;
   bool started = false, ok = true;
 
@@ -439,19 +447,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint64_t* full = &c.latf[lr.slot];
           uint8_t* dst = lat + lr.slot * slot_bytes;
           uint8_t* rdst = ropes + rr.slot * kChunk;
+          // A box holds all chunks of the slot for the tokens of one piece.
           if (elect_one()) {
             mbar_arrive_expect_tx(full, live * a.piece * 128 * (2 * a.um + (u == 0 ? 1 : 0)));
-            if (pieces == 1) {                           // one box for all chunks of the slot
+            if (pieces == 1) {
               tma_load_3d(dst, &tma_k, 0, y, 2 * a.um * u, full);
               if (u == 0) tma_load_2d(rdst, &tma_r, a.latent, y, full);
             }
           }
           __syncwarp();
-          if (pieces > 1 && lane < live) {               // a box per piece and chunk
-#pragma unroll 1
-            for (int k = 0; k < 2 * a.um; ++k)
-              tma_load_3d(dst + k * kChunk + lane * a.piece * 128, &tma_k, 0, row, 2 * a.um * u + k, full);
-            if (u == 0) tma_load_2d(rdst + lane * a.piece * 128, &tma_r, a.latent, row, full);
+          if (pieces > 1 && lane < live) {
+            tma_load_3d(dst + lane * a.row8_step, &tma_k, 0, row, 2 * a.um * u, full);
+            if (u == 0) tma_load_2d(rdst + lane * 1024, &tma_r, a.latent, row, full);
           }
           __syncwarp();
           lr.step(a.nlat);
@@ -480,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_s = idesc_bf16(64, kTile);
     constexpr uint32_t kChunkStep = kChunk >> 4;          // descriptor address units
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t dq0 = desc_kmajor_sw128(smem_u32(sq)), dl0 = desc_kmajor_sw128(smem_u32(lat));
+    const uint64_t dq0 = desc_kmajor_sw128(smem_u32(sq)), dl0 = smem_desc(smem_u32(lat), 16, a.row8_step, 2);
     const uint64_t dr0 = desc_kmajor_sw128(smem_u32(ropes));
     Ring lr, rr;
     uint32_t qphase = 0, sbuf = 0, sphase = 0;
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             const uint64_t dl = dl0 + lr.slot * (a.um * 2 * kChunkStep);
 #pragma unroll 1
-            for (int k = 0; k < 2 * a.um; ++k) chunk(u * a.um * 2 + k, dl + k * kChunkStep, u + k == 0);
+            for (int k = 0; k < 2 * a.um; ++k) chunk(u * a.um * 2 + k, dl + k * (a.chunk_step >> 4), u + k == 0);
             if (u == 0) {
               chunk(nchunk - 1, dr0 + rr.slot * kChunkStep, false);
               tc_commit(&c.ropee[rr.slot]);
@@ -537,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_o = idesc_bf16(128, N) | (1u << 15);   // A (V^T) is MN-major
     constexpr uint32_t kChunkStep = kChunk >> 4;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t dp0 = desc_kmajor_sw128(smem_u32(sp)), dv0 = smem_desc(smem_u32(lat), kChunk, 1024, 2);
+    const uint64_t dp0 = desc_kmajor_sw128(smem_u32(sp)), dv0 = smem_desc(smem_u32(lat), a.chunk_step, a.row8_step, 2);
     Ring lr;
     uint32_t pphase = 0, ophase = 0;
     while (ok && wk.next(a, started)) {
@@ -557,10 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < a.nu; ++u) {
             uint64_t dv = dv0 + slot * (a.um * 2 * kChunkStep);
 #pragma unroll 1
-            for (int m = 0; m < a.um; ++m, dv += 2 * kChunkStep, d += N)
+            for (int m = 0; m < a.um; ++m, dv += a.chunk_step >> 3, d += N)
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk)
-                tc_mma_bf16(d, dv + kk * 128, dp0 + kk * 2, idesc_o, i > 0 || kk > 0);
+                tc_mma_bf16(d, dv + kk * (a.row8_step >> 3), dp0 + kk * 2, idesc_o, i > 0 || kk > 0);
             tc_commit(&c.late[slot]);
             if (++slot == a.nlat) slot = 0;
           }
@@ -754,9 +761,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int u = 0; u < a.nu; ++u) {
             wait(&c.latf[z.slot], z.phase, 82);
-            uint4* v = reinterpret_cast<uint4*>(lat + z.slot * slot_bytes) + valid * 8;
+            uint8_t* v = lat + z.slot * slot_bytes;
 #pragma unroll 1
-            for (int i = st; i < 2 * a.um * per; i += 128) v[i / per * (kChunk / 16) + i % per] = make_uint4(0, 0, 0, 0);
+            for (int i = st; i < 2 * a.um * per; i += 128) {
+              const int k = i / per, r = valid + (i - k * per) / 8;
+              *reinterpret_cast<uint4*>(v + k * a.chunk_step + (r >> 3) * a.row8_step + (r & 7) * 128 + (i & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
             z.step(a.nlat);
           }
         }
@@ -854,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int4 j = make_int4(0, 0, 0, 0);
       if (f1 > f0) {
         // The first piece of the range is the only one that can end a sequence begun by another worker.
-        const int n0 = tiles_of(seq_len(a, c.start_b, false));
+        const int n0 = tiles_of(c.start_len);
         const int s0 = f0 - c.start_t;                     // the sequence's first tile in the common count
         if (c.start_t > 0 && s0 + n0 <= f1) {
           const int w0 = owner_of(total, s0, W);
@@ -956,10 +967,12 @@ struct AppendArgs {
   int* status;
 };
 
-__global__ void __launch_bounds__(256) mla_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(256, 6) mla_append_kernel(const __grid_constant__ AppendArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (i >= a.n) return;
+  const int p = __ldg(a.pos + i), b = __ldg(a.seq + i);
   const __nv_bfloat16* src = a.kv + i * a.ld;
   const int nlat = a.latent >> 3, nrope = a.rope >> 3;
   // the row's loads do not wait for its place
@@ -968,7 +981,6 @@ __global__ void __launch_bounds__(256) mla_append_kernel(const __grid_constant__
   for (int k = 0; k < 2; ++k)
     c[k] = lane + 32 * k < nlat ? ld_global_u4(src + (lane + 32 * k) * 8) : make_uint4(0, 0, 0, 0);
   if (lane < nrope) u = ld_global_u4(src + a.latent + lane * 8);
-  const int p = a.pos[i], b = a.seq[i];
   if (p < 0) return;                                       // padding
   if (b < 0 || b >= a.B || p >= static_cast<int64_t>(a.max_pages) * a.page ||
       (a.cos_sin != nullptr && p >= a.max_pos)) {
@@ -1027,12 +1039,11 @@ __global__ void __launch_bounds__(256) mla_append_kernel(const __grid_constant__
 
 namespace {
 
-// The cache's latent columns as [latent / 64][rows][64]: a box is `piece` rows of one 64-column chunk, or of all
-// `chunks` of a ring slot when the piece is a whole tile (a slot is that many chunks of 64 rows).
+// The cache's latent columns as [latent / 64][rows][64]: a box is `piece` rows of the `chunks` chunks of a ring slot.
 bool make_tmap_latent(CUtensorMap* m, const void* base, int64_t rows, const moe_mla_config_t* c, int piece, int chunks) {
   const uint64_t pitch = static_cast<uint64_t>(c->latent + c->rope) * 2;
   return make_tmap_strided(m, base, {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(c->latent / 64)}, {pitch, 128},
-                           {64, static_cast<uint32_t>(piece), piece == kTile ? static_cast<uint32_t>(chunks) : 1u}, 3);
+                           {64, static_cast<uint32_t>(piece), static_cast<uint32_t>(chunks)}, 3);
 }
 // Whole cache rows; the rope columns are one box of 64, zero past the row's end.
 bool make_tmap_rope(CUtensorMap* m, const void* base, int64_t rows, const moe_mla_config_t* c, int piece) {
@@ -1094,7 +1105,7 @@ int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CU
   a.nlat = (kSmemMax - fixed - a.nrope * kChunk) / slot_bytes;
   if (a.nlat > kMaxLatSlots) a.nlat = kMaxLatSlots;
   const int smem = fixed + a.nrope * kChunk + a.nlat * slot_bytes;
-  launch_kernel("mla_decode", mla_decode_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(kThreads), smem, s, tk, tr, tq,
+  launch_kernel_after("mla_decode", mla_decode_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(kThreads), smem, s, tk, tr, tq,
                 a);
   if (int e = call_error() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA) return e;
   // The join's blocks start while the last decode CTAs run and wait for their writes on the device.
@@ -1152,7 +1163,7 @@ extern "C" int moe_mla_append(const moe_mla_config_t* cfg, int n, const void* kv
   a.table = block_table;
   a.cache = static_cast<__nv_bfloat16*>(cache);
   a.status = reinterpret_cast<int*>(static_cast<char*>(ws) + mla_layout(cfg).status);
-  launch_kernel("mla_append", mla_append_kernel, dim3(static_cast<unsigned>(ceil_div(n, 8))), dim3(256), 0,
+  launch_kernel_after("mla_append", mla_append_kernel, dim3(static_cast<unsigned>(ceil_div(n, 8))), dim3(256), 0,
                 static_cast<cudaStream_t>(stream), a);
   return call.status();
 }
@@ -1192,8 +1203,11 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
   a.nu = a.nm / a.um;
   const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
   a.W = sms / a.G;
-  a.piece = cfg->page_size & -cfg->page_size;
-  if (a.piece > kTile) a.piece = kTile;
+  // Pages of whole tiles: one box a slot, chunk after chunk. Otherwise boxes of 8 tokens, which every page holds
+  // whole, each with its chunks side by side: the products' operands only need a fixed step from 8 rows to the next.
+  a.piece = cfg->page_size % kTile ? 8 : kTile;
+  a.chunk_step = a.piece * 128;
+  a.row8_step = a.piece == kTile ? 1024 : 2 * a.um * 1024;
   a.scale2 = cfg->softmax_scale * kLog2e;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_b = q_stride_b;

@@ -64,6 +64,7 @@ __global__ void add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
   const int nt = kWarpRow ? 32 : blockDim.x;
   const int i0 = kWarpRow ? (threadIdx.x & 31) : threadIdx.x;
   const int64_t row = kWarpRow ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= a.rows) return;   // whole warp, or whole CTA
   const int nvec = a.d >> 3;
   const int64_t base = row * a.d;
@@ -203,6 +204,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_bwd_kernel(const __grid_consta
     }
     cp_async_commit();
   };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   uint4 ug[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -257,6 +259,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_bwd_kernel(const __grid_consta
   }
   cp_async_wait<0>();
   float* out = a.part + static_cast<int64_t>(blockIdx.x) * a.d;
+  asm volatile("griddepcontrol.launch_dependents;");         // norm_dgamma may be placed; it waits for this grid's end
   if constexpr (kWarpRow) {
     __syncthreads();   // the stages are free: the warps' sums meet there
     float* sums = reinterpret_cast<float*>(smem);
@@ -291,6 +294,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_bwd_kernel(const __grid_consta
 // 32 threads a column.
 __global__ void __launch_bounds__(1024) norm_dgamma_kernel(const float* __restrict__ part, int n, int d,
                                                           float* __restrict__ dgamma) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the partial sums are visible
   __shared__ float s[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;
   float v = 0.0f;
@@ -329,7 +333,7 @@ int norm_bwd_ctas(int T, int d, int sms) {
 template <int V, bool kWarpRow>
 void fwd(const NormArgs& a, cudaStream_t s) {
   const int threads = kWarpRow ? 32 * kWarpsPerCta : static_cast<int>(round_up(ceil_div(a.d / 8, V), 32));
-  launch_kernel("add_rmsnorm", add_rmsnorm_kernel<V, kWarpRow>,
+  launch_kernel_after("add_rmsnorm", add_rmsnorm_kernel<V, kWarpRow>,
                 dim3(static_cast<unsigned>(ceil_div(a.rows, kWarpRow ? kWarpsPerCta : 1))), dim3(threads), 0, s, a);
 }
 
@@ -345,7 +349,7 @@ void bwd(const NormBwdArgs& a, int ctas, cudaStream_t s) {
     note(cudaErrorUnknown);
     return;
   }
-  launch_kernel("rmsnorm_bwd", rmsnorm_bwd_kernel<V, kWarpRow, S>, dim3(static_cast<unsigned>(ctas)), dim3(threads), smem,
+  launch_kernel_after("rmsnorm_bwd", rmsnorm_bwd_kernel<V, kWarpRow, S>, dim3(static_cast<unsigned>(ctas)), dim3(threads), smem,
                 s, a);
 }
 
@@ -434,7 +438,7 @@ extern "C" int moe_add_rmsnorm_backward(int T, int d, const void* dy, const void
   else if (d <= kWarpRowMax) bwd<4, true, 4>(a, ctas, s);
   else if (d <= 8192) bwd<2, false, 4>(a, ctas, s);
   else bwd<4, false, 2>(a, ctas, s);
-  launch_kernel("norm_dgamma", norm_dgamma_kernel, dim3(static_cast<unsigned>(ceil_div(d, 32))), dim3(32, 32), 0, s,
+  launch_kernel_after("norm_dgamma", norm_dgamma_kernel, dim3(static_cast<unsigned>(ceil_div(d, 32))), dim3(32, 32), 0, s,
                 static_cast<const float*>(a.part), ctas, d, dgamma);
   return call.status();
 }

@@ -13,7 +13,7 @@ from . import (MOE_ERR_INVALID_ARG, MoeError, moe_add_rmsnorm, moe_add_rmsnorm_b
 
 def check_tensor(name, t, dtype, shape):
     """A dense CUDA tensor of this type and shape, or MOE_ERR_INVALID_ARG (the library sees only an address)."""
-    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if not t.is_cuda or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise MoeError("%s: a dense CUDA %s tensor of shape %s is wanted" % (name, dtype, tuple(shape)),
                        MOE_ERR_INVALID_ARG)
 
