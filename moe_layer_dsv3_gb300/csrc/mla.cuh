@@ -1,0 +1,373 @@
+// What the latent-attention kernels share: arguments, the split of the work,
+// TMEM and barrier helpers, and the join of cut sequences.
+#pragma once
+#include <cudaTypedefs.h>
+
+#include "gemm.cuh"
+#include "prof.h"
+
+namespace moe {
+namespace mla {
+
+constexpr int kBlock = 64;                // cached tokens a CTA holds of a tile
+constexpr int kMaxHeadsCta = 64;          // heads per CTA
+constexpr int kChunk = kBlock * 128;      // 64 columns of a block: [64 tokens][128 bytes]
+constexpr int kBarBytes = 512;
+constexpr int kSmemMax = 232448;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// A tile's scores may exceed the running reference by this many powers of two
+// before O is rescaled: P and the sums stay far inside fp32 and bf16 range, and
+// their relative precision does not depend on the reference.
+constexpr float kSlack = 10.0f;
+// Reference of a head that has met no score above it: any such score is far past kSlack, and P of -inf is 0.
+constexpr float kNoRef = -3.0e38f;
+
+struct MlaArgs {
+  int B, H, latent, rope, page, num_pages, max_pages;
+  int G, hg;                 // head groups, heads per group
+  int nm, um, nu;            // latent / 128; 128-column tiles per ring slot; slots per token tile
+  int nlat, nrope;           // ring slots: latent, rope
+  int nts;                   // 64-column chunks of Q held in TMEM; the others stay in shared memory
+  int W;                     // workers per head group
+  int piece;                 // tokens per TMA box: a whole tile, or 8 where a page can end inside a tile
+  int chunk_step, row8_step; // bytes from one 64-column chunk of a slot to the next, and from 8 tokens to the next 8
+  float scale2;              // scale * log2(e)
+  const __nv_bfloat16* q;
+  int64_t q_b, q_h;          // strides of q, in elements
+  const int32_t* table;
+  const int32_t* lens;
+  __nv_bfloat16* out;
+  float* lse;                // or null
+  int* status;
+  int4* join;                // [W]: per worker that ends a cut sequence {b, first slot, first worker, pieces}
+  // Pieces of cut sequences, two per CTA:
+  float* part_o;             // [64 * latent] unnormalised output, in the register order of the epilogue
+  float* part_m;             // [64] reference (log2 units)
+  float* part_l;             // [64] sum of P as rounded for the product
+  float* part_e;             // [64] sum of P in fp32 (for the lse)
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Valid cached tokens of sequence b: lengths outside [0, capacity] are clamped (and reported once).
+__device__ __forceinline__ int seq_len(const MlaArgs& a, int b, bool report) {
+  const int n = __ldg(a.lens + b);
+  const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page;
+  if (n < 0 || n > cap) {
+    if (report) report_error(a.status, kErrBounds, 60);
+    return n < 0 ? 0 : static_cast<int>(cap);
+  }
+  return n;
+}
+template <int TILE>
+__device__ __forceinline__ int tiles_of(int len) { return (len + TILE - 1) / TILE; }
+
+// Range of tiles of worker w of W over `total` tiles, and the worker that owns tile t.
+__device__ __forceinline__ int range_begin(int total, int w, int W) {
+  return static_cast<int>(static_cast<int64_t>(total) * w / W);
+}
+__device__ __forceinline__ int owner_of(int total, int t, int W) {
+  return static_cast<int>((static_cast<int64_t>(t + 1) * W - 1) / total);
+}
+
+// Work of one worker: contiguous pieces of sequences, walked the same way by every role.
+template <int TILE>
+struct Walk {
+  int b, t, left;            // next sequence, its next tile, tiles left in the range
+  int len, nt;               // current piece's sequence: tokens, tiles
+  int ahead;                 // tokens of sequence b (read a piece early)
+  int t0, n;                 // current piece: first tile, tiles
+  bool first;                // the worker's first piece
+  __device__ __forceinline__ bool next(const MlaArgs& a, bool& started) {
+    if (left <= 0) return false;
+#pragma unroll 1
+    while (true) {
+      if (b >= a.B) return false;
+      len = ahead;
+      ahead = b + 1 < a.B ? seq_len(a, b + 1, false) : 0;
+      nt = tiles_of<TILE>(len);
+      if (t < nt) break;
+      ++b;
+      t = 0;
+    }
+    first = !started;
+    started = true;
+    t0 = t;
+    n = left < nt - t ? left : nt - t;
+    left -= n;
+    return true;
+  }
+  __device__ __forceinline__ void done() { ++b; t = 0; }
+};
+
+// TMEM loads. 16 lanes x 8 fp32 columns per step: register 4 i + {0, 1} is
+// (lane / 4, 8 i + 2 (lane % 4) + {0, 1}), register 4 i + {2, 3} the row 8 below.
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+        "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Store four 8 x 8 blocks of 16-bit values: lane l gives the address of row l % 8 of block l / 8.
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1), "r"(r2),
+               "r"(r3)
+               : "memory");
+}
+// The same, each block transposed.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0), "r"(r1),
+               "r"(r2), "r"(r3)
+               : "memory");
+}
+
+// 3-D tiled load (q: columns, heads, sequences).
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] x B[smem]^T for bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// mbar_wait in few instructions. Seven warps run five different loops here, and
+// with mbar_wait's unrolled polls at every wait the kernel was 150 KB of code:
+// its instruction-cache misses set the pace of every warp.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int* status, int site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity))
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      report_error(status, kErrTimeout, site);
+      return false;
+    }
+  return true;
+}
+
+// bar_wait by a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int site) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, status, site));
+}
+
+// Barrier over the 128 softmax threads that also gives the OR of their flags.
+__device__ __forceinline__ bool barrier_or(int id, bool flag) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(flag)), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// Ring position: slot index and the parity of its current use.
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step(int n) {
+    if (++slot == n) { slot = 0; phase ^= 1u; }
+  }
+};
+
+// This worker's range of the tiles of all sequences, laid end to end: prefix sums
+// with a run of sequences per thread, then the thread whose run holds the first
+// tile finds it. Called by all NT threads; ends with a __syncthreads.
+struct Range {
+  int total, W, f0, f1;      // all tiles, workers that get tiles, this worker's [f0, f1)
+};
+template <int NT, int TILE, int MIN_TILES, typename Control>
+__device__ __forceinline__ Range find_range(const MlaArgs& a, Control& c, int w, bool report) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (a.B + NT - 1) / NT;
+  const int b0 = tid * per < a.B ? tid * per : a.B;
+  const int b1 = b0 + per < a.B ? b0 + per : a.B;
+  int mine = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) mine += tiles_of<TILE>(seq_len(a, b, report));
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) c.scan[warp] = incl;
+  __syncthreads();
+  Range r;
+  int before = 0;
+  r.total = 0;
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) {
+    if (i < warp) before += c.scan[i];
+    r.total += c.scan[i];
+  }
+  // Each worker that gets tiles gets MIN_TILES or more (a piece costs a join), unless there are fewer.
+  const int most = (r.total + MIN_TILES - 1) / MIN_TILES;
+  r.W = a.W < most ? a.W : (most > 0 ? most : 1);
+  r.f0 = w < r.W ? range_begin(r.total, w, r.W) : r.total;
+  r.f1 = w < r.W ? range_begin(r.total, w + 1, r.W) : r.total;
+  int at = before + incl - mine;
+  if (r.f0 >= at && r.f0 < at + mine)
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const int len = seq_len(a, b, false), n = tiles_of<TILE>(len);
+      if (r.f0 < at + n) {
+        c.start_b = b;
+        c.start_t = r.f0 - at;
+        c.start_len = len;
+        break;
+      }
+      at += n;
+    }
+  __syncthreads();
+  return r;
+}
+
+// The worker that ends a cut sequence names its pieces for the join: {b, first slot, first worker, pieces}.
+// Only its first piece can end a sequence that another worker began.
+template <int TILE, typename Control>
+__device__ __forceinline__ int4 join_entry(const Control& c, const Range& r, int w) {
+  if (r.f1 <= r.f0 || c.start_t == 0) return make_int4(0, 0, 0, 0);
+  const int s0 = r.f0 - c.start_t;                         // the sequence's first tile in the common count
+  if (s0 + tiles_of<TILE>(c.start_len) > r.f1) return make_int4(0, 0, 0, 0);
+  const int w0 = owner_of(r.total, s0, r.W);
+  // it opened w0's range, or came after another piece there
+  return make_int4(c.start_b, range_begin(r.total, w0, r.W) == s0 ? 0 : 1, w0, w - w0 + 1);
+}
+
+// Joins the pieces of the sequences that the work split cut, in their order.
+// Block (worker and its CTA, 8 heads and 128 latent columns) for the sequence that
+// the worker ended; a warp takes 32 columns, in the register order in which the
+// pieces were stored. Each block reads few bytes, so that many loads are in
+// flight and a long list of pieces costs a few rounds of latency.
+// A worker is one CTA of a head group with all latent columns, or (PAIR) a pair of
+// CTAs, each with all heads and half of the columns.
+template <int N, bool PAIR>
+__global__ void __launch_bounds__(128) mla_join_kernel(const __grid_constant__ MlaArgs a) {
+  constexpr int NP = N / 8, kHeads = PAIR ? 2 * kMaxHeadsCta : kMaxHeadsCta;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the decode kernel's writes are visible
+  const int per = PAIR ? 2 : a.G;
+  const int w = blockIdx.x / per, g = blockIdx.x - w * per;
+  const int4 j = a.join[w];
+  if (j.w == 0) return;
+  const int i = blockIdx.y % NP, m = blockIdx.y / NP, q = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = 8 * i + 2 * (lane & 3);                     // this thread's heads h, h + 1 of the piece
+  auto slot_of = [&](int k) { return PAIR ? 2 * (j.z + k) + (k == 0 ? j.y : 0) : 2 * ((j.z + k) * a.G + g) + (k == 0 ? j.y : 0); };
+  auto pair = [&](const float* v, int k) { return *reinterpret_cast<const float2*>(v + slot_of(k) * kHeads + h); };
+  float2 top = make_float2(kNoRef, kNoRef);
+#pragma unroll 8
+  for (int k = 0; k < j.w; ++k) {
+    const float2 v = pair(a.part_m, k);
+    top = make_float2(fmaxf(top.x, v.x), fmaxf(top.y, v.y));
+  }
+  const float4* o = reinterpret_cast<const float4*>(a.part_o) + (2 * m * NP + i) * 128 + threadIdx.x;
+  float4 s0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s1 = s0;
+  float2 l = make_float2(0.0f, 0.0f), le = l;
+#pragma unroll 8
+  for (int k = 0; k < j.w; ++k) {
+    const float2 mk = pair(a.part_m, k), lk = pair(a.part_l, k), ek = pair(a.part_e, k);
+    const int64_t at = PAIR ? 2 * slot_of(k) + g : slot_of(k);
+    const float4* p = o + at * (kMaxHeadsCta / 4) * a.latent;
+    const float4 v0 = p[0], v1 = p[NP * 128];
+    const float fx = ex2(mk.x - top.x), fy = ex2(mk.y - top.y);
+    l = make_float2(fmaf(fx, lk.x, l.x), fmaf(fy, lk.y, l.y));
+    le = make_float2(fmaf(fx, ek.x, le.x), fmaf(fy, ek.y, le.y));
+    s0 = make_float4(fmaf(fx, v0.x, s0.x), fmaf(fy, v0.y, s0.y), fmaf(fx, v0.z, s0.z), fmaf(fy, v0.w, s0.w));
+    s1 = make_float4(fmaf(fx, v1.x, s1.x), fmaf(fy, v1.y, s1.y), fmaf(fx, v1.z, s1.z), fmaf(fy, v1.w, s1.w));
+  }
+  const float ix = l.x == 0.0f ? 0.0f : 1.0f / l.x, iy = l.y == 0.0f ? 0.0f : 1.0f / l.y;
+  const int grp = PAIR ? h >> 6 : g, hl = PAIR ? h & 63 : h;
+  const int head0 = grp * a.hg, nh = a.H - head0 < a.hg ? a.H - head0 : a.hg;
+  const int64_t row = static_cast<int64_t>(j.x) * a.H + head0 + hl;
+  if (a.lse != nullptr && m == 0 && threadIdx.x < 4 && (!PAIR || g == 0)) {
+    if (hl < nh) a.lse[row] = le.x == 0.0f ? -INFINITY : (top.x + log2f(le.x)) * kLn2;
+    if (hl + 1 < nh) a.lse[row + 1] = le.y == 0.0f ? -INFINITY : (top.y + log2f(le.y)) * kLn2;
+  }
+  // Columns c + 8 k of head h (x) and h + 1 (y). Lanes of neighbouring columns swap: the even one
+  // then stores two columns of head h, the odd one of head h + 1.
+  const float x[4] = {s0.x * ix, s0.z * ix, s1.x * ix, s1.z * ix}, y[4] = {s0.y * iy, s0.w * iy, s1.y * iy, s1.w * iy};
+  const int odd = (lane >> 2) & 1;
+  __nv_bfloat16* out =
+      a.out + (row + odd) * a.latent + (PAIR ? g * (a.latent / 2) : 0) + m * 128 + q * 32 + ((lane >> 2) & ~1);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? x[k] : y[k], 4);
+    const uint32_t v = odd ? pack_bf16x2(got, y[k]) : pack_bf16x2(x[k], got);
+    if (hl + odd < nh) *reinterpret_cast<uint32_t*>(out + 8 * k) = v;
+  }
+}
+
+// Decode with both head groups on one pair of CTAs (more than 64 heads, an even number of 128-column tiles), and
+// its condition. The maps' boxes hold half of a row's latent columns.
+bool pair_form(int heads, int latent);
+int run_decode_pair(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CUtensorMap& tq, int sms, cudaStream_t s);
+
+}  // namespace mla
+}  // namespace moe
