@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // O is rescaled only when a score of the tile passes kSlack, as in a piece's first tile; P above
         // (formed before the warps meet here) is then formed again.
-        const bool grow = barrier_or(2, over > kSlack);
+        const bool grow = barrier_or<128>(2, over > kSlack);
         if (grow && active) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -755,7 +755,8 @@ MlaLayout mla_layout(const moe_mla_config_t* c) {
 }
 
 template <int N>
-int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CUtensorMap& tq, cudaStream_t s) {
+int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CUtensorMap& tq, int sms,
+               cudaStream_t s) {
   static DevOnce once;
   if (!once.ready([] {
         return cudaFuncSetAttribute(mla_decode_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
@@ -773,9 +774,7 @@ int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CU
   launch_kernel_after("mla_decode", mla_decode_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(kThreads), smem, s, tk, tr, tq,
                 a);
   if (int e = call_error() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA) return e;
-  // The join's blocks start while the last decode CTAs run and wait for their writes on the device.
-  launch_kernel_after("mla_join", mla_join_kernel<N, false>, dim3(static_cast<unsigned>(a.W * a.G), static_cast<unsigned>(N / 8 * a.nm)),
-                      dim3(128), 0, s, a);
+  launch_join<N, false>(a, sms, s);
   return MOE_OK;
 }
 
@@ -906,10 +905,10 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
   }
   int r;
   switch (N) {
-    case 16: r = run_decode<16>(a, tk, tr, tq, s); break;
-    case 32: r = run_decode<32>(a, tk, tr, tq, s); break;
-    case 48: r = run_decode<48>(a, tk, tr, tq, s); break;
-    default: r = run_decode<64>(a, tk, tr, tq, s); break;
+    case 16: r = run_decode<16>(a, tk, tr, tq, sms, s); break;
+    case 32: r = run_decode<32>(a, tk, tr, tq, sms, s); break;
+    case 48: r = run_decode<48>(a, tk, tr, tq, sms, s); break;
+    default: r = run_decode<64>(a, tk, tr, tq, sms, s); break;
   }
   if (r) return r;
   return call.status();

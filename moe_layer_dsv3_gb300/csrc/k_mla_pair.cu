@@ -27,7 +27,8 @@ using namespace mla;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kSoft = 256;                 // softmax threads: eight warps, two per TMEM lane quarter
 constexpr int kTile = 2 * kBlock;          // cached tokens per tile, a block per CTA
 constexpr int kSlots = 5;                  // ring slots of half a row's latent columns: 2.5 tiles. A slot's barrier is
                                            // waited on within two tiles of its use, which this bound ensures
@@ -35,12 +36,12 @@ constexpr int kRopeSlots = 2;
 constexpr int kMinTiles = 2;
 constexpr int kS = 256, kQ = kS + 64;      // TMEM: O^T (128 columns per 128 of this CTA's latent ones), S, chunks of Q
 constexpr int kMaxTs = (512 - kQ) / 32;
-constexpr int kFloats = 5 * 128;           // fac, inv, and three arrays of 128 partial values
+constexpr int kFloats = 2 * 128 + 3 * kSoft;   // fac, inv, and a maximum and two sums of each softmax thread
 
 struct Smem {
   uint64_t full[kSlots], empty[kSlots];    // slots: both CTAs' data landed (even CTA) / product done
   uint64_t ropee[kRopeSlots];
-  uint64_t qf, qe;                         // Q of the piece: filled (even CTA) / free
+  uint64_t qf, qe;                         // Q in shared memory: filled (even CTA) / free
   uint64_t sf, sd[2], se;                  // S: done, for the softmax and (by tile parity) the reload / read (even CTA)
   uint64_t vl[2];                          // reload landed, by tile parity
   uint64_t pf, pe;                         // P and reload ready (even CTA) / product done
@@ -79,10 +80,6 @@ __device__ __forceinline__ void st_async(uint32_t addr, uint32_t v, uint32_t bar
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
 // Tiled loads into this CTA whose bytes count on a barrier of either CTA.
 __device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
   asm volatile(
@@ -90,6 +87,12 @@ __device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* m, in
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
+}
+
+// 64 rows of 16 bytes to four TMEM columns, in both CTAs, each from its own shared memory: rows 0-31 to lanes 0-31
+// and 64-95, rows 32-63 to lanes 32-63 and 96-127, as the pair instruction reads its 64 rows of A.
+__device__ __forceinline__ void tc_cp_rows64(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.64x128b.warpx2::02_13 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
 __device__ __forceinline__ void mma2_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -113,8 +116,8 @@ __device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a, uint64_t b, uint
 
 }  // namespace
 
-// Warps: 0 loads for the first product, 7 reloads for the second; 1 and 6 (even CTA)
-// issue the first and second products; 2-5 softmax and epilogue.
+// Warps: 0 loads for the first product, 11 reloads for the second; 1 and 10 (even CTA)
+// issue the first and second products; 2-9 softmax and epilogue.
 __global__ void __launch_bounds__(kThreads, 1)
     mla_decode_pair_kernel(const __grid_constant__ CUtensorMap tma_k, const __grid_constant__ CUtensorMap tma_r,
                            const __grid_constant__ CUtensorMap tma_q, const __grid_constant__ MlaArgs a) {
@@ -125,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nchunk = 2 * hc + 1;
   const int nss = nchunk - a.nts;
   const int slot_bytes = hc * kChunk;
+  const int nq = (a.nts + hc - 1) / hc;                // ring slots that a piece's TMEM chunks of Q pass through
   uint8_t* sq = smem;                                  // [nss][64 heads][128 bytes]
   uint8_t* sp = sq + nss * kChunk;                     // [2 token blocks][64 heads][128 bytes]: P
   uint8_t* lat = sp + 2 * kChunk;
@@ -132,9 +136,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem& c = *reinterpret_cast<Smem*>(ropes + kRopeSlots * kChunk);
   float* fac = reinterpret_cast<float*>(ropes + kRopeSlots * kChunk + kBarBytes);   // [128 heads] factors of a rescale
   float* inv = fac + 128;                              // [128 heads] 1 / sum
-  float* xm = inv + 128;                               // [128 threads] maxima, sums (rounded, fp32)
-  float* xl = xm + 128;
-  float* xe = xl + 128;
+  float* xm = inv + 128;                               // [softmax threads] maxima, sums (rounded, fp32)
+  float* xl = xm + kSoft;
+  float* xe = xl + kSoft;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = pair::cta_rank();
   const int w = static_cast<int>(pair::cluster_id());
@@ -145,14 +149,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c.empty[i], 1);
     }
     for (int i = 0; i < kRopeSlots; ++i) mbar_init(&c.ropee[i], 1);
-    mbar_init(&c.qf, 9);
+    mbar_init(&c.qf, 1);
     mbar_init(&c.qe, 1);
     mbar_init(&c.sf, 1);
-    mbar_init(&c.se, 8);
-    mbar_init(&c.pf, 8);
+    mbar_init(&c.se, 16);
+    mbar_init(&c.pf, 16);
     mbar_init(&c.pe, 1);
     mbar_init(&c.of, 1);
-    mbar_init(&c.oe, 8);
+    mbar_init(&c.oe, 16);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.sd[i], 1);
       mbar_init(&c.vl[i], 1);
@@ -204,25 +208,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     Ring lr, rr;
-    uint32_t qphase = 0;
-    int issued = 0, issued_q = 0;
-    const uint32_t full0 = pair::map_rank(smem_u32(c.full), 0), qf0 = pair::map_rank(smem_u32(&c.qf), 0);
+    int issued = 0;
+    const uint32_t full0 = pair::map_rank(smem_u32(c.full), 0);
     while (ok && wk.next(a, started)) {
       const int b = __shfl_sync(0xffffffffu, wk.b, 0), len = __shfl_sync(0xffffffffu, wk.len, 0);
       const int t0 = __shfl_sync(0xffffffffu, wk.t0, 0), t1 = t0 + __shfl_sync(0xffffffffu, wk.n, 0);
       const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
       int page = page_of(table, t0, rank, t1, len);
-      // Chunks of Q in shared memory, once the previous piece's products have read the last ones.
-      ok = warp_wait(&c.qe, qphase ^ 1u, a.status, 161);
-      if (!ok) break;
-      if (elect_one()) {
-        if (rank == 0) mbar_arrive_expect_tx(&c.qf, 2 * nss * kChunk);
+      // The chunks of Q for TMEM pass through ring slots ahead of the piece's tiles.
 #pragma unroll 1
-        for (int k = 0; k < nss; ++k) pair_load_3d(sq + k * kChunk, &tma_q, (a.nts + k) * 64, rank * a.hg, b, qf0);
+      for (int u = 0; u < nq && ok; ++u) {
+        ok = warp_wait(&c.empty[lr.slot], lr.phase ^ 1u, a.status, 161);
+        if (!ok) break;
+        const int k1 = (u + 1) * hc < a.nts ? (u + 1) * hc : a.nts;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&c.full[lr.slot], 2 * (k1 - u * hc) * kChunk);
+#pragma unroll 1
+          for (int k = u * hc; k < k1; ++k)
+            pair_load_3d(lat + lr.slot * slot_bytes + (k - u * hc) * kChunk, &tma_q, k * 64, rank * a.hg, b, full0 + lr.slot * 8);
+        }
+        __syncwarp();
+        lr.step(kSlots);
+        ++issued;
       }
-      __syncwarp();
-      qphase ^= 1u;
-      ++issued_q;
+      if (!ok) break;
       int row = row_of(t0, rank, page);
       page = page_of(table, t0 + 1, rank, t1, len);
 #pragma unroll 1
@@ -267,20 +276,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (--lr.slot < 0) { lr.slot = kSlots - 1; lr.phase ^= 1u; }
         bar_wait(&c.full[lr.slot], lr.phase, a.status, 164);
       }
-      if (issued_q > 0) bar_wait(&c.qf, qphase ^ 1u, a.status, 164);
     }
-  } else if (warp == 7) {
+  } else if (warp == 11) {
     // Reload: rows of the other CTA's block, in this CTA's half of the columns, into the slot of the half that only the
     // first product used.
     const int blk = 1 - static_cast<int>(rank);
     int slot = blk;                                        // slot of half blk of the tile
-    uint32_t phase = 0;                                    // by tile parity: bit p
-    int tile = 0;
+    uint32_t phase = 0, qphase = 0;                        // phase: by tile parity, bit p
+    int tile = 0, issued_q = 0;
+    const uint32_t qf0 = pair::map_rank(smem_u32(&c.qf), 0);
     while (ok && wk.next(a, started)) {
       const int b = __shfl_sync(0xffffffffu, wk.b, 0), len = __shfl_sync(0xffffffffu, wk.len, 0);
       const int t0 = __shfl_sync(0xffffffffu, wk.t0, 0), t1 = t0 + __shfl_sync(0xffffffffu, wk.n, 0);
       const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
       int page = page_of(table, t0, blk, t1, len);
+      // Chunks of Q in shared memory, once the previous piece's products have read the last ones.
+      ok = warp_wait(&c.qe, qphase ^ 1u, a.status, 167);
+      if (!ok) break;
+      if (elect_one()) {
+        if (rank == 0) mbar_arrive_expect_tx(&c.qf, 2 * nss * kChunk);
+#pragma unroll 1
+        for (int k = 0; k < nss; ++k) pair_load_3d(sq + k * kChunk, &tma_q, (a.nts + k) * 64, rank * a.hg, b, qf0);
+      }
+      __syncwarp();
+      qphase ^= 1u;
+      ++issued_q;
+      slot = (slot + nq) % kSlots;
       int row = row_of(t0, blk, page);
       page = page_of(table, t0 + 1, blk, t1, len);
 #pragma unroll 1
@@ -306,7 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       wk.done();
     }
-    if (lane == 0) {                                       // the last reloads have landed
+    if (lane == 0) {                                       // the last copies have landed
+      if (rank == 0 && issued_q > 0) bar_wait(&c.qf, qphase ^ 1u, a.status, 166);
       for (int i = 1; i <= 2 && i <= tile; ++i) {
         const int par = (tile - i) & 1;
         bar_wait(&c.vl[par], ((tile - i) >> 1) & 1u, a.status, 166);
@@ -324,7 +346,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tile = 0;
       while (ok && wk.next(a, started)) {
         const int n = __shfl_sync(0xffffffffu, wk.n, 0);
-        ok = warp_wait_cluster(&c.qf, qphase, a.status, 172);
+        // Q to TMEM, after the previous piece's products
+        if (tile > 0) ok = warp_wait(&c.sd[(tile - 1) & 1], ((tile - 1) >> 1) & 1u, a.status, 174);
+#pragma unroll 1
+        for (int u = 0; u < nq && ok; ++u) {
+          ok = warp_wait_cluster(&c.full[lr.slot], lr.phase, a.status, 176);
+          tc_fence_after();
+          if (ok && elect_one()) {
+            const uint64_t d0 = desc_kmajor_sw128(smem_u32(lat)) + lr.slot * (slot_bytes >> 4);
+#pragma unroll 1
+            for (int k = u * hc; k < (u + 1) * hc && k < a.nts; ++k)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) tc_cp_rows64(tm + kQ + k * 32 + 4 * j, d0 + (k - u * hc) * (kChunk >> 4) + j);
+            pair::tc_commit_mc(&c.empty[lr.slot], 0x3);
+          }
+          __syncwarp();
+          lr.step(kSlots);
+        }
+        ok = ok && warp_wait_cluster(&c.qf, qphase, a.status, 172);
         qphase ^= 1u;
         for (int i = 0; i < n && ok; ++i, ++tile) {
           ok = warp_wait_cluster(&c.se, sphase ^ 1u, a.status, 173);
@@ -364,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         wk.done();
       }
     }
-  } else if (warp == 6) {
+  } else if (warp == 10) {
     if (rank == 0) {
       // Issues O^T.
       constexpr uint32_t idesc = idesc_bf16(256, 128) | (1u << 15);   // A (V^T) is MN-major
@@ -374,6 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t pphase = 0, ophase = 0;
       while (ok && wk.next(a, started)) {
         const int n = __shfl_sync(0xffffffffu, wk.n, 0);
+        for (int u = 0; u < nq; ++u) lr.step(kSlots);
         ok = warp_wait_cluster(&c.oe, ophase ^ 1u, a.status, 171);    // the previous piece's O has been read
         ophase ^= 1u;
         for (int i = 0; i < n && ok; ++i) {
@@ -406,16 +446,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    const int q = warp & 3;
+    const int q = warp & 3, sub = (warp - 2) >> 2;
     const int st = tid - 64;                               // softmax thread
     const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
-    const int blk = q >> 1;                                // this thread's token block
+    const int blk = q >> 1;                                // this thread's tokens: 32 sub .. of this block
     const int hl = (q & 1) * 32 + lane;                    // and head of the CTA
     const int head0 = static_cast<int>(rank) * a.hg;       // first head of the CTA
     const int nh = a.H - head0 < a.hg ? a.H - head0 : a.hg;
-    const int tl = q * 32 + lane;                          // TMEM lane; the head's other block is 64 away
+    const int tl = sub * 128 + q * 32 + lane;              // a head's four threads: tl with bits 6 and 7 free
+    const bool first = blk == 0 && sub == 0;               // the one that speaks for the head
     const uint32_t se0 = pair::map_rank(smem_u32(&c.se), 0), pf0 = pair::map_rank(smem_u32(&c.pf), 0);
-    const uint32_t oe0 = pair::map_rank(smem_u32(&c.oe), 0), qf0 = pair::map_rank(smem_u32(&c.qf), 0);
+    const uint32_t oe0 = pair::map_rank(smem_u32(&c.oe), 0);
     const uint32_t other = rank ^ 1u;
     const uint32_t gx_o = pair::map_rank(smem_u32(c.gx), other), gf_o = pair::map_rank(smem_u32(c.gf), other);
     const uint32_t moved_o = pair::map_rank(smem_u32(c.moved), other);
@@ -434,55 +475,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(bar);
     };
-    // Factors of this CTA's heads are in both CTAs' arrays; wait for the other's.
-    auto exchange = [&]() {
-      named_barrier(3, 128);
-      if (st == 0) pair::mbar_arrive_cluster(gf_o + (swaps & 1) * 8);
-      wait(&c.gf[swaps & 1], (swaps >> 1) & 1u, 184);
+    // A factor per head into both CTAs' arrays (the same place in both); the other CTA's heads have arrived at the end.
+    auto exchange = [&](float* arr, uint32_t arr_o, float v) {
+      uint64_t* bar = &c.gf[swaps & 1];
+      if (st == 0) mbar_arrive_expect_tx(bar, kMaxHeadsCta * 4);
+      if (first) {
+        arr[rank * 64 + hl] = v;
+        st_async(arr_o + (rank * 64 + hl) * 4, __float_as_uint(v), gf_o + (swaps & 1) * 8);
+      }
+      named_barrier(3, kSoft);
+      wait(bar, (swaps >> 1) & 1u, 184);
       ++swaps;
     };
-    // Chunks of Q in TMEM: a row a lane, twice (lanes 0-63 and 64-127), as the instruction reads a 64-row half of A.
-    auto q_to_tmem = [&](int b) {
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + b * a.q_b + (head0 + hl) * a.q_h);
-      constexpr int kAtOnce = 3;
-#pragma unroll 1
-      for (int k0 = 0; k0 < a.nts; k0 += kAtOnce) {
-        uint4 v[kAtOnce][8];
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            v[k][j] = k0 + k < a.nts && hl < nh ? ld_global_u4(src + (k0 + k) * 8 + j) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          if (k0 + k >= a.nts) break;
-          uint32_t x[32];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            x[4 * j] = v[k][j].x;
-            x[4 * j + 1] = v[k][j].y;
-            x[4 * j + 2] = v[k][j].z;
-            x[4 * j + 3] = v[k][j].w;
-          }
-          tmem_st_32x32b_x32(tmem + tlane + kQ + (k0 + k) * 32, x);
-        }
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      arrive(qf0);
-    };
-    Walk<kTile> nx = wk;
-    bool nx_started = false;
-    bool more = nx.next(a, nx_started);
-    if (more) q_to_tmem(nx.b);
     while (wk.next(a, started)) {
+      for (int u = 0; u < nq; ++u) lr.step(kSlots);
       float ref = kNoRef, l = 0.0f, le = 0.0f;
-      // P of the scores x (a head, 64 tokens), packed, and its sums; the largest score above the reference.
+      // P of the scores x (a head, 32 tokens), packed, and its sums; the largest score above the reference.
       auto take = [&](const uint32_t* x, uint32_t* p, float& ls, float& les) {
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         float rs[4] = {}, es[4] = {};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < 16; ++i) {
           const float y0 = fmaf(__uint_as_float(x[2 * i]), a.scale2, -ref), y1 = fmaf(__uint_as_float(x[2 * i + 1]), a.scale2, -ref);
           top[i & 3] = fmaxf(top[i & 3], fmaxf(y0, y1));
           const float p0 = ex2(y0), p1 = ex2(y1);
@@ -501,22 +514,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&c.sf, sphase, 180);
         sphase ^= 1u;
         tc_fence_after();
-        uint32_t x[64], p[32];
-        tmem_ld32_async(tmem + tlane + kS, x);
-        tmem_ld32_async(tmem + tlane + kS + 32, x + 32);
+        uint32_t x[32], p[16];
+        tmem_ld32_async(tmem + tlane + kS + sub * 32, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 64; ++i) reg_fence(x[i]);
+        for (int i = 0; i < 32; ++i) reg_fence(x[i]);
         tc_fence_before();
         arrive(se0);
         if (valid < kTile) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (blk * kBlock + i >= valid) x[i] = __float_as_uint(-INFINITY);
+          for (int i = 0; i < 32; ++i)
+            if (blk * kBlock + sub * 32 + i >= valid) x[i] = __float_as_uint(-INFINITY);
         }
         float ls, les;
         const float over = take(x, p, ls, les);
-        const bool grow = barrier_or(2, over > kSlack);
+        const bool grow = barrier_or<kSoft>(2, over > kSlack);
         // O is rescaled only when a score of the tile passes kSlack in either CTA.
         if (st == 0) {
           mbar_arrive_expect_tx(&c.gx[par], 4);            // the other CTA's word
@@ -526,10 +538,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (grow) {
           float m = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) m = fmaxf(m, __uint_as_float(x[i]));
+          for (int i = 0; i < 32; ++i) m = fmaxf(m, __uint_as_float(x[i]));
           xm[tl] = m * a.scale2;
-          named_barrier(3, 128);
-          m = fmaxf(fmaxf(xm[tl], xm[tl ^ 64]), ref);
+          named_barrier(3, kSoft);
+          m = fmaxf(fmaxf(fmaxf(xm[tl], xm[tl ^ 64]), fmaxf(xm[tl ^ 128], xm[tl ^ 192])), ref);
           corr = ex2(ref - m);                             // 0 from kNoRef to a score
           l *= corr;
           le *= corr;
@@ -546,14 +558,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         wait(&c.gx[par], (tile >> 1) & 1u, 185);
         const bool rescale = (grow || *reinterpret_cast<volatile uint32_t*>(&c.moved[par]) != 0u) && ti > 0;
         if (rescale) {
-          if (blk == 0) {
-            fac[rank * 64 + hl] = corr;
-            st_cluster(fac_o + (rank * 64 + hl) * 4, __float_as_uint(corr));
-          }
-          exchange();
+          exchange(fac, fac_o, corr);
           tc_fence_after();
 #pragma unroll 1
-          for (int hc16 = 0; hc16 < 128 * mt; hc16 += 16) {
+          for (int hc16 = sub * 64 * mt; hc16 < (sub + 1) * 64 * mt; hc16 += 16) {
             uint32_t o[16];
             tmem_ld_32x32b_x16(tmem + tlane + hc16, o);
             tmem_wait_ld();
@@ -568,8 +576,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint8_t* prow = sp + blk * kChunk + hl * 128;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          *reinterpret_cast<uint4*>(prow + ((k ^ (hl & 7)) << 4)) = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(prow + (((4 * sub + k) ^ (hl & 7)) << 4)) =
+              make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
         // The reload has landed (its bytes are the second product's operand).
         wait(&c.vl[par], (tile >> 1) & 1u, 182);
         if (valid < kTile) {
@@ -581,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int per = (kBlock - first) * 8;          // 16-byte words to clear in a chunk
             uint8_t* v = lat + slot * slot_bytes;
 #pragma unroll 1
-            for (int i = st; i < hc * per; i += 128) {
+            for (int i = st; i < hc * per; i += kSoft) {
               const int k = i / per, row = first + (i - k * per) / 8;
               *reinterpret_cast<uint4*>(v + k * a.chunk_step + (row >> 3) * a.row8_step + (row & 7) * 128 + (i & 7) * 16) =
                   make_uint4(0, 0, 0, 0);
@@ -595,21 +604,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         arrive(pf0);
       }
-      // ---- epilogue of the piece, after the next one's Q
-      nx.done();
-      if (more && (more = nx.next(a, nx_started))) q_to_tmem(nx.b);
+      // ---- epilogue of the piece
       const bool whole = wk.n == wk.nt;
       const int slot = 2 * w + (wk.first ? 0 : 1);
       xl[tl] = l;
       xe[tl] = le;
-      named_barrier(3, 128);
-      if (blk == 0) {
-        const float v = l + xl[tl + 64], ve = le + xe[tl + 64];
+      named_barrier(3, kSoft);
+      float norm = 0.0f;
+      if (first) {
+        const float v = (l + xl[tl + 64]) + (xl[tl + 128] + xl[tl + 192]);
+        const float ve = (le + xe[tl + 64]) + (xe[tl + 128] + xe[tl + 192]);
         const int h = static_cast<int>(rank) * 64 + hl;
+        norm = v == 0.0f ? 0.0f : 1.0f / v;
         if (whole) {
-          const float i = v == 0.0f ? 0.0f : 1.0f / v;
-          inv[h] = i;
-          st_cluster(inv_o + h * 4, __float_as_uint(i));
           if (a.lse != nullptr && hl < nh)
             a.lse[static_cast<int64_t>(wk.b) * a.H + head0 + hl] = ve == 0.0f ? -INFINITY : (ref + log2f(ve)) * kLn2;
         } else {
@@ -618,17 +625,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.part_e[slot * 128 + h] = ve;
         }
       }
-      if (whole) exchange();
-      else named_barrier(3, 128);                          // xl and xe are free
+      if (whole) exchange(inv, inv_o, norm);
+      else named_barrier(3, kSoft);                        // xl and xe are free
       wait(&c.of, ophase, 183);
       ophase ^= 1u;
       tc_fence_after();
-      uint8_t* stage = sp + q * 2048;                      // [64 heads][16 columns] of this warp, over P
+      uint8_t* stage = sp + (sub * 4 + q) * 2048;          // [64 heads][16 columns] of this warp, over P
+      const int grp = sub;                                 // a warp takes the heads of one CTA, and its lanes' 32 columns
       float4* part = reinterpret_cast<float4*>(a.part_o + static_cast<int64_t>(2 * slot + rank) * kMaxHeadsCta * a.latent) +
                      q * 32 + lane;
 #pragma unroll 1
-      for (int it = 0; it < 4 * mt; ++it) {                // 16 latent columns of the warp's 32, heads of one CTA
-        const int grp = it & 1, mh = it >> 1;
+      for (int mh = 0; mh < 2 * mt; ++mh) {
         uint32_t o[32];
         tmem_ld_16x256b_x8(tmem + tlane + (static_cast<uint32_t>(mh & 1) << 20) + (mh >> 1) * 128 + grp * 64, o);
         tmem_wait_ld();
@@ -675,10 +682,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (seq_len(a, b, false) > 0) continue;
       __nv_bfloat16* out = a.out + (static_cast<int64_t>(b) * a.H + head0) * a.latent;
 #pragma unroll 1
-      for (int i = st; i < nh * a.latent / 8; i += 128) reinterpret_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
+      for (int i = st; i < nh * a.latent / 8; i += kSoft) reinterpret_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
       if (a.lse != nullptr)
 #pragma unroll 1
-        for (int i = st; i < nh; i += 128) a.lse[static_cast<int64_t>(b) * a.H + head0 + i] = -INFINITY;
+        for (int i = st; i < nh; i += kSoft) a.lse[static_cast<int64_t>(b) * a.H + head0 + i] = -INFINITY;
     }
   }
   // Neither CTA leaves (or frees TMEM) while the other may still use its shared memory, its TMEM or its barriers.
@@ -727,8 +734,7 @@ int run_decode_pair(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, con
     note(cudaLaunchKernelEx(&lc, mla_decode_pair_kernel, tk, tr, tq, a));
   }
   if (call_error() != cudaSuccess) return MOE_ERR_CUDA;
-  launch_kernel_after("mla_join", mla_join_kernel<128, true>,
-                      dim3(static_cast<unsigned>(2 * a.W), static_cast<unsigned>(16 * (hc / 2))), dim3(128), 0, s, a);
+  launch_join<128, true>(a, sms, s);
   return MOE_OK;
 }
 

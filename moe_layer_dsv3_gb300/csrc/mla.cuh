@@ -214,16 +214,17 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* s
   return __all_sync(0xffffffffu, bar_wait(bar, parity, status, site));
 }
 
-// Barrier over the 128 softmax threads that also gives the OR of their flags.
+// Barrier over the NT softmax threads that also gives the OR of their flags.
+template <int NT>
 __device__ __forceinline__ bool barrier_or(int id, bool flag) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(flag)), "r"(id)
+      : "r"(static_cast<uint32_t>(flag)), "r"(id), "n"(NT)
       : "memory");
   return r != 0;
 }
@@ -302,66 +303,115 @@ __device__ __forceinline__ int4 join_entry(const Control& c, const Range& r, int
   return make_int4(c.start_b, range_begin(r.total, w0, r.W) == s0 ? 0 : 1, w0, w - w0 + 1);
 }
 
-// Joins the pieces of the sequences that the work split cut, in their order.
-// Block (worker and its CTA, 8 heads and 128 latent columns) for the sequence that
-// the worker ended; a warp takes 32 columns, in the register order in which the
-// pieces were stored. Each block reads few bytes, so that many loads are in
-// flight and a long list of pieces costs a few rounds of latency.
+// Joins the pieces of the sequences that the work split cut. An item is 8 heads and
+// 128 latent columns of one cut sequence; a warp takes 32 columns, in the register
+// order in which the pieces were stored. Two halves of a block take every other
+// piece and are added in order, and each half has up to 8 pieces in flight, so that
+// a long list costs a few rounds of latency.
 // A worker is one CTA of a head group with all latent columns, or (PAIR) a pair of
 // CTAs, each with all heads and half of the columns.
+constexpr int kJoinThreads = 256;
 template <int N, bool PAIR>
-__global__ void __launch_bounds__(128) mla_join_kernel(const __grid_constant__ MlaArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) mla_join_kernel(const __grid_constant__ MlaArgs a) {
   constexpr int NP = N / 8, kHeads = PAIR ? 2 * kMaxHeadsCta : kMaxHeadsCta;
+  __shared__ int4 list[kMaxSms];
+  __shared__ int listw[kJoinThreads / 32];
+  __shared__ float4 half[2][128];
+  __shared__ float2 half_m[128], half_l[128], half_e[128];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = tid >> 7, t = tid & 127, q = t >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the decode kernel's writes are visible
-  const int per = PAIR ? 2 : a.G;
-  const int w = blockIdx.x / per, g = blockIdx.x - w * per;
-  const int4 j = a.join[w];
-  if (j.w == 0) return;
-  const int i = blockIdx.y % NP, m = blockIdx.y / NP, q = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = 8 * i + 2 * (lane & 3);                     // this thread's heads h, h + 1 of the piece
-  auto slot_of = [&](int k) { return PAIR ? 2 * (j.z + k) + (k == 0 ? j.y : 0) : 2 * ((j.z + k) * a.G + g) + (k == 0 ? j.y : 0); };
-  auto pair = [&](const float* v, int k) { return *reinterpret_cast<const float2*>(v + slot_of(k) * kHeads + h); };
-  float2 top = make_float2(kNoRef, kNoRef);
-#pragma unroll 8
-  for (int k = 0; k < j.w; ++k) {
-    const float2 v = pair(a.part_m, k);
-    top = make_float2(fmaxf(top.x, v.x), fmaxf(top.y, v.y));
+  // The workers that end a cut sequence.
+  const int4 mine = tid < a.W ? a.join[tid] : make_int4(0, 0, 0, 0);
+  const uint32_t some = __ballot_sync(0xffffffffu, mine.w != 0);
+  if (lane == 0) listw[warp] = __popc(some);
+  __syncthreads();
+  int at = __popc(some & ((1u << lane) - 1u)), count = 0;
+  for (int i = 0; i < kJoinThreads / 32; ++i) {
+    if (i < warp) at += listw[i];
+    count += listw[i];
   }
-  const float4* o = reinterpret_cast<const float4*>(a.part_o) + (2 * m * NP + i) * 128 + threadIdx.x;
-  float4 s0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s1 = s0;
-  float2 l = make_float2(0.0f, 0.0f), le = l;
-#pragma unroll 8
-  for (int k = 0; k < j.w; ++k) {
-    const float2 mk = pair(a.part_m, k), lk = pair(a.part_l, k), ek = pair(a.part_e, k);
-    const int64_t at = PAIR ? 2 * slot_of(k) + g : slot_of(k);
-    const float4* p = o + at * (kMaxHeadsCta / 4) * a.latent;
-    const float4 v0 = p[0], v1 = p[NP * 128];
-    const float fx = ex2(mk.x - top.x), fy = ex2(mk.y - top.y);
-    l = make_float2(fmaf(fx, lk.x, l.x), fmaf(fy, lk.y, l.y));
-    le = make_float2(fmaf(fx, ek.x, le.x), fmaf(fy, ek.y, le.y));
-    s0 = make_float4(fmaf(fx, v0.x, s0.x), fmaf(fy, v0.y, s0.y), fmaf(fx, v0.z, s0.z), fmaf(fy, v0.w, s0.w));
-    s1 = make_float4(fmaf(fx, v1.x, s1.x), fmaf(fy, v1.y, s1.y), fmaf(fx, v1.z, s1.z), fmaf(fy, v1.w, s1.w));
-  }
-  const float ix = l.x == 0.0f ? 0.0f : 1.0f / l.x, iy = l.y == 0.0f ? 0.0f : 1.0f / l.y;
-  const int grp = PAIR ? h >> 6 : g, hl = PAIR ? h & 63 : h;
-  const int head0 = grp * a.hg, nh = a.H - head0 < a.hg ? a.H - head0 : a.hg;
-  const int64_t row = static_cast<int64_t>(j.x) * a.H + head0 + hl;
-  if (a.lse != nullptr && m == 0 && threadIdx.x < 4 && (!PAIR || g == 0)) {
-    if (hl < nh) a.lse[row] = le.x == 0.0f ? -INFINITY : (top.x + log2f(le.x)) * kLn2;
-    if (hl + 1 < nh) a.lse[row + 1] = le.y == 0.0f ? -INFINITY : (top.y + log2f(le.y)) * kLn2;
-  }
-  // Columns c + 8 k of head h (x) and h + 1 (y). Lanes of neighbouring columns swap: the even one
-  // then stores two columns of head h, the odd one of head h + 1.
-  const float x[4] = {s0.x * ix, s0.z * ix, s1.x * ix, s1.z * ix}, y[4] = {s0.y * iy, s0.w * iy, s1.y * iy, s1.w * iy};
-  const int odd = (lane >> 2) & 1;
-  __nv_bfloat16* out =
-      a.out + (row + odd) * a.latent + (PAIR ? g * (a.latent / 2) : 0) + m * 128 + q * 32 + ((lane >> 2) & ~1);
+  if (mine.w != 0) list[at] = mine;
+  __syncthreads();
+  const int per = PAIR ? 2 : a.G, cols = a.latent / (PAIR ? 256 : 128);
+  const int items = count * per * cols * NP;
+  for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    const int i = it % NP, m = it / NP % cols, g = it / (NP * cols) % per;
+    const int4 j = list[it / (NP * cols * per)];
+    const int h = 8 * i + 2 * (lane & 3);                   // this thread's heads h, h + 1 of the piece
+    float2 top = make_float2(kNoRef, kNoRef), l = make_float2(0.0f, 0.0f), le = l;
+    float4 s0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s1 = s0;
+    auto add = [&](float2 mk, float2 lk, float2 ek, const float4& v0, const float4& v1) {
+      const float2 up = make_float2(fmaxf(top.x, mk.x), fmaxf(top.y, mk.y));
+      const float gx = ex2(top.x - up.x), gy = ex2(top.y - up.y), fx = ex2(mk.x - up.x), fy = ex2(mk.y - up.y);
+      top = up;
+      l = make_float2(fmaf(fx, lk.x, gx * l.x), fmaf(fy, lk.y, gy * l.y));
+      le = make_float2(fmaf(fx, ek.x, gx * le.x), fmaf(fy, ek.y, gy * le.y));
+      s0 = make_float4(fmaf(fx, v0.x, gx * s0.x), fmaf(fy, v0.y, gy * s0.y), fmaf(fx, v0.z, gx * s0.z), fmaf(fy, v0.w, gy * s0.w));
+      s1 = make_float4(fmaf(fx, v1.x, gx * s1.x), fmaf(fy, v1.y, gy * s1.y), fmaf(fx, v1.z, gx * s1.z), fmaf(fy, v1.w, gy * s1.w));
+    };
+#pragma unroll 1
+    for (int k0 = grp; k0 < j.w; k0 += 2 * 4) {
+      float2 mk[4], lk[4], ek[4];
+      float4 v0[4], v1[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float got = __shfl_xor_sync(0xffffffffu, odd ? x[k] : y[k], 4);
-    const uint32_t v = odd ? pack_bf16x2(got, y[k]) : pack_bf16x2(x[k], got);
-    if (hl + odd < nh) *reinterpret_cast<uint32_t*>(out + 8 * k) = v;
+      for (int u = 0; u < 4; ++u) {
+        const int k = k0 + 2 * u < j.w ? k0 + 2 * u : k0;   // past the end: a piece again, not added
+        const int slot = (PAIR ? 2 * (j.z + k) : 2 * ((j.z + k) * a.G + g)) + (k == 0 ? j.y : 0);
+        const int64_t part = PAIR ? 2 * slot + g : slot;
+        const float4* p = reinterpret_cast<const float4*>(a.part_o) + part * (kMaxHeadsCta / 4) * a.latent +
+                          (2 * m * NP + i) * 128 + t;
+        mk[u] = *reinterpret_cast<const float2*>(a.part_m + slot * kHeads + h);
+        lk[u] = *reinterpret_cast<const float2*>(a.part_l + slot * kHeads + h);
+        ek[u] = *reinterpret_cast<const float2*>(a.part_e + slot * kHeads + h);
+        v0[u] = p[0];
+        v1[u] = p[NP * 128];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (k0 + 2 * u < j.w) add(mk[u], lk[u], ek[u], v0[u], v1[u]);
+    }
+    __syncthreads();                                        // the halves' place is free
+    if (grp == 1) {
+      half[0][t] = s0;
+      half[1][t] = s1;
+      half_m[t] = top;
+      half_l[t] = l;
+      half_e[t] = le;
+    }
+    __syncthreads();
+    if (grp == 1) continue;
+    add(half_m[t], half_l[t], half_e[t], half[0][t], half[1][t]);
+    const float ix = l.x == 0.0f ? 0.0f : 1.0f / l.x, iy = l.y == 0.0f ? 0.0f : 1.0f / l.y;
+    const int hg = PAIR ? h >> 6 : g, hl = PAIR ? h & 63 : h;
+    const int head0 = hg * a.hg, nh = a.H - head0 < a.hg ? a.H - head0 : a.hg;
+    const int64_t row = static_cast<int64_t>(j.x) * a.H + head0 + hl;
+    if (a.lse != nullptr && m == 0 && t < 4 && (!PAIR || g == 0)) {
+      if (hl < nh) a.lse[row] = le.x == 0.0f ? -INFINITY : (top.x + log2f(le.x)) * kLn2;
+      if (hl + 1 < nh) a.lse[row + 1] = le.y == 0.0f ? -INFINITY : (top.y + log2f(le.y)) * kLn2;
+    }
+    // Columns c + 8 k of head h (x) and h + 1 (y). Lanes of neighbouring columns swap: the even one
+    // then stores two columns of head h, the odd one of head h + 1.
+    const float x[4] = {s0.x * ix, s0.z * ix, s1.x * ix, s1.z * ix}, y[4] = {s0.y * iy, s0.w * iy, s1.y * iy, s1.w * iy};
+    const int odd = (lane >> 2) & 1;
+    __nv_bfloat16* out =
+        a.out + (row + odd) * a.latent + (PAIR ? g * (a.latent / 2) : 0) + m * 128 + q * 32 + ((lane >> 2) & ~1);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float got = __shfl_xor_sync(0xffffffffu, odd ? x[k] : y[k], 4);
+      const uint32_t v = odd ? pack_bf16x2(got, y[k]) : pack_bf16x2(x[k], got);
+      if (hl + odd < nh) *reinterpret_cast<uint32_t*>(out + 8 * k) = v;
+    }
   }
+}
+
+// The join of a decode launch just made on the same stream. Its blocks start while the last decode CTAs run and wait
+// for their writes on the device. At most every worker but one ends a cut sequence.
+template <int N, bool PAIR>
+void launch_join(const MlaArgs& a, int sms, cudaStream_t s) {
+  const int64_t most = static_cast<int64_t>(a.W - 1) * (PAIR ? 2 : a.G) * (a.latent / (PAIR ? 256 : 128)) * (N / 8);
+  const int64_t grid = most < 5 * sms ? most : 5 * sms;
+  if (grid > 0)
+    launch_kernel_after("mla_join", mla_join_kernel<N, PAIR>, dim3(static_cast<unsigned>(grid)), dim3(kJoinThreads), 0, s, a);
 }
 
 // Decode with both head groups on one pair of CTAs (more than 64 heads, an even number of 128-column tiles), and
