@@ -304,83 +304,92 @@ __device__ __forceinline__ int4 join_entry(const Control& c, const Range& r, int
 }
 
 // Joins the pieces of the sequences that the work split cut. An item is 8 heads and
-// 128 latent columns of one cut sequence; a warp takes 32 columns, in the register
-// order in which the pieces were stored. Two halves of a block take every other
-// piece and are added in order, and each half has up to 8 pieces in flight, so that
-// a long list costs a few rounds of latency.
+// 128 latent columns of one cut sequence, for 128 threads: a warp takes 32 columns,
+// in the register order in which the pieces were stored. Half a block takes an item
+// with few pieces alone; of a long list the halves take every other piece each, four
+// in flight, and their sums are added in order, so that it costs a few rounds of
+// latency (76 pieces of 2 x 131072 tokens: 7 us; one by one it took 17 us). The order
+// of additions depends on the number of pieces only.
 // A worker is one CTA of a head group with all latent columns, or (PAIR) a pair of
 // CTAs, each with all heads and half of the columns.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 2;             // blocks an SM (4 and 8 took the same time or 1 % more)
+constexpr int kJoinFew = 4;                // pieces that a half block adds alone
 template <int N, bool PAIR>
-__global__ void __launch_bounds__(kJoinThreads) mla_join_kernel(const __grid_constant__ MlaArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 2) mla_join_kernel(const __grid_constant__ MlaArgs a) {
   constexpr int NP = N / 8, kHeads = PAIR ? 2 * kMaxHeadsCta : kMaxHeadsCta;
-  __shared__ int4 list[kMaxSms];
-  __shared__ int listw[kJoinThreads / 32];
-  __shared__ float4 half[2][128];
-  __shared__ float2 half_m[128], half_l[128], half_e[128];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, grp = tid >> 7, t = tid & 127, q = t >> 5;
+  __shared__ int4 list[kMaxSms];           // entries with few pieces from the front, the others from the back
+  __shared__ int2 counts[kMaxSms / 32];
+  __shared__ float4 sum[2][128];
+  __shared__ float2 stat[3][128];
+  const int tid = threadIdx.x, lane = tid & 31, half = tid >> 7, t = tid & 127, q = t >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the decode kernel's writes are visible
-  // The workers that end a cut sequence.
-  const int4 mine = tid < a.W ? a.join[tid] : make_int4(0, 0, 0, 0);
-  const uint32_t some = __ballot_sync(0xffffffffu, mine.w != 0);
-  if (lane == 0) listw[warp] = __popc(some);
+  // The workers that end a cut sequence: one thread looks at each.
+  static_assert(kMaxSms % 32 == 0 && kMaxSms <= kJoinThreads, "one pass over the workers");
+  const int4 e = tid < a.W ? a.join[tid] : make_int4(0, 0, 0, 0);
+  const uint32_t bf = __ballot_sync(0xffffffffu, e.w != 0 && e.w <= kJoinFew);
+  const uint32_t bm = __ballot_sync(0xffffffffu, e.w > kJoinFew);
+  if (lane == 0 && tid < kMaxSms) counts[tid >> 5] = make_int2(__popc(bf), __popc(bm));
   __syncthreads();
-  int at = __popc(some & ((1u << lane) - 1u)), count = 0;
-  for (int i = 0; i < kJoinThreads / 32; ++i) {
-    if (i < warp) at += listw[i];
-    count += listw[i];
+  int few = 0, many = 0, few_at = __popc(bf & ((1u << lane) - 1u)), many_at = __popc(bm & ((1u << lane) - 1u));
+#pragma unroll
+  for (int i = 0; i < kMaxSms / 32; ++i) {
+    const int2 c = counts[i];
+    if (i < (tid >> 5)) {
+      few_at += c.x;
+      many_at += c.y;
+    }
+    few += c.x;
+    many += c.y;
   }
-  if (mine.w != 0) list[at] = mine;
+  if (e.w != 0) list[e.w <= kJoinFew ? few_at : kMaxSms - 1 - many_at] = e;
   __syncthreads();
   const int per = PAIR ? 2 : a.G, cols = a.latent / (PAIR ? 256 : 128);
-  const int items = count * per * cols * NP;
-  for (int it = blockIdx.x; it < items; it += gridDim.x) {
-    const int i = it % NP, m = it / NP % cols, g = it / (NP * cols) % per;
-    const int4 j = list[it / (NP * cols * per)];
-    const int h = 8 * i + 2 * (lane & 3);                   // this thread's heads h, h + 1 of the piece
-    float2 top = make_float2(kNoRef, kNoRef), l = make_float2(0.0f, 0.0f), le = l;
-    float4 s0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), s1 = s0;
-    auto add = [&](float2 mk, float2 lk, float2 ek, const float4& v0, const float4& v1) {
-      const float2 up = make_float2(fmaxf(top.x, mk.x), fmaxf(top.y, mk.y));
-      const float gx = ex2(top.x - up.x), gy = ex2(top.y - up.y), fx = ex2(mk.x - up.x), fy = ex2(mk.y - up.y);
-      top = up;
-      l = make_float2(fmaf(fx, lk.x, gx * l.x), fmaf(fy, lk.y, gy * l.y));
-      le = make_float2(fmaf(fx, ek.x, gx * le.x), fmaf(fy, ek.y, gy * le.y));
-      s0 = make_float4(fmaf(fx, v0.x, gx * s0.x), fmaf(fy, v0.y, gy * s0.y), fmaf(fx, v0.z, gx * s0.z), fmaf(fy, v0.w, gy * s0.w));
-      s1 = make_float4(fmaf(fx, v1.x, gx * s1.x), fmaf(fy, v1.y, gy * s1.y), fmaf(fx, v1.z, gx * s1.z), fmaf(fy, v1.w, gy * s1.w));
-    };
+  const int each = per * cols * NP;                         // items of an entry
+
+  float2 top, l, le;                                        // of heads h and h + 1: reference, sums
+  float4 s0, s1;
+  auto add = [&](float2 mk, float2 lk, float2 ek, const float4& v0, const float4& v1) {
+    const float2 up = make_float2(fmaxf(top.x, mk.x), fmaxf(top.y, mk.y));
+    const float gx = ex2(top.x - up.x), gy = ex2(top.y - up.y), fx = ex2(mk.x - up.x), fy = ex2(mk.y - up.y);
+    top = up;
+    l = make_float2(fmaf(fx, lk.x, gx * l.x), fmaf(fy, lk.y, gy * l.y));
+    le = make_float2(fmaf(fx, ek.x, gx * le.x), fmaf(fy, ek.y, gy * le.y));
+    s0 = make_float4(fmaf(fx, v0.x, gx * s0.x), fmaf(fy, v0.y, gy * s0.y), fmaf(fx, v0.z, gx * s0.z), fmaf(fy, v0.w, gy * s0.w));
+    s1 = make_float4(fmaf(fx, v1.x, gx * s1.x), fmaf(fy, v1.y, gy * s1.y), fmaf(fx, v1.z, gx * s1.z), fmaf(fy, v1.w, gy * s1.w));
+  };
+  // Pieces first, first + step, ... of the entry, four in flight.
+  auto gather = [&](const int4& j, int g, int m, int i, int first, int step) {
+    const int h = 8 * i + 2 * (lane & 3);
+    top = make_float2(kNoRef, kNoRef);
+    l = le = make_float2(0.0f, 0.0f);
+    s0 = s1 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-    for (int k0 = grp; k0 < j.w; k0 += 2 * 4) {
+    for (int k0 = first; k0 < j.w; k0 += 4 * step) {
       float2 mk[4], lk[4], ek[4];
       float4 v0[4], v1[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int k = k0 + 2 * u < j.w ? k0 + 2 * u : k0;   // past the end: a piece again, not added
-        const int slot = (PAIR ? 2 * (j.z + k) : 2 * ((j.z + k) * a.G + g)) + (k == 0 ? j.y : 0);
-        const int64_t part = PAIR ? 2 * slot + g : slot;
-        const float4* p = reinterpret_cast<const float4*>(a.part_o) + part * (kMaxHeadsCta / 4) * a.latent +
-                          (2 * m * NP + i) * 128 + t;
-        mk[u] = *reinterpret_cast<const float2*>(a.part_m + slot * kHeads + h);
-        lk[u] = *reinterpret_cast<const float2*>(a.part_l + slot * kHeads + h);
-        ek[u] = *reinterpret_cast<const float2*>(a.part_e + slot * kHeads + h);
-        v0[u] = p[0];
-        v1[u] = p[NP * 128];
+        const int k = k0 + u * step;
+        if (k < j.w) {
+          const int slot = (PAIR ? 2 * (j.z + k) : 2 * ((j.z + k) * a.G + g)) + (k == 0 ? j.y : 0);
+          const int64_t part = PAIR ? 2 * slot + g : slot;
+          const float4* p = reinterpret_cast<const float4*>(a.part_o) + part * (kMaxHeadsCta / 4) * a.latent +
+                            (2 * m * NP + i) * 128 + t;
+          mk[u] = *reinterpret_cast<const float2*>(a.part_m + slot * kHeads + h);
+          lk[u] = *reinterpret_cast<const float2*>(a.part_l + slot * kHeads + h);
+          ek[u] = *reinterpret_cast<const float2*>(a.part_e + slot * kHeads + h);
+          v0[u] = p[0];
+          v1[u] = p[NP * 128];
+        }
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (k0 + 2 * u < j.w) add(mk[u], lk[u], ek[u], v0[u], v1[u]);
+        if (k0 + u * step < j.w) add(mk[u], lk[u], ek[u], v0[u], v1[u]);
     }
-    __syncthreads();                                        // the halves' place is free
-    if (grp == 1) {
-      half[0][t] = s0;
-      half[1][t] = s1;
-      half_m[t] = top;
-      half_l[t] = l;
-      half_e[t] = le;
-    }
-    __syncthreads();
-    if (grp == 1) continue;
-    add(half_m[t], half_l[t], half_e[t], half[0][t], half[1][t]);
+  };
+  auto store = [&](const int4& j, int g, int m, int i) {
+    const int h = 8 * i + 2 * (lane & 3);
     const float ix = l.x == 0.0f ? 0.0f : 1.0f / l.x, iy = l.y == 0.0f ? 0.0f : 1.0f / l.y;
     const int hg = PAIR ? h >> 6 : g, hl = PAIR ? h & 63 : h;
     const int head0 = hg * a.hg, nh = a.H - head0 < a.hg ? a.H - head0 : a.hg;
@@ -401,17 +410,41 @@ __global__ void __launch_bounds__(kJoinThreads) mla_join_kernel(const __grid_con
       const uint32_t v = odd ? pack_bf16x2(got, y[k]) : pack_bf16x2(x[k], got);
       if (hl + odd < nh) *reinterpret_cast<uint32_t*>(out + 8 * k) = v;
     }
+  };
+
+  for (int it = blockIdx.x * 2 + half; it < few * each; it += gridDim.x * 2) {
+    const int i = it % NP, m = it / NP % cols, g = it / (NP * cols) % per;
+    const int4 j = list[it / each];
+    gather(j, g, m, i, 0, 1);
+    store(j, g, m, i);
+  }
+  for (int it = blockIdx.x; it < many * each; it += gridDim.x) {
+    const int i = it % NP, m = it / NP % cols, g = it / (NP * cols) % per;
+    const int4 j = list[kMaxSms - 1 - it / each];
+    gather(j, g, m, i, half, 2);
+    __syncthreads();                                        // the place of the second half's sums is free
+    if (half == 1) {
+      sum[0][t] = s0;
+      sum[1][t] = s1;
+      stat[0][t] = top;
+      stat[1][t] = l;
+      stat[2][t] = le;
+    }
+    __syncthreads();
+    if (half == 0) {
+      add(stat[0][t], stat[1][t], stat[2][t], sum[0][t], sum[1][t]);
+      store(j, g, m, i);
+    }
   }
 }
 
-// The join of a decode launch just made on the same stream. Its blocks start while the last decode CTAs run and wait
-// for their writes on the device. At most every worker but one ends a cut sequence.
+// The join of a decode launch just made on the same stream. Its blocks start when the last decode CTAs leave room and
+// wait for their writes on the device.
 template <int N, bool PAIR>
 void launch_join(const MlaArgs& a, int sms, cudaStream_t s) {
-  const int64_t most = static_cast<int64_t>(a.W - 1) * (PAIR ? 2 : a.G) * (a.latent / (PAIR ? 256 : 128)) * (N / 8);
-  const int64_t grid = most < 5 * sms ? most : 5 * sms;
-  if (grid > 0)
-    launch_kernel_after("mla_join", mla_join_kernel<N, PAIR>, dim3(static_cast<unsigned>(grid)), dim3(kJoinThreads), 0, s, a);
+  const int64_t most = static_cast<int64_t>(a.W) * (PAIR ? 2 : a.G) * (a.latent / (PAIR ? 256 : 128)) * (N / 8);
+  const int64_t grid = most < kJoinBlocks * sms ? most : kJoinBlocks * sms;
+  launch_kernel_after("mla_join", mla_join_kernel<N, PAIR>, dim3(static_cast<unsigned>(grid)), dim3(kJoinThreads), 0, s, a);
 }
 
 // Decode with both head groups on one pair of CTAs (more than 64 heads, an even number of 128-column tiles), and
