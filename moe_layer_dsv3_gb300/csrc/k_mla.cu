@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kThreads = 224;
 constexpr int kTile = kBlock;             // cached tokens per tile
+constexpr int kAppendBlocks = 3;          // resident blocks an SM: 32768 tokens in 17.4 us; 4 spill and take 20.7
 constexpr int kMaxLatSlots = 12;
 constexpr int kMaxRopeSlots = 3;
 constexpr int kMinTiles = 3;              // fewest tiles of a worker: 24 tiles took 18.4 us at 3, 20.5 at 2 and 4
@@ -632,73 +633,114 @@ struct AppendArgs {
   int* status;
 };
 
-__global__ void __launch_bounds__(256, 6) mla_append_kernel(const __grid_constant__ AppendArgs a) {
+// HBM bounds it: a row in, a row out (75 MB and 11 us for 32768 tokens of 512 + 64
+// columns, measured 17.4 us of which 3 are launch and ramp). A token's place takes
+// two dependent reads (position, then page): each warp walks tokens warp,
+// warp + warps, ... with the position read two tokens ahead, and page, row and
+// rotation one ahead.
+__global__ void __launch_bounds__(256, kAppendBlocks) mla_append_kernel(const __grid_constant__ AppendArgs a) {
   const int lane = threadIdx.x & 31;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (i >= a.n) return;
-  const int p = __ldg(a.pos + i), b = __ldg(a.seq + i);
-  const __nv_bfloat16* src = a.kv + i * a.ld;
+  const int step = static_cast<int>(gridDim.x) * 8;
   const int nlat = a.latent >> 3, nrope = a.rope >> 3;
-  // the row's loads do not wait for its place
-  uint4 c[2], u = make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    c[k] = lane + 32 * k < nlat ? ld_global_u4(src + (lane + 32 * k) * 8) : make_uint4(0, 0, 0, 0);
-  if (lane < nrope) u = ld_global_u4(src + a.latent + lane * 8);
-  if (p < 0) return;                                       // padding
-  if (b < 0 || b >= a.B || p >= static_cast<int64_t>(a.max_pages) * a.page ||
-      (a.cos_sin != nullptr && p >= a.max_pos)) {
-    if (lane == 0) report_error(a.status, kErrBounds, 65);
-    return;
-  }
-  const int page = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + p / a.page);
-  if (page < 0 || page >= a.num_pages) {
-    if (lane == 0) report_error(a.status, kErrBounds, 66);
-    return;
-  }
-  __nv_bfloat16* dst = a.cache + (static_cast<int64_t>(page) * a.page + p % a.page) * (a.latent + a.rope);
-  if (a.gamma != nullptr) {
-    float v[2][8], ss = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      unpack_bf16x8(c[k], v[k]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v[k][e], v[k][e], ss);
+  const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  struct Token {
+    uint4 c[2], u;               // latent vectors lane and lane + 32, rope vector lane
+    float4 co, si;
+    int page, row;               // page and row in it (row < 0: nothing to write)
+  };
+  auto read = [&](int64_t i, int p, int b, Token& t) {
+    t.page = 0;
+    t.row = -1;
+    t.c[0] = t.c[1] = t.u = make_uint4(0, 0, 0, 0);
+    t.co = t.si = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i >= a.n || p < 0) return;                         // past the end, or padding
+    if (b < 0 || b >= a.B || p >= cap || (a.cos_sin != nullptr && p >= a.max_pos)) {
+      if (lane == 0) report_error(a.status, kErrBounds, 65);
+      return;
     }
+    const int pg = p / a.page;
+    t.row = p - pg * a.page;
+    t.page = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + pg);
+    const __nv_bfloat16* src = a.kv + i * a.ld;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float rstd = rsqrtf(ss / static_cast<float>(a.latent) + a.eps);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (lane + 32 * k < nlat) {
-        float g[8];
-        unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(a.gamma) + lane + 32 * k), g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = v[k][e] * rstd * g[e];
-        c[k] = pack_bf16x8(g);
+    for (int h = 0; h < 2; ++h)
+      if (lane + 32 * h < nlat) t.c[h] = ld_global_u4(src + (lane + 32 * h) * 8);
+    if (lane < nrope) {
+      t.u = ld_global_u4(src + a.latent + lane * 8);
+      if (a.cos_sin != nullptr) {
+        const float* cs = a.cos_sin + static_cast<int64_t>(p) * a.rope + lane * 4;
+        t.co = __ldg(reinterpret_cast<const float4*>(cs));
+        t.si = __ldg(reinterpret_cast<const float4*>(cs + a.rope / 2));
       }
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (lane + 32 * k < nlat) reinterpret_cast<uint4*>(dst)[lane + 32 * k] = c[k];
-  if (lane < nrope) {
-    if (a.cos_sin != nullptr) {
-      const float* cs = a.cos_sin + static_cast<int64_t>(p) * a.rope + lane * 4;
-      const float4 co = __ldg(reinterpret_cast<const float4*>(cs));
-      const float4 si = __ldg(reinterpret_cast<const float4*>(cs + a.rope / 2));
-      const float cc[4] = {co.x, co.y, co.z, co.w}, sn[4] = {si.x, si.y, si.z, si.w};
-      float v[8];
-      unpack_bf16x8(u, v);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x = v[2 * e], y = v[2 * e + 1];
-        v[2 * e] = x * cc[e] - y * sn[e];
-        v[2 * e + 1] = x * sn[e] + y * cc[e];
-      }
-      u = pack_bf16x8(v);
     }
-    reinterpret_cast<uint4*>(dst + a.latent)[lane] = u;
+  };
+  int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (i >= a.n) return;
+  auto place = [&](int64_t k, int& p, int& b) {
+    p = k < a.n ? __ldg(a.pos + k) : -1;
+    b = k < a.n ? __ldg(a.seq + k) : 0;
+  };
+  int p0, b0, p1, b1;
+  place(i, p0, b0);
+  place(i + step, p1, b1);
+  uint4 ug[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    ug[h] = a.gamma != nullptr && lane + 32 * h < nlat ? __ldg(reinterpret_cast<const uint4*>(a.gamma) + lane + 32 * h)
+                                                       : make_uint4(0, 0, 0, 0);
+  Token t;
+  read(i, p0, b0, t);
+  for (; i < a.n; i += step) {
+    Token nt;
+    read(i + step, p1, b1, nt);
+    place(i + 2 * step, p1, b1);
+    if (t.page < 0 || t.page >= a.num_pages) {
+      if (lane == 0) report_error(a.status, kErrBounds, 66);
+      t.row = -1;
+    }
+    if (t.row >= 0) {                                      // the same in every lane
+      __nv_bfloat16* dst = a.cache + (static_cast<int64_t>(t.page) * a.page + t.row) * (a.latent + a.rope);
+      if (a.gamma != nullptr) {
+        float v[2][8], ss = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          unpack_bf16x8(t.c[h], v[h]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) ss = fmaf(v[h][e], v[h][e], ss);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float rstd = rsqrtf(ss / static_cast<float>(a.latent) + a.eps);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float g[8];
+          unpack_bf16x8(ug[h], g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] = v[h][e] * rstd * g[e];
+          t.c[h] = pack_bf16x8(g);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (lane + 32 * h < nlat) reinterpret_cast<uint4*>(dst)[lane + 32 * h] = t.c[h];
+      if (lane < nrope) {
+        if (a.cos_sin != nullptr) {
+          const float cc[4] = {t.co.x, t.co.y, t.co.z, t.co.w}, sn[4] = {t.si.x, t.si.y, t.si.z, t.si.w};
+          float v[8];
+          unpack_bf16x8(t.u, v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = v[2 * e], y = v[2 * e + 1];
+            v[2 * e] = x * cc[e] - y * sn[e];
+            v[2 * e + 1] = x * sn[e] + y * cc[e];
+          }
+          t.u = pack_bf16x8(v);
+        }
+        reinterpret_cast<uint4*>(dst + a.latent)[lane] = t.u;
+      }
+    }
+    t = nt;
   }
 }
 
@@ -827,8 +869,9 @@ extern "C" int moe_mla_append(const moe_mla_config_t* cfg, int n, const void* kv
   a.table = block_table;
   a.cache = static_cast<__nv_bfloat16*>(cache);
   a.status = reinterpret_cast<int*>(static_cast<char*>(ws) + mla_layout(cfg).status);
-  launch_kernel_after("mla_append", mla_append_kernel, dim3(static_cast<unsigned>(ceil_div(n, 8))), dim3(256), 0,
-                static_cast<cudaStream_t>(stream), a);
+  const int64_t blocks = ceil_div(n, 8), most = static_cast<int64_t>(kAppendBlocks) * num_sms();
+  launch_kernel_after("mla_append", mla_append_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256),
+                      0, static_cast<cudaStream_t>(stream), a);
   return call.status();
 }
 

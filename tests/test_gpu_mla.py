@@ -326,3 +326,25 @@ def test_failed_tensor_map_launches_nothing(lib):
         torch.cuda.synchronize()
         assert e.value.code == lib.MOE_ERR_CUDA and (s.att.out == 7.0).all()
     s.run().check()
+
+
+@pytest.mark.parametrize("bad", [-1, -7, 400, 2 ** 31 - 1])
+def test_append_bad_page_among_many_tokens(lib, bad):
+    """Every token of a bad page is left out and the status set; all others are written, whatever their warp's next."""
+    from moe_layer_dsv3_gb300.attention import LatentAttention
+    n = 6000                                       # several tokens a warp
+    B, page, width = 2, 24, 200
+    att = LatentAttention(B, 16, 128, 32, page, B * width, width, 1.0)
+    table = torch.arange(B * width, dtype=torch.int32).view(B, width).cuda()
+    table[1, 3] = bad                              # 400 = the number of pages
+    cache = att.new_cache()
+    kv = torch.randn(n, 160, device="cuda").to(torch.bfloat16)
+    seq = (torch.arange(n) % B).int().cuda()
+    pos = (torch.arange(n) // B).int().cuda()
+    att.append(kv, cache, table, seq, pos)
+    torch.cuda.synchronize()
+    assert att.status() == (lib.MOE_ERR_BOUNDS, 66)
+    want = torch.zeros_like(cache)
+    good = ~((seq == 1) & (pos // page == 3))
+    want[(seq.long() * width + pos.long() // page)[good], (pos.long() % page)[good]] = kv[good]
+    assert torch.equal(cache, want)
