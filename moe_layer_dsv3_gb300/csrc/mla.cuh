@@ -269,7 +269,7 @@ __device__ __forceinline__ Range find_range(const MlaArgs& a, Control& c, int w,
     if (i < warp) before += c.scan[i];
     r.total += c.scan[i];
   }
-  // Each worker that gets tiles gets MIN_TILES or more (a piece costs a join), unless there are fewer.
+  // A piece costs a join, so no more workers than tiles / MIN_TILES (rounded up) get any; ranges differ by a tile at most.
   const int most = (r.total + MIN_TILES - 1) / MIN_TILES;
   r.W = a.W < most ? a.W : (most > 0 ? most : 1);
   r.f0 = w < r.W ? range_begin(r.total, w, r.W) : r.total;

@@ -105,6 +105,19 @@ CASES = {
     "heads_65": dict(lens=[300, 77], H=65, page=40),
     "heads_96": dict(lens=[256, 77, 3], H=96, page=256),
     "heads_128": dict(lens=[500, 1, 64, 1111], H=128),
+    "pair_one_token": dict(lens=[1], H=128),
+    "pair_tile_edges": dict(lens=[63, 64, 65, 127, 128, 129, 191, 192, 193, 255, 256, 257, 1], H=128),
+    "pair_empty_rows": dict(lens=[0, 70, 0, 1, 0], H=100),
+    "pair_all_empty": dict(lens=[0, 0, 0], H=128),
+    "pair_page_8": dict(lens=[300, 5, 64, 129], H=66, page=8),
+    "pair_page_24": dict(lens=[1000, 77, 200], H=127, page=24),
+    "pair_many_short": dict(lens=[(11 * i) % 300 for i in range(300)], H=72, page=16),
+    "pair_256_rope_8": dict(lens=[400, 66, 1], H=80, latent=256, rope=8, page=192),
+    "pair_256_rope_64": dict(lens=[4000, 66, 1], H=128, latent=256, rope=64),
+    "pair_large_scores": dict(lens=[3000, 70, 1], H=128, qgain=30.0),
+    "pair_two_pieces_each": dict(lens=[130 * 128] * 3, H=128),
+    "two_groups_384": dict(lens=[700, 3, 129], H=128, latent=384),
+    "two_groups_128": dict(lens=[700, 3, 129], H=90, latent=128, rope=16),
     "latent_128": dict(lens=[333, 64], H=40, latent=128, rope=8),
     "latent_256": dict(lens=[333, 65], H=128, latent=256, rope=32),
     "latent_384": dict(lens=[333, 66], H=64, latent=384, rope=56),
@@ -133,9 +146,10 @@ def test_rising_scores(lib, H):
     s.run().check()
 
 
-def test_minus_infinity_scores(lib):
+@pytest.mark.parametrize("H", [16, 128])
+def test_minus_infinity_scores(lib, H):
     """Rows whose scores are all -inf give zeros; -inf beside finite scores takes no part."""
-    s = Setup([80, 80], 16, seed=3)
+    s = Setup([80, 80], H, seed=3)
     s.q[:, :, 0] = 1.0
     rows = [s.table[b, j].item() for b in (0, 1) for j in (0, 1)]
     s.cache[rows[0], :, 0] = -float("inf")
@@ -152,8 +166,9 @@ def test_minus_infinity_scores(lib):
     assert (s.att.lse[1].double() - torch.logsumexp(sc, 1)).abs().max() < 1e-4
 
 
-def test_nan_stays_in_its_sequence(lib):
-    s = Setup([100, 100, 100], 16, seed=4)
+@pytest.mark.parametrize("H", [16, 128])
+def test_nan_stays_in_its_sequence(lib, H):
+    s = Setup([100, 100, 100], H, seed=4)
     p = s.table[1, 1].item()
     s.cache[p, 3, 500] = float("nan")
     s.run()
@@ -161,30 +176,46 @@ def test_nan_stays_in_its_sequence(lib):
     assert torch.isfinite(s.att.out[[0, 2]].float()).all()
 
 
-def test_pitched_queries_and_shared_pages(lib):
-    s = Setup([300, 200], 20, latent=256, rope=64, seed=5)
+@pytest.mark.parametrize("H", [20, 70])
+def test_pitched_queries_and_shared_pages(lib, H):
+    s = Setup([300, 200], H, latent=256, rope=64, seed=5)
     s.table[1, :3] = s.table[0, :3]              # a common prefix of 192 tokens
-    big = torch.full((2, 31, 400), float("nan"), dtype=torch.bfloat16, device="cuda")
-    big[:, 3:23, 8:328] = s.q
-    s.q = big[:, 3:23, 8:328]
+    big = torch.full((2, H + 11, 400), float("nan"), dtype=torch.bfloat16, device="cuda")
+    big[:, 3:H + 3, 8:328] = s.q
+    s.q = big[:, 3:H + 3, 8:328]
     s.run().check()
 
 
-def test_repeats_give_the_same_bytes(lib):
-    s = Setup([3000, 77, 1500], 128, seed=6).run()
+def test_interleaved_shapes_share_a_stream(lib):
+    """Calls of several shapes, one after another without waiting, with workspaces of their own."""
+    sets = [Setup([900, 5, 130], 16, seed=1), Setup([2000, 64], 128, seed=2), Setup([300] * 9, 48, seed=3, page=24)]
+    for _ in range(5):
+        for s in sets:
+            s.att.decode(s.q, s.cache, s.table, s.lens)
+    torch.cuda.synchronize()
+    for s in sets:
+        s.att.check_status()
+        s.check()
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_repeats_give_the_same_bytes(lib, H):
+    s = Setup([3000, 77, 1500], H, seed=6).run()
     a, b = s.att.out.clone(), s.att.lse.clone()
     for _ in range(3):
         s.run()
         assert torch.equal(s.att.out, a) and torch.equal(s.att.lse, b)
 
 
-def test_cache_past_32_bit_offsets(lib):
+@pytest.mark.parametrize("H", [16, 128])
+def test_cache_past_32_bit_offsets(lib, H):
     """Pages whose elements start past 2^31, and whose bytes start past 2^32."""
-    Setup([700, 64, 129], 16, seed=7, num_pages=70000).run().check()
+    Setup([700, 64, 129], H, seed=7, num_pages=70000).run().check()
 
 
-def test_graph_replay_reads_new_lengths(lib):
-    s = Setup([400, 900, 64], 16, seed=8)
+@pytest.mark.parametrize("H", [16, 128])
+def test_graph_replay_reads_new_lengths(lib, H):
+    s = Setup([400, 900, 64], H, seed=8)
     full = list(s.lens_l)
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
@@ -204,8 +235,9 @@ def test_graph_replay_reads_new_lengths(lib):
         s.check()
 
 
-def test_out_of_range_lengths_and_pages_are_reported(lib):
-    s = Setup([100, 100, 100], 16, seed=9)
+@pytest.mark.parametrize("H", [16, 128])
+def test_out_of_range_lengths_and_pages_are_reported(lib, H):
+    s = Setup([100, 100, 100], H, seed=9)
     cap = s.att.max_pages * s.page
     s.lens.copy_(torch.tensor([100, -5, 100], dtype=torch.int32))
     s.att.decode(s.q, s.cache, s.table, s.lens)
@@ -218,7 +250,7 @@ def test_out_of_range_lengths_and_pages_are_reported(lib):
     torch.cuda.synchronize()
     assert s.att.status() == (lib.MOE_ERR_BOUNDS, 60)
     for bad in (-1, s.att.num_pages, 2 ** 31 - 1):
-        s = Setup([100, 100], 16, seed=9)
+        s = Setup([100, 100], H, seed=9)
         s.table[1, 1] = bad
         s.att.decode(s.q, s.cache, s.table, s.lens)
         torch.cuda.synchronize()
@@ -317,7 +349,7 @@ def test_no_sequences_and_no_tokens(lib):
 
 def test_failed_tensor_map_launches_nothing(lib):
     s = Setup([100], 16, seed=13)
-    for k in (1, 2):                             # the cache's map; q's map fails on the second try
+    for _ in range(2):
         s.att.out.fill_(7.0)
         lib.moe_debug_fail_tensor_maps(1)
         with pytest.raises(lib.MoeError) as e:
