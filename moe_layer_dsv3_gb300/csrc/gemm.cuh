@@ -54,9 +54,9 @@ bool make_tmap(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int
 bool make_tmap_out(CUtensorMap* m, void* base, int64_t rows, int64_t cols);
 // Tiled scale array as uint32 [atoms][128]: one box = one 512-byte scale atom.
 bool make_tmap_sf(CUtensorMap* m, const void* base, int64_t atoms);
-// bf16 tensor of 2 or 3 dimensions (innermost first; strides of the outer ones in bytes), 128-byte swizzle.
-bool make_tmap_strided(CUtensorMap* m, const void* base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
-                       const uint32_t (&box)[3], int rank);
+// bf16 tensor of 2 to 4 dimensions (innermost first; strides of the outer ones in bytes), 128-byte swizzle.
+bool make_tmap_strided(CUtensorMap* m, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                       const uint32_t (&box)[4], int rank);
 
 // The epilogue / tile shape a mode shares with its per-lap form.
 __host__ __device__ constexpr int base_mode(int mode) {

@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t qphase = 0;
     int issued = 0, issued_q = 0;
     const int pieces = kTile / a.piece;
+    const int piece_step = (a.piece >> 3) * a.row8_step;
     const int oob = a.num_pages * a.page;               // a row past the cache: reads zeros
     const int h0 = g * a.hg;
     while (ok && wk.next(a, started)) {
@@ -174,7 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = t0; t < t1 && ok; ++t) {
         const int left = len - t * kTile;
         const int live = left >= kTile ? pieces : (left + a.piece - 1) / a.piece;   // pieces with tokens
-        const int y = __shfl_sync(0xffffffffu, row, 0);
+        int ys[8];
+        rows_of(row, ys);
 #pragma unroll 1
         for (int u = 0; u < a.nu && ok; ++u) {           // a slot of latent columns, the rope columns with the first
           if (u == 0) ok = warp_wait(&c.ropee[rr.slot], rr.phase ^ 1u, a.status, 63);
@@ -183,18 +185,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint64_t* full = &c.latf[lr.slot];
           uint8_t* dst = lat + lr.slot * slot_bytes;
           uint8_t* rdst = ropes + rr.slot * kChunk;
-          // A box holds all chunks of the slot for the tokens of one piece.
           if (elect_one()) {
             mbar_arrive_expect_tx(full, live * a.piece * 128 * (2 * a.um + (u == 0 ? 1 : 0)));
-            if (pieces == 1) {
-              tma_load_3d(dst, &tma_k, 0, y, 2 * a.um * u, full);
-              if (u == 0) tma_load_2d(rdst, &tma_r, a.latent, y, full);
+            // A box holds all chunks of the slot for the tokens of one piece.
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+              if (p >= live) break;
+              tma_load_4d(dst + p * piece_step, &tma_k, 0, 0, 2 * a.um * u, ys[p] >> 3, full);
+              if (u == 0) tma_load_2d(rdst + p * a.piece * 128, &tma_r, a.latent, ys[p], full);
             }
-          }
-          __syncwarp();
-          if (pieces > 1 && lane < live) {
-            tma_load_3d(dst + lane * a.row8_step, &tma_k, 0, row, 2 * a.um * u, full);
-            if (u == 0) tma_load_2d(rdst + lane * 1024, &tma_r, a.latent, row, full);
           }
           __syncwarp();
           lr.step(a.nlat);
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // descriptors stay in uniform registers. That counts: an MMA of these sizes
     // takes 23 to 48 clocks, and issuing one from a divergent branch took 100.
     constexpr uint32_t idesc_s = idesc_bf16(64, kTile);
-    constexpr uint32_t kChunkStep = kChunk >> 4;          // descriptor address units
+    constexpr uint32_t kChunkUnits = kChunk >> 4;         // descriptor address units
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dq0 = desc_kmajor_sw128(smem_u32(sq)), dl0 = smem_desc(smem_u32(lat), 16, a.row8_step, 2);
     const uint64_t dr0 = desc_kmajor_sw128(smem_u32(ropes));
@@ -251,11 +250,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, dq + kk * 2, dk + kk * 2, idesc_s, !fresh || kk > 0);
               }
             };
-            const uint64_t dl = dl0 + lr.slot * (a.um * 2 * kChunkStep);
+            const uint64_t dl = dl0 + lr.slot * (a.um * 2 * kChunkUnits);
 #pragma unroll 1
-            for (int k = 0; k < 2 * a.um; ++k) chunk(u * a.um * 2 + k, dl + k * (a.chunk_step >> 4), u + k == 0);
+            for (int k = 0; k < 2 * a.um; ++k) chunk(u * a.um * 2 + k, dl + k * (kChunkStep >> 4), u + k == 0);
             if (u == 0) {
-              chunk(nchunk - 1, dr0 + rr.slot * kChunkStep, false);
+              chunk(nchunk - 1, dr0 + rr.slot * kChunkUnits, false);
               tc_commit(&c.ropee[rr.slot]);
             }
             if (u == a.nu - 1) {
@@ -278,9 +277,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 6) {
     // Issues O^T, in a warp of its own: it then never waits behind the next tile's data.
     constexpr uint32_t idesc_o = idesc_bf16(128, N) | (1u << 15);   // A (V^T) is MN-major
-    constexpr uint32_t kChunkStep = kChunk >> 4;
+    constexpr uint32_t kChunkUnits = kChunk >> 4;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t dp0 = desc_kmajor_sw128(smem_u32(sp)), dv0 = smem_desc(smem_u32(lat), a.chunk_step, a.row8_step, 2);
+    const uint64_t dp0 = desc_kmajor_sw128(smem_u32(sp)), dv0 = smem_desc(smem_u32(lat), kChunkStep, a.row8_step, 2);
     Ring lr;
     uint32_t pphase = 0, ophase = 0;
     while (ok && wk.next(a, started)) {
@@ -298,9 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           int slot = lr.slot;
 #pragma unroll 1
           for (int u = 0; u < a.nu; ++u) {
-            uint64_t dv = dv0 + slot * (a.um * 2 * kChunkStep);
+            uint64_t dv = dv0 + slot * (a.um * 2 * kChunkUnits);
 #pragma unroll 1
-            for (int m = 0; m < a.um; ++m, dv += a.chunk_step >> 3, d += N)
+            for (int m = 0; m < a.um; ++m, dv += kChunkStep >> 3, d += N)
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk)
                 tc_mma_bf16(d, dv + kk * (a.row8_step >> 3), dp0 + kk * 2, idesc_o, i > 0 || kk > 0);
@@ -501,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int i = st; i < 2 * a.um * per; i += 128) {
               const int k = i / per, r = valid + (i - k * per) / 8;
-              *reinterpret_cast<uint4*>(v + k * a.chunk_step + (r >> 3) * a.row8_step + (r & 7) * 128 + (i & 7) * 16) =
+              *reinterpret_cast<uint4*>(v + k * kChunkStep + (r >> 3) * a.row8_step + (r & 7) * 128 + (i & 7) * 16) =
                   make_uint4(0, 0, 0, 0);
             }
             z.step(a.nlat);
@@ -746,17 +745,19 @@ __global__ void __launch_bounds__(256, kAppendBlocks) mla_append_kernel(const __
 
 namespace {
 
-// The cache's latent columns as [latent / 64][rows][64]: a box is `piece` rows of the `chunks` chunks of a ring slot.
+// The cache's latent columns as [rows / 8][latent / 64][8 rows][64]: a box is `piece` rows of the `chunks` chunks of a
+// ring slot, 8 rows of every chunk after another.
 bool make_tmap_latent(CUtensorMap* m, const void* base, int64_t rows, const moe_mla_config_t* c, int piece, int chunks) {
   const uint64_t pitch = static_cast<uint64_t>(c->latent + c->rope) * 2;
-  return make_tmap_strided(m, base, {64, static_cast<uint64_t>(rows), static_cast<uint64_t>(c->latent / 64)}, {pitch, 128},
-                           {64, static_cast<uint32_t>(piece), static_cast<uint32_t>(chunks)}, 3);
+  return make_tmap_strided(m, base, {64, 8, static_cast<uint64_t>(c->latent / 64), static_cast<uint64_t>(rows / 8)},
+                           {pitch, 128, 8 * pitch},
+                           {64, 8, static_cast<uint32_t>(chunks), static_cast<uint32_t>(piece / 8)}, 4);
 }
 // Whole cache rows; the rope columns are one box of 64, zero past the row's end.
 bool make_tmap_rope(CUtensorMap* m, const void* base, int64_t rows, const moe_mla_config_t* c, int piece) {
   const uint64_t cols = static_cast<uint64_t>(c->latent + c->rope);
-  return make_tmap_strided(m, base, {cols, static_cast<uint64_t>(rows), 1}, {cols * 2, 0},
-                           {64, static_cast<uint32_t>(piece), 1}, 2);
+  return make_tmap_strided(m, base, {cols, static_cast<uint64_t>(rows), 1, 1}, {cols * 2, 0, 0},
+                           {64, static_cast<uint32_t>(piece), 1, 1}, 2);
 }
 
 int validate_mla(const moe_mla_config_t* c) {
@@ -910,13 +911,13 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
   a.nu = a.nm / a.um;
   const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
   a.W = sms / a.G;
-  // Pages of whole tiles: one box a slot, chunk after chunk. Otherwise boxes of 8 tokens, which every page holds
-  // whole, each with its chunks side by side: the products' operands only need a fixed step from 8 rows to the next.
-  a.piece = cfg->page_size % kTile ? 8 : kTile;
-  a.chunk_step = a.piece * 128;
+  // A box takes as many tokens as every page holds whole: 8 to 64, a power of two. Groups of 8 rows, the swizzle's
+  // period, lie one after another in a slot, each with its chunks side by side, so a slot looks alike for every box.
+  a.piece = cfg->page_size & -cfg->page_size;
+  if (a.piece > kTile) a.piece = kTile;
   const bool pair = pair_form(cfg->heads, cfg->latent);
   const int chunks = pair ? a.nm : 2 * a.um;               // 64-column chunks of a ring slot
-  a.row8_step = a.piece == kTile ? 1024 : chunks * 1024;
+  a.row8_step = chunks * kChunkStep;
   a.scale2 = cfg->softmax_scale * kLog2e;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_b = q_stride_b;
@@ -937,9 +938,9 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
   if (!make_tmap_latent(&tk, cache, rows, cfg, a.piece, chunks) || !make_tmap_rope(&tr, cache, rows, cfg, a.piece))
     return MOE_ERR_CUDA;
   if (!make_tmap_strided(&tq, q,
-                         {static_cast<uint64_t>(row), static_cast<uint64_t>(cfg->heads), static_cast<uint64_t>(cfg->batch)},
-                         {static_cast<uint64_t>(q_stride_h) * 2, static_cast<uint64_t>(q_stride_b) * 2},
-                         {64, static_cast<uint32_t>(N), 1}, 3))
+                         {static_cast<uint64_t>(row), static_cast<uint64_t>(cfg->heads), static_cast<uint64_t>(cfg->batch), 1},
+                         {static_cast<uint64_t>(q_stride_h) * 2, static_cast<uint64_t>(q_stride_b) * 2, 0},
+                         {64, static_cast<uint32_t>(N), 1, 1}, 3))
     return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (pair) {

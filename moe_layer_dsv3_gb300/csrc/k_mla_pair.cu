@@ -88,6 +88,13 @@ __device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* m, in
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void pair_load_4d(void* dst, const CUtensorMap* m, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
 
 // 64 rows of 16 bytes to four TMEM columns, in both CTAs, each from its own shared memory: rows 0-31 to lanes 0-31
 // and 64-95, rows 32-63 to lanes 32-63 and 96-127, as the pair instruction reads its 64 rows of A.
@@ -188,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool started = false, ok = true;
 
   // Loads of one token block (0 or 1) of a tile. Lane p: piece p's first row. A page is read a tile ahead of its use.
-  const int pieces = kBlock / a.piece;
+  const int pieces = kBlock / a.piece, piece_step = (a.piece >> 3) * a.row8_step;
   const int oob = a.num_pages * a.page;                    // a row past the cache: reads zeros
   auto page_of = [&](const int32_t* table, int t, int blk, int t1, int len) {
     const int tok = t * kTile + blk * kBlock + lane * a.piece;
@@ -237,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int t = t0; t < t1 && ok; ++t) {
         const int live = live_of(t, rank, len), both = live_of(t, 0, len) + live_of(t, 1, len);
-        const int y = __shfl_sync(0xffffffffu, row, 0);
+        int ys[8];
+        rows_of(row, ys);
 #pragma unroll 1
         for (int u = 0; u < 2 && ok; ++u) {                // half u of the latent columns, the rope columns with half 0
           if (u == 0) ok = warp_wait(&c.ropee[rr.slot], rr.phase ^ 1u, a.status, 163);
@@ -248,15 +256,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t bar = full0 + lr.slot * 8;
           if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(&c.full[lr.slot], both * a.piece * 128 * (hc + (u == 0 ? 1 : 0)));
-            if (pieces == 1 && live) {
-              pair_load_3d(dst, &tma_k, 0, y, hc * u, bar);
-              if (u == 0) pair::tma_load_2d(rdst, &tma_r, a.latent, y, bar);
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+              if (p >= live) break;
+              pair_load_4d(dst + p * piece_step, &tma_k, 0, 0, hc * u, ys[p] >> 3, bar);
+              if (u == 0) pair::tma_load_2d(rdst + p * a.piece * 128, &tma_r, a.latent, ys[p], bar);
             }
-          }
-          __syncwarp();
-          if (pieces > 1 && lane < live) {
-            pair_load_3d(dst + lane * a.row8_step, &tma_k, 0, row, hc * u, bar);
-            if (u == 0) pair::tma_load_2d(rdst + lane * 1024, &tma_r, a.latent, row, bar);
           }
           __syncwarp();
           lr.step(kSlots);
@@ -307,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int t = t0; t < t1 && ok; ++t, ++tile) {
         const int live = live_of(t, blk, len);
-        const int y = __shfl_sync(0xffffffffu, row, 0);
+        int ys[8];
+        rows_of(row, ys);
         const int par = tile & 1;
         ok = warp_wait(&c.sd[par], (phase >> par) & 1u, a.status, 165);
         if (!ok) break;
@@ -315,10 +321,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* dst = lat + slot * slot_bytes;
         if (elect_one()) {
           mbar_arrive_expect_tx(&c.vl[par], live * a.piece * 128 * hc);
-          if (pieces == 1 && live) tma_load_3d(dst, &tma_k, 0, y, hc * rank, &c.vl[par]);
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            if (p >= live) break;
+            tma_load_4d(dst + p * piece_step, &tma_k, 0, 0, hc * rank, ys[p] >> 3, &c.vl[par]);
+          }
         }
-        __syncwarp();
-        if (pieces > 1 && lane < live) tma_load_3d(dst + lane * a.row8_step, &tma_k, 0, row, hc * rank, &c.vl[par]);
         __syncwarp();
         slot += 2;
         if (slot >= kSlots) slot -= kSlots;
@@ -385,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               };
               const uint64_t dl = dl0 + lr.slot * (slot_bytes >> 4);
 #pragma unroll 1
-              for (int k = 0; k < hc; ++k) chunk(u * hc + k, dl + k * (a.chunk_step >> 4), u + k == 0);
+              for (int k = 0; k < hc; ++k) chunk(u * hc + k, dl + k * (kChunkStep >> 4), u + k == 0);
               if (u == 0) {
                 chunk(nchunk - 1, dr0 + rr.slot * (kChunk >> 4), false);
                 pair::tc_commit_mc(&c.ropee[rr.slot], 0x3);
@@ -408,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Issues O^T.
       constexpr uint32_t idesc = idesc_bf16(256, 128) | (1u << 15);   // A (V^T) is MN-major
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint64_t dp0 = desc_kmajor_sw128(smem_u32(sp)), dv0 = smem_desc(smem_u32(lat), a.chunk_step, a.row8_step, 2);
+      const uint64_t dp0 = desc_kmajor_sw128(smem_u32(sp)), dv0 = smem_desc(smem_u32(lat), kChunkStep, a.row8_step, 2);
       Ring lr;
       uint32_t pphase = 0, ophase = 0;
       while (ok && wk.next(a, started)) {
@@ -428,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint64_t dv = dv0 + slot * (slot_bytes >> 4);
               uint32_t d = tm;
 #pragma unroll 1
-              for (int m = 0; m < mt; ++m, dv += a.chunk_step >> 3, d += 128)
+              for (int m = 0; m < mt; ++m, dv += kChunkStep >> 3, d += 128)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                   mma2_ss(d, dv + kk * (a.row8_step >> 3), dp0 + blk * (kChunk >> 4) + kk * 2, idesc, i > 0 || blk + kk > 0);
@@ -592,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int i = st; i < hc * per; i += kSoft) {
               const int k = i / per, row = first + (i - k * per) / 8;
-              *reinterpret_cast<uint4*>(v + k * a.chunk_step + (row >> 3) * a.row8_step + (row & 7) * 128 + (i & 7) * 16) =
+              *reinterpret_cast<uint4*>(v + k * kChunkStep + (row >> 3) * a.row8_step + (row & 7) * 128 + (i & 7) * 16) =
                   make_uint4(0, 0, 0, 0);
             }
             if (++slot == kSlots) slot = 0;
