@@ -39,7 +39,7 @@ constexpr int kThreads = 224;
 constexpr int kTile = kBlock;             // cached tokens per tile
 constexpr int kAppendBlocks = 3;          // resident blocks an SM: 32768 tokens in 17.4 us; 4 spill and take 20.7
 constexpr int kMaxLatSlots = 12;
-constexpr int kMaxRopeSlots = 3;
+constexpr int kMaxRopeSlots = kMaxLatSlots;
 constexpr int kMinTiles = 3;              // fewest tiles of a worker: 24 tiles took 18.4 us at 3, 20.5 at 2 and 4
 
 struct Smem {
@@ -138,26 +138,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring lr, rr;
     uint32_t qphase = 0;
     int issued = 0, issued_q = 0;
+    BoxRows<kTile> rows;
     const int pieces = kTile / a.piece;
     const int piece_step = (a.piece >> 3) * a.row8_step;
-    const int oob = a.num_pages * a.page;               // a row past the cache: reads zeros
     const int h0 = g * a.hg;
     while (ok && wk.next(a, started)) {
       const int b = __shfl_sync(0xffffffffu, wk.b, 0), len = __shfl_sync(0xffffffffu, wk.len, 0);
       const int t0 = __shfl_sync(0xffffffffu, wk.t0, 0), t1 = t0 + __shfl_sync(0xffffffffu, wk.n, 0);
-      // Lane p: page of piece p of tile t, and its first row. Pages are read a tile ahead of their use.
-      const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
-      auto page_of = [&](int t) {
-        const int tok = t * kTile + lane * a.piece;
-        return (lane < pieces && t < t1 && tok < len) ? __ldg(table + tok / a.page) : 0;
-      };
-      auto row_of = [&](int t, int page) {
-        const int tok = t * kTile + lane * a.piece;
-        if (page >= 0 && page < a.num_pages) return page * a.page + tok % a.page;
-        report_error(a.status, kErrBounds, 62);
-        return oob;
-      };
-      int page = page_of(t0);
+      rows.start(a, b, t0, t1, 0, len);
       // Q of this sequence and head group, once the previous piece's products have read the last one.
       ok = warp_wait(&c.qe, qphase ^ 1u, a.status, 61);
       if (!ok) break;
@@ -169,14 +157,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       qphase ^= 1u;
       ++issued_q;
-      int row = row_of(t0, page);
-      page = page_of(t0 + 1);
+      rows.turn(a, t0);
 #pragma unroll 1
       for (int t = t0; t < t1 && ok; ++t) {
         const int left = len - t * kTile;
         const int live = left >= kTile ? pieces : (left + a.piece - 1) / a.piece;   // pieces with tokens
         int ys[8];
-        rows_of(row, ys);
+        rows.get(a, t, ys);
 #pragma unroll 1
         for (int u = 0; u < a.nu && ok; ++u) {           // a slot of latent columns, the rope columns with the first
           if (u == 0) ok = warp_wait(&c.ropee[rr.slot], rr.phase ^ 1u, a.status, 63);
@@ -200,8 +187,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++issued;
         }
         rr.step(a.nrope);
-        row = row_of(t + 1, page);
-        page = page_of(t + 2);
       }
       wk.done();
     }
@@ -809,9 +794,12 @@ int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CU
   // a row past 64 * nchunk columns does not exist: a rope part under 64 columns is zero-filled by its TMA box only
   a.nts = Plan<N>::kMaxTs < nchunk - 1 ? Plan<N>::kMaxTs : (a.rope == 64 && Plan<N>::kMaxTs >= nchunk ? nchunk : nchunk - 1);
   const int fixed = 1024 + kBarBytes + kMaxHeadsCta * 4 + (nchunk - a.nts) * N * 128 + N * 128;
-  a.nrope = N <= 32 ? 3 : 2;
-  const int slot_bytes = a.um * 2 * kChunk;
-  a.nlat = (kSmemMax - fixed - a.nrope * kChunk) / slot_bytes;
+  // The ring: rope slots for as many whole tiles as fit, latent slots in the rest (3 and 6 at 512 + 64 columns and few
+  // heads, 9 and 9 at 128 + 64).
+  const int slot_bytes = a.um * 2 * kChunk, ring = kSmemMax - fixed;
+  a.nrope = ring / (a.nu * slot_bytes + kChunk);
+  if (a.nrope > kMaxRopeSlots) a.nrope = kMaxRopeSlots;
+  a.nlat = (ring - a.nrope * kChunk) / slot_bytes;
   if (a.nlat > kMaxLatSlots) a.nlat = kMaxLatSlots;
   const int smem = fixed + a.nrope * kChunk + a.nlat * slot_bytes;
   launch_kernel_after("mla_decode", mla_decode_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(kThreads), smem, s, tk, tr, tq,

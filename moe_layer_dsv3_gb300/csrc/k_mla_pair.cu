@@ -194,19 +194,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   wk.left = r.f1 - r.f0;
   bool started = false, ok = true;
 
-  // Loads of one token block (0 or 1) of a tile. Lane p: piece p's first row. A page is read a tile ahead of its use.
+  // Loads of one token block (0 or 1) of a tile.
   const int pieces = kBlock / a.piece, piece_step = (a.piece >> 3) * a.row8_step;
-  const int oob = a.num_pages * a.page;                    // a row past the cache: reads zeros
-  auto page_of = [&](const int32_t* table, int t, int blk, int t1, int len) {
-    const int tok = t * kTile + blk * kBlock + lane * a.piece;
-    return (lane < pieces && t < t1 && tok < len) ? __ldg(table + tok / a.page) : 0;
-  };
-  auto row_of = [&](int t, int blk, int page) {
-    const int tok = t * kTile + blk * kBlock + lane * a.piece;
-    if (page >= 0 && page < a.num_pages) return page * a.page + tok % a.page;
-    report_error(a.status, kErrBounds, 62);
-    return oob;
-  };
+  BoxRows<kTile> rows;
   // Pieces of block blk of tile t that hold tokens.
   auto live_of = [&](int t, int blk, int len) {
     const int left = len - t * kTile - blk * kBlock;
@@ -220,8 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && wk.next(a, started)) {
       const int b = __shfl_sync(0xffffffffu, wk.b, 0), len = __shfl_sync(0xffffffffu, wk.len, 0);
       const int t0 = __shfl_sync(0xffffffffu, wk.t0, 0), t1 = t0 + __shfl_sync(0xffffffffu, wk.n, 0);
-      const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
-      int page = page_of(table, t0, rank, t1, len);
+      rows.start(a, b, t0, t1, rank * kBlock, len);
       // The chunks of Q for TMEM pass through ring slots ahead of the piece's tiles.
 #pragma unroll 1
       for (int u = 0; u < nq && ok; ++u) {
@@ -239,13 +228,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++issued;
       }
       if (!ok) break;
-      int row = row_of(t0, rank, page);
-      page = page_of(table, t0 + 1, rank, t1, len);
+      rows.turn(a, t0);
 #pragma unroll 1
       for (int t = t0; t < t1 && ok; ++t) {
         const int live = live_of(t, rank, len), both = live_of(t, 0, len) + live_of(t, 1, len);
         int ys[8];
-        rows_of(row, ys);
+        rows.get(a, t, ys);
 #pragma unroll 1
         for (int u = 0; u < 2 && ok; ++u) {                // half u of the latent columns, the rope columns with half 0
           if (u == 0) ok = warp_wait(&c.ropee[rr.slot], rr.phase ^ 1u, a.status, 163);
@@ -268,8 +256,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++issued;
         }
         rr.step(kRopeSlots);
-        row = row_of(t + 1, rank, page);
-        page = page_of(table, t + 2, rank, t1, len);
       }
       wk.done();
     }
@@ -293,8 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && wk.next(a, started)) {
       const int b = __shfl_sync(0xffffffffu, wk.b, 0), len = __shfl_sync(0xffffffffu, wk.len, 0);
       const int t0 = __shfl_sync(0xffffffffu, wk.t0, 0), t1 = t0 + __shfl_sync(0xffffffffu, wk.n, 0);
-      const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
-      int page = page_of(table, t0, blk, t1, len);
+      rows.start(a, b, t0, t1, blk * kBlock, len);
       // Chunks of Q in shared memory, once the previous piece's products have read the last ones.
       ok = warp_wait(&c.qe, qphase ^ 1u, a.status, 167);
       if (!ok) break;
@@ -307,13 +292,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       qphase ^= 1u;
       ++issued_q;
       slot = (slot + nq) % kSlots;
-      int row = row_of(t0, blk, page);
-      page = page_of(table, t0 + 1, blk, t1, len);
+      rows.turn(a, t0);
 #pragma unroll 1
       for (int t = t0; t < t1 && ok; ++t, ++tile) {
         const int live = live_of(t, blk, len);
         int ys[8];
-        rows_of(row, ys);
+        rows.get(a, t, ys);
         const int par = tile & 1;
         ok = warp_wait(&c.sd[par], (phase >> par) & 1u, a.status, 165);
         if (!ok) break;
@@ -330,8 +314,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         slot += 2;
         if (slot >= kSlots) slot -= kSlots;
-        row = row_of(t + 1, blk, page);
-        page = page_of(table, t + 2, blk, t1, len);
       }
       wk.done();
     }

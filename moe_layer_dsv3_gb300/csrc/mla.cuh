@@ -239,13 +239,47 @@ __device__ __forceinline__ bool barrier_or(int id, bool flag) {
   return r != 0;
 }
 
-// The first rows of a tile's pieces, from lane p for piece p to every lane: the issuing lane then has them in registers.
-// At 8 boxes of 8 tokens that is faster than a lane per box (83 x 4955 tokens, one head: 84.6 and 87.3 us; a loop with a
-// shuffle before each box took 119).
-__device__ __forceinline__ void rows_of(int row, int (&ys)[8]) {
+// Cache rows of the TMA boxes that one warp loads of a sequence: `pieces` boxes of a block of 64 tokens a tile. Lane l
+// holds the first row of box l % pieces of the l / pieces-th tile from `tb` on, so one read of the page table serves 32
+// boxes, and the pages of the next 32 are read while these are used.
+template <int TILE>
+struct BoxRows {
+  const int32_t* table;
+  int pieces;
+  int first, len, t1;        // first token of the block in a tile; the sequence's tokens; end of the walked tiles
+  int tb, row, page, rest;   // page, rest: the next batch
+  __device__ __forceinline__ void fetch(const MlaArgs& a, int t) {
+    const int lane = threadIdx.x & 31;
+    const int tile = t + lane / pieces, tok = tile * TILE + first + lane % pieces * a.piece, at = tok / a.page;
+    rest = tok - at * a.page;
+    page = tile < t1 && tok < len ? __ldg(table + at) : 0;
+  }
+  __device__ __forceinline__ void turn(const MlaArgs& a, int t) {
+    tb = t;
+    if (page >= 0 && page < a.num_pages) {
+      row = page * a.page + rest;
+    } else {
+      report_error(a.status, kErrBounds, 62);
+      row = a.num_pages * a.page;                          // past the cache: reads zeros
+    }
+    fetch(a, t + a.piece / 2);                             // 32 boxes are piece / 2 tiles
+  }
+  __device__ __forceinline__ void start(const MlaArgs& a, int b, int t0, int t1_, int first_, int len_) {
+    table = a.table + static_cast<int64_t>(b) * a.max_pages;
+    pieces = kBlock / a.piece;
+    first = first_;
+    len = len_;
+    t1 = t1_;
+    fetch(a, t0);
+  }
+  // The rows of tile t's boxes, in every lane: the issuing lane then has them in registers. At 8 boxes of 8 tokens that
+  // is faster than a lane per box (83 x 4955 tokens, one head: 84.6 and 87.3 us; a shuffle before each box took 119).
+  __device__ __forceinline__ void get(const MlaArgs& a, int t, int (&ys)[8]) {
+    if (t - tb == a.piece / 2) turn(a, t);
 #pragma unroll
-  for (int p = 0; p < 8; ++p) ys[p] = __shfl_sync(0xffffffffu, row, p);
-}
+    for (int p = 0; p < 8; ++p) ys[p] = __shfl_sync(0xffffffffu, row, (t - tb) * pieces + p);
+  }
+};
 
 // Ring position: slot index and the parity of its current use.
 struct Ring {
