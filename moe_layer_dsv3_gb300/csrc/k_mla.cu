@@ -805,7 +805,7 @@ int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CU
   launch_kernel_after("mla_decode", mla_decode_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(kThreads), smem, s, tk, tr, tq,
                 a);
   if (int e = call_error() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA) return e;
-  launch_join<N, false>(a, sms, s);
+  launch_join<N, false, kTile, kMinTiles>(a, sms, s);
   return MOE_OK;
 }
 

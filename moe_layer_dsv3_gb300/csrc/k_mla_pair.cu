@@ -705,26 +705,10 @@ int run_decode_pair(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, con
   a.nts = kMaxTs < nchunk - 1 ? kMaxTs : (a.rope == 64 && kMaxTs >= nchunk ? nchunk : nchunk - 1);
   const size_t smem = 1024 + static_cast<size_t>(nchunk - a.nts + 2 + kSlots * hc + kRopeSlots) * kChunk + kBarBytes +
                       kFloats * sizeof(float);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(static_cast<unsigned>(2 * a.W));
-  lc.blockDim = dim3(kThreads);
-  lc.dynamicSmemBytes = smem;
-  lc.stream = s;
-  lc.attrs = attr;
-  lc.numAttrs = 2;
-  {
-    Prof prof("mla_decode_pair", s);
-    note(cudaLaunchKernelEx(&lc, mla_decode_pair_kernel, tk, tr, tq, a));
-  }
+  launch_cluster_after("mla_decode_pair", mla_decode_pair_kernel, dim3(static_cast<unsigned>(2 * a.W)), 2, dim3(kThreads),
+                       smem, s, tk, tr, tq, a);
   if (call_error() != cudaSuccess) return MOE_ERR_CUDA;
-  launch_join<128, true>(a, sms, s);
+  launch_join<128, true, kTile, kMinTiles>(a, sms, s);
   return MOE_OK;
 }
 

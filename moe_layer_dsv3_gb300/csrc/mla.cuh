@@ -153,6 +153,20 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, ui
                : "memory");
 }
 
+// CTAs of this cluster.
+__device__ __forceinline__ uint32_t num_ctas() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Stores to shared memory of a CTA of the cluster.
+__device__ __forceinline__ void st_cluster(uint32_t addr, const float4& v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, const float2& v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
+}
+
 // 3-D tiled load (q: columns, heads, sequences).
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
   asm volatile(
@@ -357,30 +371,44 @@ __device__ __forceinline__ int4 join_entry(const Control& c, const Range& r, int
 
 // Joins the pieces of the sequences that the work split cut. An item is 8 heads and
 // 128 latent columns of one cut sequence, for 128 threads: a warp takes 32 columns,
-// in the register order in which the pieces were stored. Half a block takes an item
-// with few pieces alone; of a long list the halves take every other piece each, four
-// in flight, and their sums are added in order, so that it costs a few rounds of
-// latency (76 pieces of 2 x 131072 tokens: 7 us; one by one it took 17 us). The order
-// of additions depends on the number of pieces only.
+// in the register order in which the pieces were stored. Bound by the latency of
+// dependent rounds of loads, four pieces each. So half a block takes an item with a
+// short list alone, and of a long one the half blocks of a cluster take every group-th
+// piece each, and their sums are added in order. What counts as short depends on how
+// many items there are: where they fill the grid, two or three rounds in a row cost
+// less than meeting (37 x 700 tokens, 20 heads: 22.7 us for the call with 12 pieces,
+// 23.7 with 4); where they do not, the halves meet earlier (1500 tokens: 14.1, 14.5).
+// The order of additions depends on the lengths only.
 // A worker is one CTA of a head group with all latent columns, or (PAIR) a pair of
 // CTAs, each with all heads and half of the columns.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinBlocks = 2;             // blocks an SM (4 and 8 took the same time or 1 % more)
-constexpr int kJoinFew = 4;                // pieces that a half block adds alone
+constexpr int kJoinBlocks = 2;             // blocks an SM
+constexpr int kJoinFew = 4, kJoinFewFull = 12;   // pieces that a half block adds alone: in general, and if items fill the grid
+// Where a sequence can have many pieces and items are few, a cluster of four blocks shares an item: 46 -> 34 us for
+// 100000 tokens of 16 heads. At up to 32 pieces it costs more than it gives (8 pieces of 1500 tokens: 13.8 -> 15.1 us).
+constexpr int kJoinCluster = 4;
+constexpr int kJoinLong = 32;
+struct JoinPart {
+  float4 sum[2][128];
+  float2 stat[3][4];                       // of the heads of lane % 4
+};
 template <int N, bool PAIR>
 __global__ void __launch_bounds__(kJoinThreads, 2) mla_join_kernel(const __grid_constant__ MlaArgs a) {
   constexpr int NP = N / 8, kHeads = PAIR ? 2 * kMaxHeadsCta : kMaxHeadsCta;
   __shared__ int4 list[kMaxSms];           // entries with few pieces from the front, the others from the back
   __shared__ int2 counts[kMaxSms / 32];
-  __shared__ float4 sum[2][128];
-  __shared__ float2 stat[3][128];
+  extern __shared__ uint8_t smem_raw[];
+  JoinPart* parts = reinterpret_cast<JoinPart*>(smem_raw);  // first block of the cluster: the other half blocks' sums
   const int tid = threadIdx.x, lane = tid & 31, half = tid >> 7, t = tid & 127, q = t >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the decode kernel's writes are visible
   // The workers that end a cut sequence: one thread looks at each.
   static_assert(kMaxSms % 32 == 0 && kMaxSms <= kJoinThreads, "one pass over the workers");
   const int4 e = tid < a.W ? a.join[tid] : make_int4(0, 0, 0, 0);
-  const uint32_t bf = __ballot_sync(0xffffffffu, e.w != 0 && e.w <= kJoinFew);
-  const uint32_t bm = __ballot_sync(0xffffffffu, e.w > kJoinFew);
+  const int per = PAIR ? 2 : a.G, cols = a.latent / (PAIR ? 256 : 128);
+  const int each = per * cols * NP;                         // items of an entry
+  const int alone = __syncthreads_count(e.w != 0) * each > static_cast<int>(gridDim.x) ? kJoinFewFull : kJoinFew;
+  const uint32_t bf = __ballot_sync(0xffffffffu, e.w != 0 && e.w <= alone);
+  const uint32_t bm = __ballot_sync(0xffffffffu, e.w > alone);
   if (lane == 0 && tid < kMaxSms) counts[tid >> 5] = make_int2(__popc(bf), __popc(bm));
   __syncthreads();
   int few = 0, many = 0, few_at = __popc(bf & ((1u << lane) - 1u)), many_at = __popc(bm & ((1u << lane) - 1u));
@@ -394,10 +422,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) mla_join_kernel(const __grid_
     few += c.x;
     many += c.y;
   }
-  if (e.w != 0) list[e.w <= kJoinFew ? few_at : kMaxSms - 1 - many_at] = e;
+  if (e.w != 0) list[e.w <= alone ? few_at : kMaxSms - 1 - many_at] = e;
   __syncthreads();
-  const int per = PAIR ? 2 : a.G, cols = a.latent / (PAIR ? 256 : 128);
-  const int each = per * cols * NP;                         // items of an entry
 
   float2 top, l, le;                                        // of heads h and h + 1: reference, sums
   float4 s0, s1;
@@ -470,21 +496,35 @@ __global__ void __launch_bounds__(kJoinThreads, 2) mla_join_kernel(const __grid_
     gather(j, g, m, i, 0, 1);
     store(j, g, m, i);
   }
-  for (int it = blockIdx.x; it < many * each; it += gridDim.x) {
+  // Long lists: the half blocks of a cluster take every group-th piece each.
+  const int nc = static_cast<int>(num_ctas()), groups = 2 * nc, group = 2 * static_cast<int>(pair::cta_rank()) + half;
+#pragma unroll 1
+  for (int it = static_cast<int>(pair::cluster_id()); it < many * each; it += static_cast<int>(pair::num_clusters())) {
     const int i = it % NP, m = it / NP % cols, g = it / (NP * cols) % per;
     const int4 j = list[kMaxSms - 1 - it / each];
-    gather(j, g, m, i, half, 2);
-    __syncthreads();                                        // the place of the second half's sums is free
-    if (half == 1) {
-      sum[0][t] = s0;
-      sum[1][t] = s1;
-      stat[0][t] = top;
-      stat[1][t] = l;
-      stat[2][t] = le;
+    gather(j, g, m, i, group, groups);
+    if (nc > 1) pair::cluster_sync();                       // the place of the sums is free
+    else __syncthreads();
+    if (group > 0) {
+      const uint32_t to = pair::map_rank(smem_u32(&parts[group - 1]), 0);
+      st_cluster(to + t * sizeof(float4), s0);
+      st_cluster(to + (128 + t) * sizeof(float4), s1);
+      if (t < 4) {
+        const uint32_t st = to + offsetof(JoinPart, stat) + t * sizeof(float2);
+        st_cluster(st, top);
+        st_cluster(st + 4 * sizeof(float2), l);
+        st_cluster(st + 8 * sizeof(float2), le);
+      }
     }
-    __syncthreads();
-    if (half == 0) {
-      add(stat[0][t], stat[1][t], stat[2][t], sum[0][t], sum[1][t]);
+    if (nc > 1) pair::cluster_sync();
+    else __syncthreads();
+    if (group == 0) {
+      const int n = j.w < groups ? j.w : groups;
+#pragma unroll 1
+      for (int k = 0; k < n - 1; ++k) {
+        const JoinPart& p = parts[k];
+        add(p.stat[0][lane & 3], p.stat[1][lane & 3], p.stat[2][lane & 3], p.sum[0][t], p.sum[1][t]);
+      }
       store(j, g, m, i);
     }
   }
@@ -492,11 +532,17 @@ __global__ void __launch_bounds__(kJoinThreads, 2) mla_join_kernel(const __grid_
 
 // The join of a decode launch just made on the same stream. Its blocks start when the last decode CTAs leave room and
 // wait for their writes on the device.
-template <int N, bool PAIR>
+template <int N, bool PAIR, int TILE, int MIN_TILES>
 void launch_join(const MlaArgs& a, int sms, cudaStream_t s) {
-  const int64_t most = static_cast<int64_t>(a.W) * (PAIR ? 2 : a.G) * (a.latent / (PAIR ? 256 : 128)) * (N / 8);
-  const int64_t grid = most < kJoinBlocks * sms ? most : kJoinBlocks * sms;
-  launch_kernel_after("mla_join", mla_join_kernel<N, PAIR>, dim3(static_cast<unsigned>(grid)), dim3(kJoinThreads), 0, s, a);
+  const int64_t each = (PAIR ? 2 : a.G) * (a.latent / (PAIR ? 256 : 128)) * (N / 8);
+  const int64_t most = a.B < a.W ? a.B : a.W;               // sequences that can be cut
+  const int64_t tiles = ceil_div(static_cast<int64_t>(a.max_pages) * a.page, TILE);
+  const int64_t slots = static_cast<int64_t>(kJoinBlocks) * sms;
+  const int64_t pieces = tiles / MIN_TILES < a.W ? tiles / MIN_TILES : a.W;
+  const int cluster = pieces > kJoinLong && most * each * kJoinCluster <= slots ? kJoinCluster : 1;
+  const int64_t grid = most * each * cluster < slots ? most * each * cluster : slots;
+  launch_cluster_after("mla_join", mla_join_kernel<N, PAIR>, dim3(static_cast<unsigned>(grid)), cluster,
+                       dim3(kJoinThreads), (2 * cluster - 1) * sizeof(JoinPart), s, a);
 }
 
 // Decode with both head groups on one pair of CTAs (more than 64 heads, an even number of 128-column tiles), and
