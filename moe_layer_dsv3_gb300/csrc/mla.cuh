@@ -491,8 +491,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2) mla_join_kernel(const __grid_
   };
 
   for (int it = blockIdx.x * 2 + half; it < few * each; it += gridDim.x * 2) {
-    const int i = it % NP, m = it / NP % cols, g = it / (NP * cols) % per;
-    const int4 j = list[it / each];
+    const int n = it / each, mg = (it - n * each) / NP, i = it % NP;
+    const int g = mg >= cols ? 1 : 0, m = mg - g * cols;   // (at most two head groups or column halves)
+    const int4 j = list[n];
     gather(j, g, m, i, 0, 1);
     store(j, g, m, i);
   }
@@ -500,8 +501,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2) mla_join_kernel(const __grid_
   const int nc = static_cast<int>(num_ctas()), groups = 2 * nc, group = 2 * static_cast<int>(pair::cta_rank()) + half;
 #pragma unroll 1
   for (int it = static_cast<int>(pair::cluster_id()); it < many * each; it += static_cast<int>(pair::num_clusters())) {
-    const int i = it % NP, m = it / NP % cols, g = it / (NP * cols) % per;
-    const int4 j = list[kMaxSms - 1 - it / each];
+    const int e = it / each, mg = (it - e * each) / NP, i = it % NP;
+    const int g = mg >= cols ? 1 : 0, m = mg - g * cols;
+    const int4 j = list[kMaxSms - 1 - e];
     gather(j, g, m, i, group, groups);
     if (nc > 1) pair::cluster_sync();                       // the place of the sums is free
     else __syncthreads();
