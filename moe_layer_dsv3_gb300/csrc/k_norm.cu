@@ -8,9 +8,10 @@
 // Both directions move each element once and compute a dozen operations on
 // it, so HBM bounds them: a row stays on chip (in registers forward, in shared
 // memory backward, where rows arrive ahead of their turn) between its reduction
-// and its outputs. Measured at 16384 x 7168: forward with residual and codes 152 us
-// (1.06 GB, 1.03 of the copy rate), backward 134 us (0.94 GB, 1.03). Sums, rstd and dgamma are held in fp32; h, y and dx are rounded
-// to bf16 once, at the store. The codes are MX of the rounded y: the layer's
+// and its outputs. Measured at 16384 x 7168: forward with residual and codes 151 us
+// (1.06 GB, 1.04 of the copy rate), backward 135 us (0.94 GB, 1.03); one row forward
+// takes 2.5 us on the device. Sums, rstd and dgamma are held in fp32; h, y and dx are
+// rounded to bf16 once, at the store. The codes are MX of the rounded y: the layer's
 // experts then read the same bytes as if they had quantised the bf16 rows.
 #include "moe_internal.h"
 #include "mx.cuh"
@@ -317,7 +318,10 @@ constexpr int kWarpsPerCta = 8;
 constexpr int bwd_smem(int stages, int vectors, int threads) { return stages * 3 * vectors * threads * 16; }
 
 // Launch shape of the gradient. A row of up to 1024 columns takes a warp (16 rows a
-// CTA), a wider one a CTA with 2 vectors a thread up to 8192 columns and 4 beyond.
+// CTA: 16384 x 1024 took 41 us with 8 and takes 27), a wider one a CTA with 2 vectors a
+// thread up to 8192 columns and 4 beyond. With 4, h and dy are read again from shared
+// memory after the reduction (2000 x 16384: 62 us with them in registers, 48 without);
+// with 2 they stay in registers (11982 x 4480: 79 us read again, 74 kept).
 // Rows in flight and CTAs an SM fill its shared memory, but no more CTAs than keep
 // about 8192 columns in work: each leaves a partial of dgamma, and 2 CTAs of 4480
 // columns took 82 us where 1 takes 74 (11982 rows).
