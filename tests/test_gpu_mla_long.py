@@ -23,6 +23,8 @@ LONG = {
     "two_long_one_short": dict(lens=[12000, 1, 9000], H=16, latent=256, page=16),
     "two_groups": dict(lens=[20000, 64], H=100, latent=384),
     "lists_fill_the_grid": dict(lens=[3000 + 17 * i for i in range(40)], H=20),
+    "short_lists_of_a_pair": dict(lens=[700 + 13 * i for i in range(40)], H=127),
+    "short_lists_of_64_heads": dict(lens=[800 + 7 * i for i in range(130)], H=63, latent=256, page=32),
     "long_lists_fill_the_grid": dict(lens=[9000, 9001, 9002, 9003, 9004, 9005, 9006], H=128),
 }
 
