@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t qphase = 0;
     int issued = 0, issued_q = 0;
     BoxRows<kTile> rows;
-    const int pieces = kTile / a.piece;
+    const int pieces = kTile >> a.piece_log;
     const int piece_step = (a.piece >> 3) * a.row8_step;
     const int h0 = g * a.hg;
     while (ok && wk.next(a, started)) {
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int t = t0; t < t1 && ok; ++t) {
         const int left = len - t * kTile;
-        const int live = left >= kTile ? pieces : (left + a.piece - 1) / a.piece;   // pieces with tokens
+        const int live = left >= kTile ? pieces : (left + a.piece - 1) >> a.piece_log;   // pieces with tokens
         int ys[8];
         rows.get(a, t, ys);
 #pragma unroll 1
@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kChunkUnits = kChunk >> 4;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t dp0 = desc_kmajor_sw128(smem_u32(sp)), dv0 = smem_desc(smem_u32(lat), kChunkStep, a.row8_step, 2);
+    if (lane == 0 && g == 0) a.join[w] = join_entry<kTile>(c, r, w);
     Ring lr;
     uint32_t pphase = 0, ophase = 0;
     while (ok && wk.next(a, started)) {
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             l[k] *= corr;
             le[k] *= corr;
             ref[k] = m;
-            if ((lane & 3) == 0) fac[hr + 8 * k] = corr;
+            if (ti > 0 && (lane & 3) == 0) fac[hr + 8 * k] = corr;
           }
           take(x, p, ls, les);
         }
@@ -450,27 +451,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           pphase ^= 1u;
         }
         any_tile = true;
-        if (grow) {
+        if (grow && ti > 0) {
           named_barrier(3, 128);                           // fac is written
-          if (ti > 0) {
-            tc_fence_after();
+          tc_fence_after();
 #pragma unroll 1
-            for (int m = 0; m < nm; ++m)
+          for (int m = 0; m < nm; ++m)
 #pragma unroll 1
-              for (int hc = 0; hc < N; hc += 16) {
-                uint32_t o[16];
-                const uint32_t at = tmem + tlane + m * N + hc;
-                tmem_ld_32x32b_x16(at, o);
-                tmem_wait_ld();
+            for (int hc = 0; hc < N; hc += 16) {
+              uint32_t o[16];
+              const uint32_t at = tmem + tlane + m * N + hc;
+              tmem_ld_32x32b_x16(at, o);
+              tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  reg_fence(o[j]);
-                  o[j] = __float_as_uint(__uint_as_float(o[j]) * fac[hc + j]);
-                }
-                tmem_st_32x32b_x16(at, o);
+              for (int j = 0; j < 16; ++j) {
+                reg_fence(o[j]);
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * fac[hc + j]);
               }
-            tmem_wait_st();
-          }
+              tmem_st_32x32b_x16(at, o);
+            }
+          tmem_wait_st();
         }
         if (active) {
           const int h = 16 * q + (lane & 15);              // lanes 0-7, 8-15: rows of the first two blocks; 16-31: the next token block
@@ -545,49 +544,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint8_t* stage = sp + q * (N * 32);                  // [N heads][16 columns] of this warp, over P
       __nv_bfloat16* out = a.out + (static_cast<int64_t>(wk.b) * a.H + head0) * a.latent;
       float4* part = reinterpret_cast<float4*>(a.part_o + static_cast<int64_t>(slot) * kMaxHeadsCta * a.latent) + q * 32 + lane;
+      constexpr int kAtOnce = N <= 32 ? 2 : 1;             // blocks read from TMEM at once
 #pragma unroll 1
-      for (int mh = 0; mh < 2 * nm; ++mh) {
-        uint32_t o[4 * NP];
+      for (int mh0 = 0; mh0 < 2 * nm; mh0 += kAtOnce) {
+        uint32_t ob[kAtOnce][4 * NP];
 #pragma unroll
-        for (int i = 0; i < NP; i += 2)
-          tmem_ld_16x256b_x2(tmem + tlane + (static_cast<uint32_t>(mh & 1) << 20) + (mh >> 1) * N + 8 * i, o + 4 * i);
+        for (int b = 0; b < kAtOnce; ++b)
+#pragma unroll
+          for (int i = 0; i < NP; i += 2)
+            tmem_ld_16x256b_x2(tmem + tlane + (static_cast<uint32_t>((mh0 + b) & 1) << 20) + ((mh0 + b) >> 1) * N + 8 * i,
+                               ob[b] + 4 * i);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 4 * NP; ++i) reg_fence(o[i]);
-        if (whole) {
-          // Normalised, rounded and turned through shared memory: two lanes then store 32 bytes of a head.
+        for (int b = 0; b < kAtOnce; ++b) {
+          uint32_t (&o)[4 * NP] = ob[b];
+          const int mh = mh0 + b;
 #pragma unroll
-          for (int i = 0; i < NP; i += 2) {
-            uint32_t w[4];
+          for (int i = 0; i < 4 * NP; ++i) reg_fence(o[i]);
+          if (whole) {
+            // Normalised, rounded and turned through shared memory: two lanes then store 32 bytes of a head.
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack_bf16x2(__uint_as_float(o[4 * i + 2 * k]) * f[i + (k >> 1)].x,
-                                 __uint_as_float(o[4 * i + 2 * k + 1]) * f[i + (k >> 1)].y);
-            const int h = 8 * (i + (lane >> 4)) + (lane & 7);
-            stmatrix_x4_trans(smem_u32(stage) + h * 32 + ((((lane >> 3) ^ (h >> 2)) & 1) << 4), w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < NP; i += 2) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w[k] = pack_bf16x2(__uint_as_float(o[4 * i + 2 * k]) * f[i + (k >> 1)].x,
+                                   __uint_as_float(o[4 * i + 2 * k + 1]) * f[i + (k >> 1)].y);
+              const int h = 8 * (i + (lane >> 4)) + (lane & 7);
+              stmatrix_x4_trans(smem_u32(stage) + h * 32 + ((((lane >> 3) ^ (h >> 2)) & 1) << 4), w[0], w[1], w[2], w[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < N / 16; ++k) {
+              const int h = 16 * k + (lane >> 1), ch = lane & 1;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + h * 32 + (((ch ^ (h >> 2)) & 1) << 4));
+              if (h < nh)
+                *reinterpret_cast<uint4*>(out + h * a.latent + (mh >> 1) * 128 + q * 32 + (mh & 1) * 16 + ch * 8) = v;
+            }
+            __syncwarp();
+          } else {
+            // A partial keeps this register order: every store is 512 bytes in a row.
+#pragma unroll
+            for (int i = 0; i < NP; ++i)
+              part[(mh * NP + i) * 128] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                      __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
           }
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < N / 16; ++k) {
-            const int h = 16 * k + (lane >> 1), ch = lane & 1;
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + h * 32 + (((ch ^ (h >> 2)) & 1) << 4));
-            if (h < nh)
-              *reinterpret_cast<uint4*>(out + h * a.latent + (mh >> 1) * 128 + q * 32 + (mh & 1) * 16 + ch * 8) = v;
-          }
-          __syncwarp();
-        } else {
-          // A partial keeps this register order: every store is 512 bytes in a row.
-#pragma unroll
-          for (int i = 0; i < NP; ++i)
-            part[(mh * NP + i) * 128] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                                    __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
         }
       }
       tc_fence_before();
       mbar_arrive(&c.oe);
       wk.done();
     }
-    if (st == 0 && g == 0) a.join[w] = join_entry<kTile>(c, r, w);
     // Sequences without tokens: zero rows, lse = -inf.
 #pragma unroll 1
     for (int b = w; b < a.B; b += a.W) {
@@ -910,6 +917,13 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
   // period, lie one after another in a slot, each with its chunks side by side, so a slot looks alike for every box.
   a.piece = cfg->page_size & -cfg->page_size;
   if (a.piece > kTile) a.piece = kTile;
+  for (a.piece_log = 3; 1 << a.piece_log < a.piece;) ++a.piece_log;
+  // Division by the page size as a multiplication (T. Granlund and P. L. Montgomery, 1994): with L = ceil(log2 page) and
+  // m = floor(2^(31 + L) / page) + 1, n m / 2^(31 + L) rounded down is n / page for every n below 2^31.
+  int log = 3;
+  while ((int64_t{1} << log) < a.page) ++log;
+  a.page_mul = static_cast<uint32_t>((uint64_t{1} << (31 + log)) / a.page + 1);
+  a.page_shift = log - 1;
   const bool pair = pair_form(cfg->heads, cfg->latent);
   const int chunks = pair ? a.nm : 2 * a.um;               // 64-column chunks of a ring slot
   a.row8_step = chunks * kChunkStep;

@@ -202,12 +202,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool started = false, ok = true;
 
   // Loads of one token block (0 or 1) of a tile.
-  const int pieces = kBlock / a.piece, piece_step = (a.piece >> 3) * a.row8_step;
+  const int pieces = kBlock >> a.piece_log, piece_step = (a.piece >> 3) * a.row8_step;
   BoxRows<kTile> rows;
   // Pieces of block blk of tile t that hold tokens.
   auto live_of = [&](int t, int blk, int len) {
     const int left = len - t * kTile - blk * kBlock;
-    return left <= 0 ? 0 : (left >= kBlock ? pieces : (left + a.piece - 1) / a.piece);
+    return left <= 0 ? 0 : (left >= kBlock ? pieces : (left + a.piece - 1) >> a.piece_log);
   };
 
   if (warp == 0) {
@@ -406,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc = idesc_bf16(256, 128) | (1u << 15);   // A (V^T) is MN-major
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint64_t dp0 = desc_kmajor_sw128(smem_u32(sp)), dv0 = smem_desc(smem_u32(lat), kChunkStep, a.row8_step, 2);
+      if (lane == 0) a.join[w] = join_entry<kTile>(c, r, w);
       Ring lr;
       uint32_t pphase = 0, ophase = 0;
       while (ok && wk.next(a, started)) {
@@ -672,7 +673,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       arrive(oe0);
       wk.done();
     }
-    if (st == 0 && rank == 0) a.join[w] = join_entry<kTile>(c, r, w);
     // Sequences without tokens: zero rows, lse = -inf.
 #pragma unroll 1
     for (int b = w; b < a.B; b += a.W) {

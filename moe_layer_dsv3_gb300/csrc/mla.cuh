@@ -32,6 +32,9 @@ struct MlaArgs {
   int nts;                   // 64-column chunks of Q held in TMEM; the others stay in shared memory
   int W;                     // workers per head group
   int piece;                 // tokens per TMA box: 64, or as many as every page holds whole
+  int piece_log;             // its logarithm
+  uint32_t page_mul;         // token / page = token * page_mul / 2^(32 + page_shift)
+  int page_shift;
   int row8_step;             // bytes from 8 tokens of a ring slot to the next 8
   float scale2;              // scale * log2(e)
   const __nv_bfloat16* q;
@@ -69,8 +72,11 @@ template <int TILE>
 __device__ __forceinline__ int tiles_of(int len) { return (len + TILE - 1) / TILE; }
 
 // Range of tiles of worker w of W over `total` tiles, and the worker that owns tile t.
+// total * w / W rounded down, in 32 bits: the remainder times w stays below W * W. (Two 64-bit divisions here were part
+// of every worker's start.)
 __device__ __forceinline__ int range_begin(int total, int w, int W) {
-  return static_cast<int>(static_cast<int64_t>(total) * w / W);
+  const unsigned q = static_cast<unsigned>(total) / static_cast<unsigned>(W), rest = total - q * W;
+  return static_cast<int>(q * w + rest * static_cast<unsigned>(w) / static_cast<unsigned>(W));
 }
 __device__ __forceinline__ int owner_of(int total, int t, int W) {
   return static_cast<int>((static_cast<int64_t>(t + 1) * W - 1) / total);
@@ -259,12 +265,12 @@ __device__ __forceinline__ bool barrier_or(int id, bool flag) {
 template <int TILE>
 struct BoxRows {
   const int32_t* table;
-  int pieces;
   int first, len, t1;        // first token of the block in a tile; the sequence's tokens; end of the walked tiles
   int tb, row, page, rest;   // page, rest: the next batch
   __device__ __forceinline__ void fetch(const MlaArgs& a, int t) {
-    const int lane = threadIdx.x & 31;
-    const int tile = t + lane / pieces, tok = tile * TILE + first + lane % pieces * a.piece, at = tok / a.page;
+    const int lane = threadIdx.x & 31, box = lane << a.piece_log;   // boxes are 64 tokens of a tile after another
+    const int tile = t + (box >> 6), tok = tile * TILE + first + (box & 63);
+    const int at = static_cast<int>(__umulhi(static_cast<uint32_t>(tok), a.page_mul) >> a.page_shift);
     rest = tok - at * a.page;
     page = tile < t1 && tok < len ? __ldg(table + at) : 0;
   }
@@ -280,7 +286,6 @@ struct BoxRows {
   }
   __device__ __forceinline__ void start(const MlaArgs& a, int b, int t0, int t1_, int first_, int len_) {
     table = a.table + static_cast<int64_t>(b) * a.max_pages;
-    pieces = kBlock / a.piece;
     first = first_;
     len = len_;
     t1 = t1_;
@@ -291,7 +296,7 @@ struct BoxRows {
   __device__ __forceinline__ void get(const MlaArgs& a, int t, int (&ys)[8]) {
     if (t - tb == a.piece / 2) turn(a, t);
 #pragma unroll
-    for (int p = 0; p < 8; ++p) ys[p] = __shfl_sync(0xffffffffu, row, (t - tb) * pieces + p);
+    for (int p = 0; p < 8; ++p) ys[p] = __shfl_sync(0xffffffffu, row, (((t - tb) * kBlock) >> a.piece_log) + p);
   }
 };
 
