@@ -69,15 +69,17 @@ __device__ __forceinline__ int seq_len(const MlaArgs& a, int b, bool report) {
   return n;
 }
 template <int TILE>
-__device__ __forceinline__ int tiles_of(int len) { return (len + TILE - 1) / TILE; }
+__device__ __forceinline__ int tiles_of(int len) {         // (len may end within a tile of 2^31)
+  return static_cast<int>((static_cast<uint32_t>(len) + TILE - 1) / TILE);
+}
 
-// Range of tiles of worker w of W over `total` tiles, and the worker that owns tile t.
-// total * w / W rounded down, in 32 bits: the remainder times w stays below W * W. (Two 64-bit divisions here were part
-// of every worker's start.)
+// First tile of worker w of W over `total` tiles: total * w / W rounded down, in 32 bits (the remainder times w stays
+// below W * W; two 64-bit divisions here were part of every worker's start).
 __device__ __forceinline__ int range_begin(int total, int w, int W) {
   const unsigned q = static_cast<unsigned>(total) / static_cast<unsigned>(W), rest = total - q * W;
   return static_cast<int>(q * w + rest * static_cast<unsigned>(w) / static_cast<unsigned>(W));
 }
+// The worker that owns tile t.
 __device__ __forceinline__ int owner_of(int total, int t, int W) {
   return static_cast<int>((static_cast<int64_t>(t + 1) * W - 1) / total);
 }
@@ -269,10 +271,11 @@ struct BoxRows {
   int tb, row, page, rest;   // page, rest: the next batch
   __device__ __forceinline__ void fetch(const MlaArgs& a, int t) {
     const int lane = threadIdx.x & 31, box = lane << a.piece_log;   // boxes are 64 tokens of a tile after another
-    const int tile = t + (box >> 6), tok = tile * TILE + first + (box & 63);
-    const int at = static_cast<int>(__umulhi(static_cast<uint32_t>(tok), a.page_mul) >> a.page_shift);
-    rest = tok - at * a.page;
-    page = tile < t1 && tok < len ? __ldg(table + at) : 0;
+    const int tile = t + (box >> 6);
+    const uint32_t tok = static_cast<uint32_t>(tile) * TILE + first + (box & 63);   // 2^31 or more only past the end
+    const int at = static_cast<int>(__umulhi(tok, a.page_mul) >> a.page_shift);
+    rest = static_cast<int>(tok) - at * a.page;
+    page = tile < t1 && tok < static_cast<uint32_t>(len) ? __ldg(table + at) : 0;
   }
   __device__ __forceinline__ void turn(const MlaArgs& a, int t) {
     tb = t;

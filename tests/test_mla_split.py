@@ -64,3 +64,28 @@ def test_split(seed):
             # consecutive workers, each with its range's first piece after the first one
             assert [w for _, _, w, _ in got] == list(range(w0, w0 + count))
             assert got[0][3] == first_slot and all(s == 0 for _, _, _, s in got[1:])
+
+
+def test_range_begin_in_32_bits():
+    """range_begin: total * w / W from the quotient and the remainder of total / W."""
+    r = random.Random(1)
+    for _ in range(20000):
+        W = r.randint(1, 160)
+        total, w = r.choice([r.randrange(2 ** 31), r.randrange(1, 2000), W, 2 ** 31 - 1]), r.randint(0, W)
+        q, rest = divmod(total, W)
+        assert rest * w < 2 ** 32 and q * w + rest * w // W == total * w // W
+
+
+def test_page_of_a_token_by_multiplication():
+    """BoxRows: token / page as the high word of a product, for every page size and token the library takes."""
+    r = random.Random(2)
+    pages = list(range(8, 2049, 8)) + [2 ** k + d for k in range(5, 31) for d in (-8, 0, 8)] + [2 ** 31 - 8]
+    for page in pages:
+        log = 3
+        while 2 ** log < page:
+            log += 1
+        mul = 2 ** (31 + log) // page + 1
+        assert mul < 2 ** 32
+        some = [r.randrange(2 ** 31 // page + 1) * page + d for d in (-1, 0, 1) for _ in range(20)]
+        for tok in [0, 1, page - 1, page, 2 ** 31 - 1] + [t for t in some if 0 <= t < 2 ** 31]:
+            assert ((tok * mul) >> 32) >> (log - 1) == tok // page
