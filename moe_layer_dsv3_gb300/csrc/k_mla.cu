@@ -324,37 +324,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
       if (ok) ok = bar_wait(bar, parity, a.status, site);
     };
-    // Chunks of Q that the TMEM plan holds: row 16 q + lane of the quarter's lanes 0-15, two values a
-    // column. Lanes l and l + 16 load half a row of a chunk each; lane l stores it whole.
+    // Chunks of Q that the TMEM plan holds: row 16 q + r in lane r of the quarter's lanes 0-15, two values a column. A lane
+    // loads what the store takes from it: of rows lane / 4 and lane / 4 + 8, the (lane % 4)-th 8 bytes of every 32. All
+    // loads are under way together. (16 bytes of a row of its own per lane took twice the sectors, and a start of
+    // 3300 clocks with 16 heads, 6600 with 32.)
     auto q_to_tmem = [&](int b) {
       if (active) {
-        const int h = 16 * q + (lane & 15);
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + b * a.q_b + (head0 + h) * a.q_h) + (lane >> 4) * 4;
-        constexpr int kAtOnce = P::kMaxTs < 5 ? P::kMaxTs : 5;
-#pragma unroll 1
-        for (int k0 = 0; k0 < a.nts; k0 += kAtOnce) {
-          uint4 v[kAtOnce][4];
+        const int h = 16 * q + (lane >> 2);
+        const uint2* src = reinterpret_cast<const uint2*>(a.q + b * a.q_b + (head0 + h) * a.q_h) + (lane & 3);
+        const int64_t down = 8 * a.q_h / 4;                // 8 rows on, in 8-byte words
+        uint2 v[P::kMaxTs][4][2];
 #pragma unroll
-          for (int k = 0; k < kAtOnce; ++k)
+        for (int k = 0; k < P::kMaxTs; ++k)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              v[k][j] = k0 + k < a.nts && h < nh ? ld_global_u4(src + (k0 + k) * 8 + j) : make_uint4(0, 0, 0, 0);
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) {
-            if (k0 + k >= a.nts) break;
-            uint32_t r[32];
+            for (int e = 0; e < 2; ++e)
+              v[k][j][e] = k < a.nts && h + 8 * e < nh ? ld_global_u2(src + k * 16 + j * 4 + e * down) : make_uint2(0, 0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t w[4] = {v[k][j].x, v[k][j].y, v[k][j].z, v[k][j].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                r[4 * j + e] = w[e];
-                r[16 + 4 * j + e] = __shfl_xor_sync(0xffffffffu, w[e], 16);
-              }
-            }
-            tmem_st_32x32b_x32(tmem + tlane + P::kQ + (k0 + k) * 32, r);
-          }
-        }
+        for (int k = 0; k < P::kMaxTs; ++k)
+          if (k < a.nts) tmem_st_16x256b_x4(tmem + tlane + P::kQ + k * 32, &v[k][0][0]);
         tmem_wait_st();
         tc_fence_before();
       }
