@@ -59,8 +59,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Valid cached tokens of sequence b: lengths outside [0, capacity] are clamped (and reported once).
-__device__ __forceinline__ int seq_len(const MlaArgs& a, int b, bool report) {
-  const int n = __ldg(a.lens + b);
+__device__ __forceinline__ int valid_len(const MlaArgs& a, int n, bool report) {
   const int64_t cap = static_cast<int64_t>(a.max_pages) * a.page;
   if (n < 0 || n > cap) {
     if (report) report_error(a.status, kErrBounds, 60);
@@ -68,6 +67,7 @@ __device__ __forceinline__ int seq_len(const MlaArgs& a, int b, bool report) {
   }
   return n;
 }
+__device__ __forceinline__ int seq_len(const MlaArgs& a, int b, bool report) { return valid_len(a, __ldg(a.lens + b), report); }
 template <int TILE>
 __device__ __forceinline__ int tiles_of(int len) {         // (len may end within a tile of 2^31)
   return static_cast<int>((static_cast<uint32_t>(len) + TILE - 1) / TILE);
@@ -89,7 +89,7 @@ template <int TILE>
 struct Walk {
   int b, t, left;            // next sequence, its next tile, tiles left in the range
   int len, nt;               // current piece's sequence: tokens, tiles
-  int ahead;                 // tokens of sequence b (read a piece early)
+  int ahead;                 // length of sequence b as given: read a piece early, looked at when its turn comes
   int t0, n;                 // current piece: first tile, tiles
   bool first;                // the worker's first piece
   __device__ __forceinline__ bool next(const MlaArgs& a, bool& started) {
@@ -97,8 +97,8 @@ struct Walk {
 #pragma unroll 1
     while (true) {
       if (b >= a.B) return false;
-      len = ahead;
-      ahead = b + 1 < a.B ? seq_len(a, b + 1, false) : 0;
+      len = valid_len(a, ahead, false);
+      ahead = b + 1 < a.B ? __ldg(a.lens + b + 1) : 0;
       nt = tiles_of<TILE>(len);
       if (t < nt) break;
       ++b;
