@@ -29,7 +29,7 @@
 // lengths and the call can be captured in a graph.
 //
 // Measured: 64 sequences of about 16384 tokens with 16 heads (1.15 GB) in 177 us,
-// 0.95 of the copy rate; 37 of about 700 tokens with 20 heads in 22.5 us, of which
+// 0.95 of the copy rate; 37 of about 700 tokens with 20 heads in 21.1 us, of which
 // the cache's bytes need 4.4: there the kernels' starts, a piece's Q and output, and
 // the join's rounds of loads are what is left. More than 64 heads run here only where
 // the pair form does not take them (latent columns not a multiple of 256): each of two

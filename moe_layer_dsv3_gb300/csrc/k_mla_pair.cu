@@ -22,7 +22,7 @@
 //
 // Measured at 512 + 64 columns and 128 heads: 128 sequences of about 4096 tokens
 // (646 MB) in 140-143 us, of which this kernel takes 126 (0.75 of the copy rate, the
-// tensor pipe 52 % active); 2 sequences of 131072 tokens in 71-72 us. The
+// tensor pipe 54 % active); 2 sequences of 131072 tokens in 71-72 us. The
 // form of 64 heads a CTA took 200 and 106 us. Between the two limits stands the
 // chain of a tile: scores, softmax, reload and second product follow one another,
 // with two and a half tiles in the ring and one S buffer left in TMEM.
