@@ -47,7 +47,8 @@ constexpr int kTile = kBlock;             // cached tokens per tile
 constexpr int kAppendBlocks = 3;          // resident blocks an SM: 32768 tokens in 17.2 us; 4 spill more and take 20.7
 constexpr int kMaxLatSlots = 12;
 constexpr int kMaxRopeSlots = kMaxLatSlots;
-constexpr int kMinTiles = 3;              // fewest tiles of a worker: 24 tiles took 18.4 us at 3, 20.5 at 2 and 4
+constexpr int kMinTiles = 3;              // fewest tiles of a worker: 1500 tokens, and 37 sequences of about 700, took
+                                          // 12.9 and 22.2 us at 2, 13.3 and 21.3 at 3, 14.5 and 21.9 at 4
 
 struct Smem {
   uint64_t latf[kMaxLatSlots], late[kMaxLatSlots];     // latent slots: filled / free

@@ -260,9 +260,9 @@ __device__ __forceinline__ bool barrier_or(int id, bool flag) {
   return r != 0;
 }
 
-// Cache rows of the TMA boxes that one warp loads of a sequence: `pieces` boxes of a block of 64 tokens a tile. Lane l
-// holds the first row of box l % pieces of the l / pieces-th tile from `tb` on, so one read of the page table serves 32
-// boxes, and the pages of the next 32 are read while these are used.
+// Cache rows of the TMA boxes that one warp loads of a sequence: those of a block of 64 tokens a tile, `piece` tokens
+// each. Lane l holds the first row of the l-th box from tile `tb` on, so one read of the page table serves 32 boxes, and
+// the pages of the next 32 are read while these are used.
 template <int TILE>
 struct BoxRows {
   const int32_t* table;
