@@ -443,7 +443,7 @@ MOE_API int moe_add_rmsnorm_backward(int T, int d, const void* dy, const void* d
  *               sequence's pages are never read. Pages may be shared.
  * batch >= 0; heads 1..128; latent 128, 256, 384 or 512; rope a multiple of 8 up to
  * 64; page_size a multiple of 8; num_pages * page_size and max_pages * page_size
- * below 2^31; softmax_scale > 0 and finite. */
+ * below 2^31; softmax_scale > 0 and, times log2(e), finite in fp32 (up to 2.35e38). */
 typedef struct moe_mla_config {
   int batch, heads, latent, rope, page_size, num_pages, max_pages;
   float softmax_scale;
@@ -477,7 +477,10 @@ MOE_API int moe_mla_append(const moe_mla_config_t* cfg, int n, const void* kv, i
  *      j < seq_lens[b] of softmax_scale q . k_j.
  *   lse fp32 [batch][heads] (or NULL): log sum_j exp(softmax_scale q . k_j).
  * A sequence of length 0 gets zeros and lse = -inf, and so does a row whose scores
- * are all -inf. Cache rows past a sequence's length may hold anything, NaN included.
+ * are all -inf. An infinite value in the cache makes its own column NaN where its p
+ * is 0, as the formula does. Scores are fp32 in powers of two: softmax_scale q . k is
+ * infinite, or below 2e38 in size. Cache rows past a sequence's length may hold
+ * anything, NaN included.
  * Products take bf16 operands (P is rounded to bf16, and normalised by the sum of
  * the rounded values) and accumulate in fp32; statistics are fp32.
  * A length outside [0, max_pages * page_size] is clamped and a page out of range

@@ -34,6 +34,8 @@
 // the join's rounds of loads are what is left. More than 64 heads run here only where
 // the pair form does not take them (latent columns not a multiple of 256): each of two
 // head groups then reads the cache.
+#include <cmath>
+
 #include "mla.cuh"
 
 namespace moe {
@@ -755,7 +757,8 @@ int validate_mla(const moe_mla_config_t* c) {
   if (c->latent < 128 || c->latent > 512 || c->latent % 128) return MOE_ERR_INVALID_ARG;
   if (c->rope < 8 || c->rope > 64 || c->rope % 8) return MOE_ERR_INVALID_ARG;
   if (c->page_size < 8 || c->page_size % 8 || c->num_pages < 1 || c->max_pages < 1) return MOE_ERR_INVALID_ARG;
-  if (!(c->softmax_scale > 0.0f) || c->softmax_scale > 3.0e38f) return MOE_ERR_INVALID_ARG;
+  // the kernels work in powers of two: with a factor past fp32's range a score of 0 would be NaN
+  if (!(c->softmax_scale > 0.0f) || !std::isfinite(c->softmax_scale * kLog2e)) return MOE_ERR_INVALID_ARG;
   const int64_t lim = (1LL << 31) - 1;
   const int64_t cap = static_cast<int64_t>(c->max_pages) * c->page_size;
   // row coordinates and token positions are 32-bit, and so is the count of tiles of all sequences
