@@ -126,6 +126,13 @@ def _p(x):
     return None if x is None or x == 0 else int(x)
 
 
+def _int32(name: str, *values) -> None:
+    # ctypes would keep a larger integer's low 32 bits, and the call would do other work than was asked for
+    for v in values:
+        if not -(1 << 31) <= v < 1 << 31:
+            raise MoeError("%s: %d is past 32 bits and" % (name, v), MOE_ERR_INVALID_ARG)
+
+
 MOE_FLAG_LAP_LAUNCHES = 1   # one mover launch + one GEMM launch per ring lap instead of one launch for all laps
 MOE_FLAG_WGRAD_PAIR = 2     # weight gradients on CTA pairs (256-row tiles) instead of single-CTA 128 x 256 tiles
 MOE_FLAG_X_QUANTIZED = 4    # moe_forward / moe_dispatch take MX(x) from the workspace instead of quantising x
@@ -244,24 +251,30 @@ def moe_scales_to_tiled(canon, rows, K, tiled, stream=0):
 
 
 def moe_add_rmsnorm(T, d, x, residual, gamma, eps, h, y, rstd=0, codes=0, scales=0, scales_tiled=0, stream=0):
+    if (T | d) >> 31:
+        _int32("moe_add_rmsnorm", T, d)
     _check("moe_add_rmsnorm",
            _lib.moe_add_rmsnorm(T, d, _p(x), _p(residual), _p(gamma), float(eps), _p(h), _p(y), _p(rstd), _p(codes),
                                 _p(scales), _p(scales_tiled), _p(stream)))
 
 
 def moe_add_rmsnorm_backward_workspace(T, d) -> int:
+    _int32("moe_add_rmsnorm_backward_workspace", T, d)
     n = ctypes.c_size_t()
     _check("moe_add_rmsnorm_backward_workspace", _lib.moe_add_rmsnorm_backward_workspace(T, d, ctypes.byref(n)))
     return n.value
 
 
 def moe_add_rmsnorm_backward(T, d, dy, dres, h, gamma, rstd, dx, dgamma, ws, stream=0):
+    if (T | d) >> 31:
+        _int32("moe_add_rmsnorm_backward", T, d)
     _check("moe_add_rmsnorm_backward",
            _lib.moe_add_rmsnorm_backward(T, d, _p(dy), _p(dres), _p(h), _p(gamma), _p(rstd), _p(dx), _p(dgamma), _p(ws),
                                          _p(stream)))
 
 
 def mla_config(batch, heads, latent=512, rope=64, page_size=64, num_pages=1, max_pages=1, softmax_scale=1.0) -> MlaConfig:
+    _int32("mla_config", batch, heads, latent, rope, page_size, num_pages, max_pages)
     return MlaConfig(batch, heads, latent, rope, page_size, num_pages, max_pages, softmax_scale)
 
 
@@ -272,6 +285,8 @@ def moe_mla_workspace_size(cfg: MlaConfig) -> int:
 
 
 def moe_mla_append(cfg, n, kv, ld_kv, gamma, eps, cos_sin, max_pos, seq, pos, block_table, cache, ws, stream=0):
+    if (n | ld_kv | max_pos) >> 31:
+        _int32("moe_mla_append", n, ld_kv, max_pos)
     _check("moe_mla_append",
            _lib.moe_mla_append(ctypes.byref(cfg), n, _p(kv), ld_kv, _p(gamma), float(eps), _p(cos_sin), max_pos, _p(seq),
                                _p(pos), _p(block_table), _p(cache), _p(ws), _p(stream)))
