@@ -53,7 +53,7 @@ struct Smem {
   uint64_t vl[2];                          // reload landed, by tile parity
   uint64_t pf, pe;                         // P and reload ready (even CTA) / product done
   uint64_t of, oe;                         // O: all products of the piece done / read (even CTA)
-  uint64_t gx[2], gf[2];                   // from the other CTA: "moved" word, by tile parity / factors, alternating
+  uint64_t gx[2], gf[2];                   // "moved" word of the other CTA, by tile parity / both CTAs' factors, alternating
   uint32_t moved[2];
   uint32_t tmem;
   int scan[kThreads / 32];
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c.sd[i], 1);
       mbar_init(&c.vl[i], 1);
       mbar_init(&c.gx[i], 1);
-      mbar_init(&c.gf[i], 1);
+      mbar_init(&c.gf[i], 2);
     }
     fence_barrier_init();
     fence_proxy_async();
@@ -463,8 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int swaps = 0;                                         // exchanges so far
     Ring lr;                                               // ring position of the current tile
     int tile = 0;
-    // After a wait that gave up, these threads stop waiting but keep walking: all of them then meet at every
-    // barrier, and the kernel ends.
+    // After a wait that gave up, these threads stop waiting but keep walking, so that all of them meet at every
+    // CTA barrier and the kernel ends. A thread that gave up may read a word that the other CTA is still to write.
+    // So nothing between the CTAs decides whether a CTA barrier is met: only `grow`, which a barrier hands out, and
+    // the walk do. A thread that gave up sends nothing either: each of its waits is then paired with at most one
+    // arrival of its own, and the others' waits run out too.
     auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
       if (ok) ok = bar_wait_cluster(bar, parity, a.status, site);
     };
@@ -473,15 +476,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(bar);
     };
-    // A factor per head into both CTAs' arrays (the same place in both); the other CTA's heads have arrived at the end.
+    // A factor per head into both CTAs' arrays (the same place in both), complete in this CTA at the end. Two warps
+    // speak for the 64 heads; each arrives after its own stores and expects 32 words of the other CTA.
     auto exchange = [&](float* arr, uint32_t arr_o, float v) {
       uint64_t* bar = &c.gf[swaps & 1];
-      if (st == 0) mbar_arrive_expect_tx(bar, kMaxHeadsCta * 4);
       if (first) {
-        arr[rank * 64 + hl] = v;
-        st_async(arr_o + (rank * 64 + hl) * 4, __float_as_uint(v), gf_o + (swaps & 1) * 8);
+        if (ok) {
+          arr[rank * 64 + hl] = v;
+          st_async(arr_o + (rank * 64 + hl) * 4, __float_as_uint(v), gf_o + (swaps & 1) * 8);
+        }
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive_expect_tx(bar, 32 * 4);
       }
-      named_barrier(3, kSoft);
       wait(bar, (swaps >> 1) & 1u, 184);
       ++swaps;
     };
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float over = take(x, p, ls, les);
         const bool grow = barrier_or<kSoft>(2, over > kSlack);
         // O is rescaled only when a score of the tile passes kSlack in either CTA.
-        if (st == 0) {
+        if (st == 0 && ok) {
           mbar_arrive_expect_tx(&c.gx[par], 4);            // the other CTA's word
           st_async(moved_o + par * 4, grow ? 1u : 0u, gx_o + par * 8);
         }
@@ -554,8 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           pphase ^= 1u;
         }
         wait(&c.gx[par], (tile >> 1) & 1u, 185);
-        const bool rescale = (grow || *reinterpret_cast<volatile uint32_t*>(&c.moved[par]) != 0u) && ti > 0;
-        if (rescale) {
+        const bool theirs = *reinterpret_cast<volatile uint32_t*>(&c.moved[par]) != 0u;
+        if (__any_sync(0xffffffffu, grow || theirs) && ti > 0) {       // one answer a warp, also after a wait that gave up
           exchange(fac, fac_o, corr);
           tc_fence_after();
 #pragma unroll 1
@@ -624,7 +630,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (whole) exchange(inv, inv_o, norm);
-      else named_barrier(3, kSoft);                        // xl and xe are free
       wait(&c.of, ophase, 183);
       ophase ^= 1u;
       tc_fence_after();
