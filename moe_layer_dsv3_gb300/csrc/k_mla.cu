@@ -205,9 +205,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int i = 0, n = issued < a.nlat ? issued : a.nlat; i < n; ++i) {
         if (--lr.slot < 0) { lr.slot = a.nlat - 1; lr.phase ^= 1u; }
-        bar_wait(&c.latf[lr.slot], lr.phase, a.status, 64);
+        ok = bar_wait(&c.latf[lr.slot], lr.phase, a.status, 64) && ok;
       }
-      if (issued_q > 0) bar_wait(&c.qf, qphase ^ 1u, a.status, 64);
+      if (issued_q > 0) ok = bar_wait(&c.qf, qphase ^ 1u, a.status, 64) && ok;
     }
   } else if (warp == 1) {
     // Issues S. The whole warp walks the tiles and waits, and one elected lane
@@ -323,9 +323,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int hr = 16 * q + (lane >> 2);                   // this thread's heads: rows hr and hr + 8 of S
     bool any_tile = false;                                 // a product into O has been issued before this tile
     // After a wait that gave up, these threads stop waiting but keep walking: all 128 then
-    // meet at every barrier, and the kernel ends.
+    // meet at every CTA barrier, and the kernel ends. They arrive on no memory barrier any more: no barrier
+    // gets more arrivals than it expects, and the other warps' waits run out too.
     auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
       if (ok) ok = bar_wait(bar, parity, a.status, site);
+    };
+    auto arrive = [&](uint64_t* bar) {
+      if (ok) mbar_arrive(bar);
     };
     // Chunks of Q that the TMEM plan holds: row 16 q + r in lane r of the quarter's lanes 0-15, two values a column. A lane
     // loads what the store takes from it: of rows lane / 4 and lane / 4 + 8, the (lane % 4)-th 8 bytes of every 32. All
@@ -350,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_st();
         tc_fence_before();
       }
-      mbar_arrive(&c.qf);
+      arrive(&c.qf);
     };
     // One piece ahead: its Q goes in as soon as the last scores of the piece before are done.
     Walk<kTile> nx = wk;
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) reg_fence(x[i]);
           tc_fence_before();
         }
-        mbar_arrive(&c.se[sbuf]);
+        arrive(&c.se[sbuf]);
         if (++sbuf == P::kBufs) {
           sbuf = 0;
           sphase ^= 1u;
@@ -492,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int u = 0; u < a.nu; ++u) lr.step(a.nlat);
         fence_proxy_async();
         tc_fence_before();
-        mbar_arrive(&c.pf);
+        arrive(&c.pf);
       }
       // ---- epilogue of the piece, after the next one's Q
       nx.done();
@@ -584,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive(&c.oe);
+      arrive(&c.oe);
       wk.done();
     }
     // Sequences without tokens: zero rows, lse = -inf.
@@ -600,9 +604,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   tc_fence_before();
-  __syncthreads();
+  // After a wait that gave up, products may be under way that nobody waits for.
+  if (__syncthreads_or(!ok)) drain_pause();
   if (warp == 1) {
     tc_fence_after();
+    __syncwarp();
     tmem_dealloc(tmem, 512);
   }
 }

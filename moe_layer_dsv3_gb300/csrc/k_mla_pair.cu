@@ -55,6 +55,7 @@ struct Smem {
   uint64_t of, oe;                         // O: all products of the piece done / read (even CTA)
   uint64_t gx[2], gf[2];                   // "moved" word of the other CTA, by tile parity / both CTAs' factors, alternating
   uint32_t moved[2];
+  uint32_t failed;                         // a wait gave up in either CTA
   uint32_t tmem;
   int scan[kThreads / 32];
   int start_b, start_t, start_len;
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int w = static_cast<int>(pair::cluster_id());
 
   if (tid == 0) {
+    c.failed = 0;
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&c.full[i], 1);
       mbar_init(&c.empty[i], 1);
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int i = 0, n = issued < kSlots ? issued : kSlots; i < n; ++i) {
         if (--lr.slot < 0) { lr.slot = kSlots - 1; lr.phase ^= 1u; }
-        bar_wait(&c.full[lr.slot], lr.phase, a.status, 164);
+        ok = bar_wait(&c.full[lr.slot], lr.phase, a.status, 164) && ok;
       }
     }
   } else if (warp == 11) {
@@ -325,10 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       wk.done();
     }
     if (lane == 0) {                                       // the last copies have landed
-      if (rank == 0 && issued_q > 0) bar_wait(&c.qf, qphase ^ 1u, a.status, 166);
+      if (rank == 0 && issued_q > 0) ok = bar_wait(&c.qf, qphase ^ 1u, a.status, 166) && ok;
       for (int i = 1; i <= 2 && i <= tile; ++i) {
         const int par = (tile - i) & 1;
-        bar_wait(&c.vl[par], ((tile - i) >> 1) & 1u, a.status, 166);
+        ok = bar_wait(&c.vl[par], ((tile - i) >> 1) & 1u, a.status, 166) && ok;
       }
     }
   } else if (warp == 1) {
@@ -466,15 +468,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // After a wait that gave up, these threads stop waiting but keep walking, so that all of them meet at every
     // CTA barrier and the kernel ends. A thread that gave up may read a word that the other CTA is still to write.
     // So nothing between the CTAs decides whether a CTA barrier is met: only `grow`, which a barrier hands out, and
-    // the walk do. A thread that gave up sends nothing either: each of its waits is then paired with at most one
-    // arrival of its own, and the others' waits run out too.
+    // the walk do. A thread that gave up sends nothing and arrives on no memory barrier: no barrier gets more arrivals
+    // than it expects, no product starts on what is not there, and the others' waits run out too.
     auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
       if (ok) ok = bar_wait_cluster(bar, parity, a.status, site);
     };
     // One arrival of this warp on a barrier of the even CTA.
     auto arrive = [&](uint32_t bar) {
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(bar);
+      if (lane == 0 && ok) mbar_arrive_remote(bar);
     };
     // A factor per head into both CTAs' arrays (the same place in both), complete in this CTA at the end. Two warps
     // speak for the 64 heads; each arrives after its own stores and expects 32 words of the other CTA.
@@ -690,10 +692,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = st; i < nh; i += kSoft) a.lse[static_cast<int64_t>(b) * a.H + head0 + i] = -INFINITY;
     }
   }
-  // Neither CTA leaves (or frees TMEM) while the other may still use its shared memory, its TMEM or its barriers.
+  // Neither CTA leaves (or frees TMEM) while the other may still use its shared memory, its TMEM or its barriers. After
+  // a wait that gave up, both stay until what was under way without anybody waiting for it has landed.
+  if (!ok) {
+    st_cluster(pair::map_rank(smem_u32(&c.failed), 0), 1u);
+    st_cluster(pair::map_rank(smem_u32(&c.failed), 1), 1u);
+  }
   tc_fence_before();
   __syncwarp();
   pair::cluster_sync();
+  if (*reinterpret_cast<volatile uint32_t*>(&c.failed) != 0u) {
+    drain_pause();
+    __syncwarp();
+    pair::cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     pair::tmem_dealloc(tmem, 512);

@@ -171,6 +171,9 @@ __device__ __forceinline__ uint32_t num_ctas() {
 __device__ __forceinline__ void st_cluster(uint32_t addr, const float4& v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void st_cluster(uint32_t addr, const float2& v) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
 }
@@ -243,6 +246,16 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int* st
 // bar_wait by a whole warp: the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int site) {
   return __all_sync(0xffffffffu, bar_wait(bar, parity, status, site));
+}
+
+// How long a CTA whose wait gave up stays before it leaves: copies, products and words of the other CTA that nobody
+// waits for any more take a few microseconds.
+constexpr uint64_t kDrainNs = 100000;
+__device__ __forceinline__ void drain_pause() {
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  while (global_timer_ns() - t0 < kDrainNs) {
+  }
 }
 
 // Barrier over the NT softmax threads that also gives the OR of their flags.

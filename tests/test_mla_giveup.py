@@ -126,6 +126,8 @@ def run(seed, give_up):
             break
         what = r.choices([x for _, x in todo], [x for x, _ in todo])[0]
         if what[0] == "deliver":
+            # words still under way when all threads are done: only where a thread gave up, and both CTAs then stay a while
+            assert gave_up or any(a[0] != "end" for a in at.values()), seed
             bar, word, n = net.pop(what[1])
             if word is not None:
                 word[0].moved[word[1]] = word[2]
@@ -151,13 +153,35 @@ def test_every_wait_ends_where_none_gives_up():
         assert run(seed, False) == 0
 
 
+def _source(name):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "moe_layer_dsv3_gb300", "csrc", name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
 def test_no_cta_barrier_depends_on_what_the_other_cta_sent():
     """The exchange holds no CTA barrier, and one answer a warp leads into it, as the model has it."""
-    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "moe_layer_dsv3_gb300", "csrc",
-                        "k_mla_pair.cu")
-    src = open(path).read()
+    src = _source("k_mla_pair.cu")
     body = re.search(r"auto exchange = \[&\].*?\n    };", src, re.S).group(0)
     assert "named_barrier" not in body and "barrier_or" not in body and "__syncthreads" not in body
     read = src.index("&c.moved[par]) != 0u")
     lead = src[read:src.index("exchange(fac", read)]
     assert "__any_sync" in lead
+
+
+@pytest.mark.parametrize("name,raw", [("k_mla.cu", "mbar_arrive("), ("k_mla_pair.cu", "mbar_arrive_remote(")])
+def test_softmax_threads_arrive_only_while_their_waits_hold(name, raw):
+    """Arrivals of a thread that runs ahead without waiting could be more than a barrier expects, or start a product early."""
+    src = _source(name)
+    soft = src[src.index("auto wait = [&]"):src.rindex("tmem_dealloc(tmem")]
+    arrive = re.search(r"auto arrive = \[&\].*?\n    };", soft, re.S).group(0)
+    assert re.search(r"if \([^;]*\bok\b[^;]*\) " + re.escape(raw), arrive)
+    assert raw not in soft.replace(arrive, "")
+
+
+@pytest.mark.parametrize("name", ["k_mla.cu", "k_mla_pair.cu"])
+def test_a_cta_stays_after_a_wait_that_gave_up(name):
+    """Between the last barrier of all roles and the release of TMEM, if any thread gave up."""
+    src = _source(name)
+    end = src[:src.rindex("tmem_dealloc(tmem")]
+    assert "drain_pause()" in end[end.rindex("tc_fence_before()"):]
