@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(256, kAppendBlocks) mla_append_kernel(const __
     }
     const int pg = p / a.page;
     t.row = p - pg * a.page;
-    t.page = __ldg(a.table + static_cast<int64_t>(b) * a.max_pages + pg);
+    t.page = ld_global_s32(a.table + static_cast<int64_t>(b) * a.max_pages + pg);
     const __nv_bfloat16* src = a.kv + i * a.ld;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -666,16 +666,16 @@ __global__ void __launch_bounds__(256, kAppendBlocks) mla_append_kernel(const __
       t.u = ld_global_u4(src + a.latent + lane * 8);
       if (a.cos_sin != nullptr) {
         const float* cs = a.cos_sin + static_cast<int64_t>(p) * a.rope + lane * 4;
-        t.co = __ldg(reinterpret_cast<const float4*>(cs));
-        t.si = __ldg(reinterpret_cast<const float4*>(cs + a.rope / 2));
+        t.co = ld_global_f4(cs);
+        t.si = ld_global_f4(cs + a.rope / 2);
       }
     }
   };
   int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (i >= a.n) return;
   auto place = [&](int64_t k, int& p, int& b) {
-    p = k < a.n ? __ldg(a.pos + k) : -1;
-    b = k < a.n ? __ldg(a.seq + k) : 0;
+    p = k < a.n ? ld_global_s32(a.pos + k) : -1;
+    b = k < a.n ? ld_global_s32(a.seq + k) : 0;
   };
   int p0, b0, p1, b1;
   place(i, p0, b0);
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(256, kAppendBlocks) mla_append_kernel(const __
   uint4 ug[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
-    ug[h] = a.gamma != nullptr && lane + 32 * h < nlat ? __ldg(reinterpret_cast<const uint4*>(a.gamma) + lane + 32 * h)
+    ug[h] = a.gamma != nullptr && lane + 32 * h < nlat ? ld_global_u4(a.gamma + (lane + 32 * h) * 8)
                                                        : make_uint4(0, 0, 0, 0);
   Token t;
   read(i, p0, b0, t);

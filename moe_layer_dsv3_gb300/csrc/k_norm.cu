@@ -96,7 +96,7 @@ __global__ void add_rmsnorm_kernel(const __grid_constant__ NormArgs a) {
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int i = i0 + j * nt;
-    ug[j] = i < nvec ? __ldg(reinterpret_cast<const uint4*>(a.gamma) + i) : make_uint4(0, 0, 0, 0);
+    ug[j] = i < nvec ? ld_global_u4(a.gamma + i * 8) : make_uint4(0, 0, 0, 0);
   }
   float h[V][8];
   float ss = 0.0f;
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_bwd_kernel(const __grid_consta
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int i = i0 + j * nt;
-    ug[j] = i < nvec ? __ldg(reinterpret_cast<const uint4*>(a.gamma) + i) : make_uint4(0, 0, 0, 0);
+    ug[j] = i < nvec ? ld_global_u4(a.gamma + i * 8) : make_uint4(0, 0, 0, 0);
   }
   float acc[V][8] = {};
 #pragma unroll
@@ -296,8 +296,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_bwd_kernel(const __grid_consta
 
 // dgamma[c] = sum over n partial rows, in a fixed order: 32 columns a CTA,
 // 32 threads a column.
-__global__ void __launch_bounds__(1024) norm_dgamma_kernel(const float* __restrict__ part, int n, int d,
-                                                          float* __restrict__ dgamma) {
+__global__ void __launch_bounds__(1024) norm_dgamma_kernel(const float* part, int n, int d, float* dgamma) {
   asm volatile("griddepcontrol.wait;" ::: "memory");       // the partial sums are visible
   __shared__ float s[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x;

@@ -67,7 +67,7 @@ __device__ __forceinline__ int valid_len(const MlaArgs& a, int n, bool report) {
   }
   return n;
 }
-__device__ __forceinline__ int seq_len(const MlaArgs& a, int b, bool report) { return valid_len(a, __ldg(a.lens + b), report); }
+__device__ __forceinline__ int seq_len(const MlaArgs& a, int b, bool report) { return valid_len(a, ld_global_s32(a.lens + b), report); }
 template <int TILE>
 __device__ __forceinline__ int tiles_of(int len) {         // (len may end within a tile of 2^31)
   return static_cast<int>((static_cast<uint32_t>(len) + TILE - 1) / TILE);
@@ -98,7 +98,7 @@ struct Walk {
     while (true) {
       if (b >= a.B) return false;
       len = valid_len(a, ahead, false);
-      ahead = b + 1 < a.B ? __ldg(a.lens + b + 1) : 0;
+      ahead = b + 1 < a.B ? ld_global_s32(a.lens + b + 1) : 0;
       nt = tiles_of<TILE>(len);
       if (t < nt) break;
       ++b;
@@ -287,7 +287,7 @@ struct BoxRows {
     const uint32_t tok = static_cast<uint32_t>(tile) * TILE + first + (box & 63);   // 2^31 or more only past the end
     const int at = static_cast<int>(__umulhi(tok, a.page_mul) >> a.page_shift);
     rest = static_cast<int>(tok) - at * a.page;
-    page = tile < t1 && tok < static_cast<uint32_t>(len) ? __ldg(table + at) : 0;
+    page = tile < t1 && tok < static_cast<uint32_t>(len) ? ld_global_s32(table + at) : 0;
   }
   __device__ __forceinline__ void turn(const MlaArgs& a, int t) {
     tb = t;
