@@ -445,6 +445,7 @@ extern "C" int moe_add_rmsnorm_backward(int T, int d, const void* dy, const void
   else if (d <= kWarpRowMax) bwd<4, true, 2>(a, b, ctas, s);
   else if (d <= 8192) bwd<2, false, 4>(a, b, ctas, s);
   else bwd<4, false, 2>(a, b, ctas, s);
+  if (call_error() != cudaSuccess) return call.status();      // no partial sums to add
   launch_kernel_after("norm_dgamma", norm_dgamma_kernel, dim3(static_cast<unsigned>(ceil_div(d, 32))), dim3(32, 32), 0, s,
                 static_cast<const float*>(a.part), ctas, d, dgamma);
   return call.status();

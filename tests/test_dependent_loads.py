@@ -2,7 +2,7 @@
 
 They start early and wait with griddepcontrol.wait, so what they read may be written while they live. A read-only
 load (__ldg, or a const __restrict__ pointer's) is not defined for that, and the compiler may move one ahead of the
-wait.
+wait. And no kernel is launched on the results of one whose set-up or launch failed.
 """
 import os
 import re
@@ -31,3 +31,14 @@ def test_no_read_only_loads(name):
     code = _code(name)
     assert "__ldg" not in code and "ld.global.nc" not in code
     assert not re.search(r"const [\w:]+\s*\*\s*__restrict__", code)
+
+
+@pytest.mark.parametrize("name,first,then", [
+    ("k_norm.cu", "else bwd<4, false, 2>(", 'launch_kernel_after("norm_dgamma"'),
+    ("k_mla.cu", 'launch_kernel_after("mla_decode"', "launch_join<"),
+    ("k_mla_pair.cu", 'launch_cluster_after("mla_decode_pair"', "launch_join<")])
+def test_no_launch_on_the_results_of_a_failed_one(name, first, then):
+    """A workspace that nothing filled is not summed: the call's error is looked at between the two launches."""
+    code = _code(name)
+    at = code.rindex(first)
+    assert re.search(r"if \([^;]*call_error\(\)[^;]*\) return", code[at:code.index(then, at)])
