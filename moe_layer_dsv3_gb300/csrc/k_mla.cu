@@ -917,12 +917,9 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
   a.piece = cfg->page_size & -cfg->page_size;
   if (a.piece > kTile) a.piece = kTile;
   for (a.piece_log = 3; 1 << a.piece_log < a.piece;) ++a.piece_log;
-  // Division by the page size as a multiplication (T. Granlund and P. L. Montgomery, 1994): with L = ceil(log2 page) and
-  // m = floor(2^(31 + L) / page) + 1, n m / 2^(31 + L) rounded down is n / page for every n below 2^31.
-  int log = 3;
-  while ((int64_t{1} << log) < a.page) ++log;
-  a.page_mul = static_cast<uint32_t>((uint64_t{1} << (31 + log)) / a.page + 1);
-  a.page_shift = log - 1;
+  const PageDiv pd = page_div(a.page);
+  a.page_mul = pd.mul;
+  a.page_shift = pd.shift;
   const bool pair = pair_form(cfg->heads, cfg->latent);
   const int chunks = pair ? a.nm : 2 * a.um;               // 64-column chunks of a ring slot
   a.row8_step = chunks * kChunkStep;

@@ -4,6 +4,7 @@
 #include <cudaTypedefs.h>
 
 #include "gemm.cuh"
+#include "mla_split.h"
 #include "prof.h"
 
 namespace moe {
@@ -33,7 +34,7 @@ struct MlaArgs {
   int W;                     // workers per head group
   int piece;                 // tokens per TMA box: 64, or as many as every page holds whole
   int piece_log;             // its logarithm
-  uint32_t page_mul;         // token / page = token * page_mul / 2^(32 + page_shift)
+  uint32_t page_mul;         // see page_div
   int page_shift;
   int row8_step;             // bytes from 8 tokens of a ring slot to the next 8
   float scale2;              // scale * log2(e)
@@ -69,20 +70,7 @@ __device__ __forceinline__ int valid_len(const MlaArgs& a, int n, bool report) {
 }
 __device__ __forceinline__ int seq_len(const MlaArgs& a, int b, bool report) { return valid_len(a, ld_global_s32(a.lens + b), report); }
 template <int TILE>
-__device__ __forceinline__ int tiles_of(int len) {         // (len may end within a tile of 2^31)
-  return static_cast<int>((static_cast<uint32_t>(len) + TILE - 1) / TILE);
-}
-
-// First tile of worker w of W over `total` tiles: total * w / W rounded down, in 32 bits (the remainder times w stays
-// below W * W; two 64-bit divisions here were part of every worker's start).
-__device__ __forceinline__ int range_begin(int total, int w, int W) {
-  const unsigned q = static_cast<unsigned>(total) / static_cast<unsigned>(W), rest = total - q * W;
-  return static_cast<int>(q * w + rest * static_cast<unsigned>(w) / static_cast<unsigned>(W));
-}
-// The worker that owns tile t.
-__device__ __forceinline__ int owner_of(int total, int t, int W) {
-  return static_cast<int>((static_cast<int64_t>(t + 1) * W - 1) / total);
-}
+__device__ __forceinline__ int tiles_of(int len) { return tiles_of(len, TILE); }
 
 // Work of one worker: contiguous pieces of sequences, walked the same way by every role.
 template <int TILE>
@@ -285,7 +273,7 @@ struct BoxRows {
     const int lane = threadIdx.x & 31, box = lane << a.piece_log;   // boxes are 64 tokens of a tile after another
     const int tile = t + (box >> 6);
     const uint32_t tok = static_cast<uint32_t>(tile) * TILE + first + (box & 63);   // 2^31 or more only past the end
-    const int at = static_cast<int>(__umulhi(tok, a.page_mul) >> a.page_shift);
+    const int at = page_of(tok, a.page_mul, a.page_shift);
     rest = static_cast<int>(tok) - at * a.page;
     page = tile < t1 && tok < static_cast<uint32_t>(len) ? ld_global_s32(table + at) : 0;
   }
@@ -356,8 +344,7 @@ __device__ __forceinline__ Range find_range(const MlaArgs& a, Control& c, int w,
     r.total += c.scan[i];
   }
   // A piece costs a join, so no more workers than tiles / MIN_TILES (rounded up) get any; ranges differ by a tile at most.
-  const int most = (r.total + MIN_TILES - 1) / MIN_TILES;
-  r.W = a.W < most ? a.W : (most > 0 ? most : 1);
+  r.W = workers_of(r.total, a.W, MIN_TILES);
   r.f0 = w < r.W ? range_begin(r.total, w, r.W) : r.total;
   r.f1 = w < r.W ? range_begin(r.total, w + 1, r.W) : r.total;
   int at = before + incl - mine;
@@ -384,9 +371,8 @@ __device__ __forceinline__ int4 join_entry(const Control& c, const Range& r, int
   if (r.f1 <= r.f0 || c.start_t == 0) return make_int4(0, 0, 0, 0);
   const int s0 = r.f0 - c.start_t;                         // the sequence's first tile in the common count
   if (s0 + tiles_of<TILE>(c.start_len) > r.f1) return make_int4(0, 0, 0, 0);
-  const int w0 = owner_of(r.total, s0, r.W);
-  // it opened w0's range, or came after another piece there
-  return make_int4(c.start_b, range_begin(r.total, w0, r.W) == s0 ? 0 : 1, w0, w - w0 + 1);
+  const Cut cut = cut_of(r.total, r.W, s0, w);
+  return make_int4(c.start_b, cut.slot, cut.worker, cut.pieces);
 }
 
 // Joins the pieces of the sequences that the work split cut. An item is 8 heads and
