@@ -21,11 +21,13 @@
 // their heads (shared::cluster stores) and both rescale their columns of O^T.
 //
 // Measured at 512 + 64 columns and 128 heads: 128 sequences of about 4096 tokens
-// (646 MB) in 140-143 us, of which this kernel takes 126 (0.75 of the copy rate, the
-// tensor pipe 54 % active); 2 sequences of 131072 tokens in 71-72 us. The
-// form of 64 heads a CTA took 200 and 106 us. Between the two limits stands the
-// chain of a tile: scores, softmax, reload and second product follow one another,
-// with two and a half tiles in the ring and one S buffer left in TMEM.
+// (646 MB) in 140-144 us, of which this kernel takes 127 (0.75 of the copy rate, the
+// tensor pipe 54 % active); 2 sequences of 131072 tokens in 71-73 us. The
+// form of 64 heads a CTA took 200 and 106 us. Between the two limits stand the
+// hand-offs of a tile: scores, softmax and second product follow one another, with
+// one S buffer. In the first build, 159 us a call, leaving out the reload or the
+// exponentials changed nothing, leaving out both products gave 142, and without
+// products and loads 109 were left.
 #include "mla.cuh"
 
 namespace moe {
@@ -78,8 +80,9 @@ __device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity
   return __all_sync(0xffffffffu, bar_wait_cluster(bar, parity, status, site));
 }
 // Arrive on a barrier of either CTA, ordering only what this CTA's own memory holds: registers that were read from
-// TMEM, or operands written here for this SM's tensor core (with their proxy fence). A release at cluster scope
-// took about 1000 clocks, twice a tile.
+// TMEM, or operands written here for this SM's tensor core. Each writer has passed its fence to the async proxy, and
+// its warp's barrier, before the arrival leaves this SM, and the other CTA reads none of it: it only issues the product.
+// A release at cluster scope took about 1000 clocks, twice a tile.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

@@ -62,7 +62,8 @@ class AddRMSNorm:
     def backward(self, dy, gamma, dres=None, stream=0, h=None, rstd=None):
         """Write dx (the gradient of x and residual) and dgamma, and return dx.
 
-        h and rstd default to those of the last forward call.
+        h and rstd default to those of the last forward call. Without a residual that call keeps x itself as h, so x
+        has to hold the same values until here; the norm's own h, y, rstd, dx and dgamma last until its next call.
         """
         h = self._saved if h is None else h
         rstd = self.rstd if rstd is None else rstd
