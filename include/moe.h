@@ -494,6 +494,36 @@ MOE_API int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_t q
 /* moe_status for the workspace of the latent-attention calls. */
 MOE_API int moe_mla_status(const moe_mla_config_t* cfg, void* ws, int* code, int* site, int clear, moe_stream_t stream);
 
+/* The whole layer for a few tokens: moe_route, moe_schedule and moe_forward in one
+ * call of three launches, for decoding steps and drafted tokens.
+ *   logits = x Wr^T, the choice of moe_route (idx, w), and
+ *   y = sum_j w_j MX(h_j) Wd_j^T + the shared expert's, h = silu(g) u, [g | u] = MX(x) Wgu^T,
+ * with the quantised weights of moe_quantize_weights (the same blob: it does not
+ * depend on T) and MX(x), MX(h) as in moe_forward. Products and sums are fp32, and y
+ * is rounded to bf16 once (moe_forward rounds each expert's output before it sums
+ * them). Logits are summed in another order than moe_route's: scores that differ in
+ * their last bits only may be chosen otherwise.
+ *   cfg: as for moe_route and moe_forward, with T <= MOE_FEW_MAX_T; capacity,
+ *   n_mover_warps, and the flags of other passes have no effect (MOE_FLAG_X_QUANTIZED
+ *   is refused).
+ *   x, y bf16 [T][d]; w_router bf16 [E][d]; bias fp32 [E]; topk_idx int32 [T][k] and
+ *   topk_w fp32 [T][k] are written.
+ *   ws: moe_few_workspace_size bytes, zero before the first call; calls that share it
+ *   must be ordered by the caller. It grows with T, so that of a larger T serves too.
+ * A token whose scores are NaN gets y = NaN and sets the status to MOE_ERR_BOUNDS.
+ * An expert that no token chose is not read, and a token's y does not depend on the
+ * other tokens' values (its last bits may depend on how many there are and on what
+ * they chose, since sums are cut where the work is). x, w_router, wq, y and ws on
+ * 16-byte boundaries. Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_ARCH,
+ * MOE_ERR_CUDA. */
+#define MOE_FEW_MAX_T 64
+MOE_API int moe_few_workspace_size(const moe_config_t* cfg, size_t* bytes);
+MOE_API int moe_few_forward(const moe_config_t* cfg, const void* x, const void* w_router, const float* bias, const void* wq,
+                            int32_t* topk_idx, float* topk_w, void* y, void* ws, moe_stream_t stream);
+
+/* moe_status for the workspace of moe_few_forward. */
+MOE_API int moe_few_status(const moe_config_t* cfg, void* ws, int* code, int* site, int clear, moe_stream_t stream);
+
 /* Measurement hooks (process-wide, for benchmarks; not part of the layer).
  * moe_profile_enable(1): every kernel launch of the library is bracketed by a
  * pair of CUDA events recorded on its launch stream (events come from a pool

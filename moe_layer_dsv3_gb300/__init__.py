@@ -95,6 +95,9 @@ _SIGS = {
     "moe_mla_append": [_MLA, _I, _P, _I, _P, ctypes.c_float, _P, _I, _P, _P, _P, _P, _P, _P],
     "moe_mla_decode": [_MLA, _P, ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P],
     "moe_mla_status": [_MLA, _P, ctypes.POINTER(_I), ctypes.POINTER(_I), _I, _P],
+    "moe_few_workspace_size": [_CFG, _SZ],
+    "moe_few_forward": [_CFG, _P, _P, _P, _P, _P, _P, _P, _P, _P],
+    "moe_few_status": [_CFG, _P, ctypes.POINTER(_I), ctypes.POINTER(_I), _I, _P],
     "moe_profile_enable": [_I],
     "moe_profile_read": [ctypes.c_void_p, _I, ctypes.POINTER(_I)],
     "moe_profile_trace": [ctypes.c_void_p, _I, ctypes.POINTER(_I)],
@@ -137,6 +140,7 @@ MOE_FLAG_LAP_LAUNCHES = 1   # one mover launch + one GEMM launch per ring lap in
 MOE_FLAG_WGRAD_PAIR = 2     # weight gradients on CTA pairs (256-row tiles) instead of single-CTA 128 x 256 tiles
 MOE_FLAG_X_QUANTIZED = 4    # moe_forward / moe_dispatch take MX(x) from the workspace instead of quantising x
 MOE_NORM_MAX_D = 16384
+MOE_FEW_MAX_T = 64
 
 
 def config(T, d, E, k, n_groups=1, topk_groups=1, I=128, n_shared=0, capacity=0, flags=0,
@@ -301,6 +305,25 @@ def moe_mla_decode(cfg, q, q_stride_b, q_stride_h, cache, block_table, seq_lens,
 def moe_mla_status(cfg, ws, clear=True, stream=0):
     code, site = ctypes.c_int(), ctypes.c_int()
     _check("moe_mla_status", _lib.moe_mla_status(ctypes.byref(cfg), _p(ws), ctypes.byref(code), ctypes.byref(site),
+                                                 1 if clear else 0, _p(stream)))
+    return code.value, site.value
+
+
+def moe_few_workspace_size(cfg: MoeConfig) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_few_workspace_size", _lib.moe_few_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def moe_few_forward(cfg, x, w_router, bias, wq, topk_idx, topk_w, y, ws, stream=0):
+    _check("moe_few_forward",
+           _lib.moe_few_forward(ctypes.byref(cfg), _p(x), _p(w_router), _p(bias), _p(wq), _p(topk_idx), _p(topk_w), _p(y),
+                                _p(ws), _p(stream)))
+
+
+def moe_few_status(cfg, ws, clear=True, stream=0):
+    code, site = ctypes.c_int(), ctypes.c_int()
+    _check("moe_few_status", _lib.moe_few_status(ctypes.byref(cfg), _p(ws), ctypes.byref(code), ctypes.byref(site),
                                                  1 if clear else 0, _p(stream)))
     return code.value, site.value
 
