@@ -65,7 +65,8 @@ enum {
   MOE_ERR_WORKSPACE = 4,       /* workspace or weight blob too small */
   MOE_ERR_TIMEOUT = 5,         /* (device status) a bounded wait gave up */
   MOE_ERR_BOUNDS = 6,          /* (device status) an index check failed */
-  MOE_ERR_SCRATCH = 7          /* moe_route_noalloc: T * E exceeds its fixed scratch */
+  MOE_ERR_SCRATCH = 7,         /* moe_route_noalloc: T * E exceeds its fixed scratch */
+  MOE_ERR_PAGES = 8            /* (device status) moe_pages_update: not enough free pages */
 };
 
 /* Layer shape.
@@ -449,7 +450,7 @@ typedef struct moe_mla_config {
   float softmax_scale;
 } moe_mla_config_t;
 
-/* Workspace of the two calls below: a status word and the pieces of sequences
+/* Workspace of the calls below: a status word and the pieces of sequences
  * that the work split cuts (it depends on latent only, about 45 MB at 512). Its
  * first 16 bytes have to be zero before the first call (moe_mla_status clears them too). */
 MOE_API int moe_mla_workspace_size(const moe_mla_config_t* cfg, size_t* bytes);
@@ -491,8 +492,66 @@ MOE_API int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_t q
                            const void* cache, const int32_t* block_table, const int32_t* seq_lens, void* out,
                            float* lse, void* ws, moe_stream_t stream);
 
+/* Attention of a tree of drafted tokens a sequence (speculative decoding): the
+ * drafted tokens are the sequence's last ones in the cache (moe_mla_append), and each
+ * sees all tokens before the drafted ones and those drafted tokens that its mask names.
+ *   drafts: most drafted tokens of a sequence, 1..MOE_MLA_MAX_DRAFTS.
+ *   q: bf16, element (b, i, h, c) of drafted token i at b * q_stride_b +
+ *      (i * heads + h) * q_stride_h + c (strides in elements, multiples of 8).
+ *   seq_lens int32 [batch]: tokens of each sequence, the drafted ones included.
+ *   draft_lens int32 [batch]: drafted tokens of each sequence, or NULL: `drafts` each
+ *      (0 of an empty sequence).
+ *   tree uint64 [batch][drafts]: bit j of word i: drafted token i sees drafted token j. Any bits
+ *      may be set (a token sees itself by its own bit); those past the sequence's
+ *      drafted tokens are ignored. NULL: a chain, each sees itself and the ones before it.
+ *   out bf16 [batch][drafts][heads][latent], lse fp32 [batch][drafts][heads] (or NULL): as
+ *      for moe_mla_decode, over the tokens that are seen. Rows of tokens past
+ *      the sequence's drafted ones, and rows that see nothing, get zeros and -inf.
+ * With one drafted token a sequence this is moe_mla_decode. A cached row that is not
+ * finite reaches every drafted token of its sequence: its column is NaN also where p is 0.
+ * A count outside [0, min(drafts, seq_lens)] is clamped and sets the status to
+ * MOE_ERR_BOUNDS; everything else is as for moe_mla_decode, the workspace too. */
+#define MOE_MLA_MAX_DRAFTS 64
+MOE_API int moe_mla_decode_tree(const moe_mla_config_t* cfg, int drafts, const void* q, int64_t q_stride_b,
+                                int64_t q_stride_h, const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                                const int32_t* draft_lens, const uint64_t* tree, void* out, float* lse, void* ws,
+                                moe_stream_t stream);
+
 /* moe_status for the workspace of the latent-attention calls. */
 MOE_API int moe_mla_status(const moe_mla_config_t* cfg, void* ws, int* code, int* site, int clear, moe_stream_t stream);
+
+/* Block tables and slot maps from request lengths: sequence b goes from seq_lens[b]
+ * tokens to target[b]. One that grows past its last page takes pages from the pool, one
+ * that shrinks (rejected drafts, a finished request) leaves those past its new end.
+ *   block_table int32 [batch][max_pages], as for moe_mla_append: entries of taken pages
+ *     are written, all others stay (those of left pages too: they are past the end).
+ *   free_pages int32 [num_pages], free_count int32 [1]: the pool, a stack whose top is
+ *     entry free_count - 1. Pages that are left go on it in order (sequence by
+ *     sequence, a sequence's pages in order), then taken ones come off it, for the first
+ *     growing sequence first. Entries past the new count are not written.
+ *   lens_out int32 [batch], count_out int32 [1]: target and the new count; they may be
+ *     seq_lens and free_count.
+ *   seq, pos, slot int32 [max_new]: of every new token, sequence by sequence, its sequence,
+ *     its position in it and its row in the cache (page * page_size + place in the page);
+ *     0, -1, -1 past the last one, which moe_mla_append skips.
+ *   starts int32 [batch + 1]: first new token of a sequence; starts[batch] is their number.
+ * A step that cannot be made (not enough free pages: MOE_ERR_PAGES; a length outside
+ * [0, max_pages * page_size], more than max_new new tokens, a count outside [0, num_pages],
+ * more pages left than the pool has room for: MOE_ERR_BOUNDS) changes nothing and writes
+ * no tokens; the status tells. A page out of range in the table or the pool sets the
+ * status to MOE_ERR_BOUNDS; its tokens get slot -1. Pages must not be shared by sequences
+ * that may leave them. Everything is read on the device, so a captured call replays.
+ * batch 0..MOE_PAGES_MAX_BATCH; num_pages * page_size and (max_pages + 1) * page_size below
+ * 2^31 - 1; seq, pos, slot and ws on 16-byte boundaries. ws: 16 bytes, zero before the
+ * first call (moe_pages_status clears them too); calls that share it must be ordered. */
+#define MOE_PAGES_MAX_BATCH 8192
+MOE_API int moe_pages_update(int batch, int page_size, int num_pages, int max_pages, int max_new, const int32_t* seq_lens,
+                             const int32_t* target, int32_t* block_table, int32_t* free_pages, const int32_t* free_count,
+                             int32_t* lens_out, int32_t* count_out, int32_t* seq, int32_t* pos, int32_t* slot,
+                             int32_t* starts, void* ws, moe_stream_t stream);
+
+/* moe_status for the workspace of moe_pages_update. */
+MOE_API int moe_pages_status(void* ws, int* code, int* site, int clear, moe_stream_t stream);
 
 /* The whole layer for a few tokens: moe_route, moe_schedule and moe_forward in one
  * call of three launches, for decoding steps and drafted tokens.

@@ -31,6 +31,7 @@ MOE_ERR_WORKSPACE = 4
 MOE_ERR_TIMEOUT = 5
 MOE_ERR_BOUNDS = 6
 MOE_ERR_SCRATCH = 7
+MOE_ERR_PAGES = 8
 
 WS_NAMES = ["STATUS", "META", "COUNTS", "OFFSETS", "POFF", "RANK", "POS", "INV", "ROWSRC", "LAPTILES", "HIST",
             "BASE", "LOGITS", "SSEL", "XQ", "XQ_SF", "RING_X", "RING_X_SF", "GU", "HQ", "HQ_SF", "HTOK", "HTOK_SF",
@@ -94,7 +95,10 @@ _SIGS = {
     "moe_mla_workspace_size": [_MLA, _SZ],
     "moe_mla_append": [_MLA, _I, _P, _I, _P, ctypes.c_float, _P, _I, _P, _P, _P, _P, _P, _P],
     "moe_mla_decode": [_MLA, _P, ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P],
+    "moe_mla_decode_tree": [_MLA, _I, _P, ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P, _P, _P],
     "moe_mla_status": [_MLA, _P, ctypes.POINTER(_I), ctypes.POINTER(_I), _I, _P],
+    "moe_pages_update": [_I] * 5 + [_P] * 13,
+    "moe_pages_status": [_P, ctypes.POINTER(_I), ctypes.POINTER(_I), _I, _P],
     "moe_few_workspace_size": [_CFG, _SZ],
     "moe_few_forward": [_CFG, _P, _P, _P, _P, _P, _P, _P, _P, _P],
     "moe_few_status": [_CFG, _P, ctypes.POINTER(_I), ctypes.POINTER(_I), _I, _P],
@@ -141,6 +145,8 @@ MOE_FLAG_WGRAD_PAIR = 2     # weight gradients on CTA pairs (256-row tiles) inst
 MOE_FLAG_X_QUANTIZED = 4    # moe_forward / moe_dispatch take MX(x) from the workspace instead of quantising x
 MOE_NORM_MAX_D = 16384
 MOE_FEW_MAX_T = 64
+MOE_MLA_MAX_DRAFTS = 64
+MOE_PAGES_MAX_BATCH = 8192
 
 
 def config(T, d, E, k, n_groups=1, topk_groups=1, I=128, n_shared=0, capacity=0, flags=0,
@@ -302,10 +308,36 @@ def moe_mla_decode(cfg, q, q_stride_b, q_stride_h, cache, block_table, seq_lens,
                                _p(out), _p(lse), _p(ws), _p(stream)))
 
 
+def moe_mla_decode_tree(cfg, drafts, q, q_stride_b, q_stride_h, cache, block_table, seq_lens, draft_lens, tree, out, lse, ws,
+                        stream=0):
+    if drafts >> 31:
+        _int32("moe_mla_decode_tree", drafts)
+    _check("moe_mla_decode_tree",
+           _lib.moe_mla_decode_tree(ctypes.byref(cfg), drafts, _p(q), q_stride_b, q_stride_h, _p(cache), _p(block_table),
+                                    _p(seq_lens), _p(draft_lens), _p(tree), _p(out), _p(lse), _p(ws), _p(stream)))
+
+
 def moe_mla_status(cfg, ws, clear=True, stream=0):
     code, site = ctypes.c_int(), ctypes.c_int()
     _check("moe_mla_status", _lib.moe_mla_status(ctypes.byref(cfg), _p(ws), ctypes.byref(code), ctypes.byref(site),
                                                  1 if clear else 0, _p(stream)))
+    return code.value, site.value
+
+
+def moe_pages_update(batch, page_size, num_pages, max_pages, max_new, seq_lens, target, block_table, free_pages, free_count,
+                     lens_out, count_out, seq, pos, slot, starts, ws, stream=0):
+    if (batch | page_size | num_pages | max_pages | max_new) >> 31:
+        _int32("moe_pages_update", batch, page_size, num_pages, max_pages, max_new)
+    _check("moe_pages_update",
+           _lib.moe_pages_update(batch, page_size, num_pages, max_pages, max_new, _p(seq_lens), _p(target), _p(block_table),
+                                 _p(free_pages), _p(free_count), _p(lens_out), _p(count_out), _p(seq), _p(pos), _p(slot),
+                                 _p(starts), _p(ws), _p(stream)))
+
+
+def moe_pages_status(ws, clear=True, stream=0):
+    code, site = ctypes.c_int(), ctypes.c_int()
+    _check("moe_pages_status", _lib.moe_pages_status(_p(ws), ctypes.byref(code), ctypes.byref(site), 1 if clear else 0,
+                                                     _p(stream)))
     return code.value, site.value
 
 

@@ -88,7 +88,7 @@ struct Plan {
 
 // Threads: warp 0 loads (TMA), warps 1 and 6 issue the MMAs of S and O^T, warps
 // 2-5 do the softmax and the epilogue (TMEM lane quarter warp % 4).
-template <int N>
+template <int N, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_decode_kernel(const __grid_constant__ CUtensorMap tma_k, const __grid_constant__ CUtensorMap tma_r,
                       const __grid_constant__ CUtensorMap tma_q, const __grid_constant__ MlaArgs a) {
@@ -136,11 +136,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");       // inputs and workspace of the stream's earlier kernels
   tc_fence_before();
-  const Range r = find_range<kThreads, kTile, kMinTiles>(a, c, w, blockIdx.x == 0);
+  const Range r = find_range<TREE, kThreads, kTile, kMinTiles>(a, c, w, blockIdx.x == 0);
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;");       // the join's blocks may be placed; they wait for this grid's end
   const uint32_t tmem = c.tmem;
-  Walk<kTile> wk;
+  Walk<kTile, TREE> wk;
   wk.b = c.start_b;
   wk.t = c.start_t;
   wk.ahead = c.start_len;
@@ -161,14 +161,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && wk.next(a, started)) {
       const int b = __shfl_sync(0xffffffffu, wk.b, 0), len = __shfl_sync(0xffffffffu, wk.len, 0);
       const int t0 = __shfl_sync(0xffffffffu, wk.t0, 0), t1 = t0 + __shfl_sync(0xffffffffu, wk.n, 0);
-      rows.start(a, b, t0, t1, 0, len);
+      const Item item = item_of<TREE>(a, b);
+      rows.start(a, item.seq, t0, t1, 0, len);
       // Q of this sequence and head group, once the previous piece's products have read the last one.
       ok = warp_wait(&c.qe, qphase ^ 1u, a.status, 61);
       if (!ok) break;
       if (elect_one()) {
         mbar_arrive_expect_tx(&c.qf, nss * N * 128);
 #pragma unroll 1
-        for (int k = 0; k < nss; ++k) tma_load_3d(sq + k * N * 128, &tma_q, (a.nts + k) * 64, h0, b, &c.qf);
+        for (int k = 0; k < nss; ++k) tma_load_3d(sq + k * N * 128, &tma_q, (a.nts + k) * 64, item.row0 + h0, item.seq, &c.qf);
       }
       __syncwarp();
       qphase ^= 1u;
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int sbuf = 0;
     Ring lr;                                               // latent ring position of the current tile
     const int head0 = g * a.hg;                            // first head of the group
-    const int nh = a.H - head0 < a.hg ? a.H - head0 : a.hg;
+    auto heads_of = [&](const Item& it) { return it.rows - head0 < a.hg ? it.rows - head0 : a.hg; };
     const bool active = 16 * q < N;                        // this warp's 16 rows of S hold heads
     const int hr = 16 * q + (lane >> 2);                   // this thread's heads: rows hr and hr + 8 of S
     bool any_tile = false;                                 // a product into O has been issued before this tile
@@ -343,8 +344,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 3300 clocks with 16 heads, 6600 with 32.)
     auto q_to_tmem = [&](int b) {
       if (active) {
+        const Item it = item_of<TREE>(a, b);
+        const int nh = heads_of(it);
         const int h = 16 * q + (lane >> 2);
-        const uint2* src = reinterpret_cast<const uint2*>(a.q + b * a.q_b + (head0 + h) * a.q_h) + (lane & 3);
+        const uint2* src = reinterpret_cast<const uint2*>(a.q + it.seq * a.q_b + (it.row0 + head0 + h) * a.q_h) + (lane & 3);
         const int64_t down = 8 * a.q_h / 4;                // 8 rows on, in 8-byte words
         uint2 v[P::kMaxTs][4][2];
 #pragma unroll
@@ -363,12 +366,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       arrive(&c.qf);
     };
     // One piece ahead: its Q goes in as soon as the last scores of the piece before are done.
-    Walk<kTile> nx = wk;
+    Walk<kTile, TREE> nx = wk;
     bool nx_started = false;
     bool more = nx.next(a, nx_started);
     if (more) q_to_tmem(nx.b);
     while (wk.next(a, started)) {
       float ref[2] = {kNoRef, kNoRef}, l[2] = {0.0f, 0.0f}, le[2] = {0.0f, 0.0f};
+      const Item item = item_of<TREE>(a, wk.b);
+      const int nh = heads_of(item);
+      Sight sight[2];                                      // of this thread's rows
+      int prefix = 0;
+      if constexpr (TREE) {
+        const int drafted = drafts_of(a, item.seq, wk.len, st == 0);
+        prefix = wk.len - drafted;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) sight[k] = sight_of(a, item.seq, item.row0 + hr + 8 * k, drafted);
+      }
       // P of the scores x, packed to bf16, and its row sums (this thread's part): as rounded for the product,
       // which normalise the output, and in fp32 for the lse. Returns the largest score above its head's
       // reference, in powers of two.
@@ -413,7 +426,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           sphase ^= 1u;
         }
         if (active) {
-          if (valid < kTile) {
+          if constexpr (TREE) {
+            const int t64 = (wk.t0 + ti) * kTile;
+            if (t64 + kTile > prefix || !sight[0].live || !sight[1].live) {
+              uint64_t see[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) see[k] = sees(sight[k], prefix, t64) >> (2 * (lane & 3));
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((see[(i >> 1) & 1] >> (8 * (i >> 2) + (i & 1))) & 1u)) x[i] = __float_as_uint(-INFINITY);
+            }
+          } else if (valid < kTile) {
             const int col = 2 * (lane & 3);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -524,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (whole) {
               fac[h] = v == 0.0f ? 0.0f : 1.0f / v;
               if (a.lse != nullptr && h < nh)
-                a.lse[static_cast<int64_t>(wk.b) * a.H + head0 + h] = ve == 0.0f ? -INFINITY : (ref[k] + log2f(ve)) * kLn2;
+                a.lse[static_cast<int64_t>(item.seq) * a.H + item.row0 + head0 + h] = ve == 0.0f ? -INFINITY : (ref[k] + log2f(ve)) * kLn2;
             } else {
               a.part_m[slot * kMaxHeadsCta + h] = ref[k];
               a.part_l[slot * kMaxHeadsCta + h] = v;
@@ -544,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < NP; ++i) f[i] = reinterpret_cast<const float2*>(fac)[4 * i + (lane & 3)];
       uint8_t* stage = sp + q * (N * 32);                  // [N heads][16 columns] of this warp, over P
-      __nv_bfloat16* out = a.out + (static_cast<int64_t>(wk.b) * a.H + head0) * a.latent;
+      __nv_bfloat16* out = a.out + (static_cast<int64_t>(item.seq) * a.H + item.row0 + head0) * a.latent;
       float4* part = reinterpret_cast<float4*>(a.part_o + static_cast<int64_t>(slot) * kMaxHeadsCta * a.latent) + q * 32 + lane;
       constexpr int kAtOnce = N <= 32 ? 2 : 1;             // blocks read from TMEM at once
 #pragma unroll 1
@@ -600,13 +623,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Sequences without tokens: zero rows, lse = -inf.
 #pragma unroll 1
     for (int b = w; b < a.B; b += a.W) {
-      if (seq_len(a, b, false) > 0) continue;
-      __nv_bfloat16* out = a.out + (static_cast<int64_t>(b) * a.H + head0) * a.latent;
+      if (seq_len<TREE>(a, b, false) > 0) continue;
+      const Item item = item_of<TREE>(a, b);
+      const int nh = heads_of(item);
+      const int64_t at = static_cast<int64_t>(item.seq) * a.H + item.row0 + head0;
+      __nv_bfloat16* out = a.out + at * a.latent;
 #pragma unroll 1
       for (int i = st; i < nh * a.latent / 8; i += 128) reinterpret_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
       if (a.lse != nullptr)
 #pragma unroll 1
-        for (int i = st; i < nh; i += 128) a.lse[static_cast<int64_t>(b) * a.H + head0 + i] = -INFINITY;
+        for (int i = st; i < nh; i += 128) a.lse[at + i] = -INFINITY;
+      if constexpr (TREE) {
+        if (st == 0) drafts_of(a, item.seq, 0, true);
+      }
     }
   }
   tc_fence_before();
@@ -801,12 +830,12 @@ MlaLayout mla_layout(const moe_mla_config_t* c) {
   return L;
 }
 
-template <int N>
+template <int N, bool TREE>
 int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CUtensorMap& tq, int sms,
                cudaStream_t s) {
   static DevOnce once;
   if (!once.ready([] {
-        return cudaFuncSetAttribute(mla_decode_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+        return cudaFuncSetAttribute(mla_decode_kernel<N, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
       }))
     return MOE_ERR_CUDA;
   const int nchunk = 2 * a.nm + 1;
@@ -821,14 +850,103 @@ int run_decode(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CU
   a.nlat = (ring - a.nrope * kChunk) / slot_bytes;
   if (a.nlat > kMaxLatSlots) a.nlat = kMaxLatSlots;
   const int smem = fixed + a.nrope * kChunk + a.nlat * slot_bytes;
-  launch_kernel_after("mla_decode", mla_decode_kernel<N>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(kThreads), smem, s, tk, tr, tq,
+  launch_kernel_after("mla_decode", mla_decode_kernel<N, TREE>, dim3(static_cast<unsigned>(a.W * a.G)), dim3(kThreads), smem, s, tk, tr, tq,
                 a);
   if (int e = call_error() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA) return e;
-  launch_join<N, false, kTile, kMinTiles>(a, sms, s);
+  launch_join<N, false, TREE, kTile, kMinTiles>(a, sms, s);
   return MOE_OK;
 }
 
 inline bool mis(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+// The launches of moe_mla_decode and (TREE) moe_mla_decode_tree: `a` comes with what is the tree's own.
+template <bool TREE>
+int decode(const moe_mla_config_t* cfg, MlaArgs a, const void* q, int64_t q_stride_b, int64_t q_stride_h, const void* cache,
+           const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse, void* ws, cudaStream_t s) {
+  CallScope call;
+  if (!get_encode()) return MOE_ERR_CUDA;
+  const MlaLayout L = mla_layout(cfg);
+  char* base = static_cast<char*>(ws);
+  const int row = cfg->latent + cfg->rope;
+  const int rows_walked = TREE ? a.hv : cfg->heads;        // rows of a walked item
+  a.B = cfg->batch * a.V;
+  a.latent = cfg->latent;
+  a.rope = cfg->rope;
+  a.page = cfg->page_size;
+  a.num_pages = cfg->num_pages;
+  a.max_pages = cfg->max_pages;
+  a.G = static_cast<int>(ceil_div(rows_walked, kMaxHeadsCta));
+  a.hg = static_cast<int>(ceil_div(rows_walked, a.G));
+  a.nm = cfg->latent / 128;
+  a.um = a.nm % 2 ? 1 : 2;
+  a.nu = a.nm / a.um;
+  const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
+  a.W = sms / a.G;
+  // A box takes as many tokens as every page holds whole: 8 to 64, a power of two. Groups of 8 rows, the swizzle's
+  // period, lie one after another in a slot, each with its chunks side by side, so a slot looks alike for every box.
+  a.piece = cfg->page_size & -cfg->page_size;
+  if (a.piece > kTile) a.piece = kTile;
+  for (a.piece_log = 3; 1 << a.piece_log < a.piece;) ++a.piece_log;
+  const PageDiv pd = page_div(a.page);
+  a.page_mul = pd.mul;
+  a.page_shift = pd.shift;
+  const bool pair = pair_form(rows_walked, cfg->latent);
+  const int chunks = pair ? a.nm : 2 * a.um;               // 64-column chunks of a ring slot
+  a.row8_step = chunks * kChunkStep;
+  a.scale2 = cfg->softmax_scale * kLog2e;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_b = q_stride_b;
+  a.q_h = q_stride_h;
+  a.table = block_table;
+  a.lens = seq_lens;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.status = reinterpret_cast<int*>(base + L.status);
+  a.join = reinterpret_cast<int4*>(base + L.join);
+  a.part_m = reinterpret_cast<float*>(base + L.m);
+  a.part_l = reinterpret_cast<float*>(base + L.l);
+  a.part_e = reinterpret_cast<float*>(base + L.e);
+  a.part_o = reinterpret_cast<float*>(base + L.o);
+  const int N = pair ? kMaxHeadsCta : static_cast<int>(round_up(a.hg, 16));
+  CUtensorMap tk, tr, tq;
+  const int64_t rows = static_cast<int64_t>(cfg->num_pages) * cfg->page_size;
+  if (!make_tmap_latent(&tk, cache, rows, cfg, a.piece, chunks) || !make_tmap_rope(&tr, cache, rows, cfg, a.piece))
+    return MOE_ERR_CUDA;
+  if (!make_tmap_strided(&tq, q,
+                         {static_cast<uint64_t>(row), static_cast<uint64_t>(a.H), static_cast<uint64_t>(cfg->batch), 1},
+                         {static_cast<uint64_t>(q_stride_h) * 2, static_cast<uint64_t>(q_stride_b) * 2, 0},
+                         {64, static_cast<uint32_t>(N), 1, 1}, 3))
+    return MOE_ERR_CUDA;
+  if (pair) {
+    if (int r = run_decode_pair<TREE>(a, tk, tr, tq, sms, s)) return r;
+    return call.status();
+  }
+  int r;
+  switch (N) {
+    case 16: r = run_decode<16, TREE>(a, tk, tr, tq, sms, s); break;
+    case 32: r = run_decode<32, TREE>(a, tk, tr, tq, sms, s); break;
+    case 48: r = run_decode<48, TREE>(a, tk, tr, tq, sms, s); break;
+    default: r = run_decode<64, TREE>(a, tk, tr, tq, sms, s); break;
+  }
+  if (r) return r;
+  return call.status();
+}
+
+// What the two calls refuse alike.
+int refuse_decode(const moe_mla_config_t* cfg, const void* q, int64_t q_stride_b, int64_t q_stride_h, const void* cache,
+                  const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse, void* ws, int64_t least_b) {
+  const int row = cfg->latent + cfg->rope;
+  if (cache == nullptr || ws == nullptr) return MOE_ERR_INVALID_ARG;
+  if (cfg->batch > 0 && (q == nullptr || block_table == nullptr || seq_lens == nullptr || out == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  // strides in elements; a TMA dimension's pitch is below 2^40 bytes
+  if (q_stride_h < row || q_stride_b < least_b || q_stride_h % 8 || q_stride_b % 8 || q_stride_h >= (1LL << 38) ||
+      q_stride_b >= (1LL << 38))
+    return MOE_ERR_INVALID_ARG;
+  if (mis(q, 16) || mis(cache, 16) || mis(out, 16) || mis(ws, 16) || mis(lse, 4) || mis(block_table, 4) || mis(seq_lens, 4))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
 
 }  // namespace
 
@@ -887,86 +1005,41 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
                               const void* cache, const int32_t* block_table, const int32_t* seq_lens, void* out,
                               float* lse, void* ws, moe_stream_t stream) {
   if (int r = validate_mla(cfg)) return r;
-  const int row = cfg->latent + cfg->rope;
-  if (cache == nullptr || ws == nullptr) return MOE_ERR_INVALID_ARG;
-  if (cfg->batch > 0 && (q == nullptr || block_table == nullptr || seq_lens == nullptr || out == nullptr))
-    return MOE_ERR_INVALID_ARG;
-  // strides in elements; a TMA dimension's pitch is below 2^40 bytes
-  if (q_stride_h < row || q_stride_b < row || q_stride_h % 8 || q_stride_b % 8 || q_stride_h >= (1LL << 38) ||
-      q_stride_b >= (1LL << 38))
-    return MOE_ERR_INVALID_ARG;
-  if (mis(q, 16) || mis(cache, 16) || mis(out, 16) || mis(ws, 16) || mis(lse, 4) || mis(block_table, 4) || mis(seq_lens, 4))
-    return MOE_ERR_INVALID_ARG;
+  if (int r = refuse_decode(cfg, q, q_stride_b, q_stride_h, cache, block_table, seq_lens, out, lse, ws, cfg->latent + cfg->rope))
+    return r;
   if (!arch_ok()) return MOE_ERR_UNSUPPORTED_ARCH;
-  CallScope call;
   if (cfg->batch == 0) return MOE_OK;
-  if (!get_encode()) return MOE_ERR_CUDA;
-  const MlaLayout L = mla_layout(cfg);
-  char* base = static_cast<char*>(ws);
   MlaArgs a{};
-  a.B = cfg->batch;
   a.H = cfg->heads;
-  a.latent = cfg->latent;
-  a.rope = cfg->rope;
-  a.page = cfg->page_size;
-  a.num_pages = cfg->num_pages;
-  a.max_pages = cfg->max_pages;
-  a.G = static_cast<int>(ceil_div(cfg->heads, kMaxHeadsCta));
-  a.hg = static_cast<int>(ceil_div(cfg->heads, a.G));
-  a.nm = cfg->latent / 128;
-  a.um = a.nm % 2 ? 1 : 2;
-  a.nu = a.nm / a.um;
-  const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
-  a.W = sms / a.G;
-  // A box takes as many tokens as every page holds whole: 8 to 64, a power of two. Groups of 8 rows, the swizzle's
-  // period, lie one after another in a slot, each with its chunks side by side, so a slot looks alike for every box.
-  a.piece = cfg->page_size & -cfg->page_size;
-  if (a.piece > kTile) a.piece = kTile;
-  for (a.piece_log = 3; 1 << a.piece_log < a.piece;) ++a.piece_log;
-  const PageDiv pd = page_div(a.page);
-  a.page_mul = pd.mul;
-  a.page_shift = pd.shift;
-  const bool pair = pair_form(cfg->heads, cfg->latent);
-  const int chunks = pair ? a.nm : 2 * a.um;               // 64-column chunks of a ring slot
-  a.row8_step = chunks * kChunkStep;
-  a.scale2 = cfg->softmax_scale * kLog2e;
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.q_b = q_stride_b;
-  a.q_h = q_stride_h;
-  a.table = block_table;
-  a.lens = seq_lens;
-  a.out = static_cast<__nv_bfloat16*>(out);
-  a.lse = lse;
-  a.status = reinterpret_cast<int*>(base + L.status);
-  a.join = reinterpret_cast<int4*>(base + L.join);
-  a.part_m = reinterpret_cast<float*>(base + L.m);
-  a.part_l = reinterpret_cast<float*>(base + L.l);
-  a.part_e = reinterpret_cast<float*>(base + L.e);
-  a.part_o = reinterpret_cast<float*>(base + L.o);
-  const int N = pair ? kMaxHeadsCta : static_cast<int>(round_up(a.hg, 16));
-  CUtensorMap tk, tr, tq;
-  const int64_t rows = static_cast<int64_t>(cfg->num_pages) * cfg->page_size;
-  if (!make_tmap_latent(&tk, cache, rows, cfg, a.piece, chunks) || !make_tmap_rope(&tr, cache, rows, cfg, a.piece))
-    return MOE_ERR_CUDA;
-  if (!make_tmap_strided(&tq, q,
-                         {static_cast<uint64_t>(row), static_cast<uint64_t>(cfg->heads), static_cast<uint64_t>(cfg->batch), 1},
-                         {static_cast<uint64_t>(q_stride_h) * 2, static_cast<uint64_t>(q_stride_b) * 2, 0},
-                         {64, static_cast<uint32_t>(N), 1, 1}, 3))
-    return MOE_ERR_CUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (pair) {
-    if (int r = run_decode_pair(a, tk, tr, tq, sms, s)) return r;
-    return call.status();
-  }
-  int r;
-  switch (N) {
-    case 16: r = run_decode<16>(a, tk, tr, tq, sms, s); break;
-    case 32: r = run_decode<32>(a, tk, tr, tq, sms, s); break;
-    case 48: r = run_decode<48>(a, tk, tr, tq, sms, s); break;
-    default: r = run_decode<64>(a, tk, tr, tq, sms, s); break;
-  }
-  if (r) return r;
-  return call.status();
+  a.V = 1;
+  return decode<false>(cfg, a, q, q_stride_b, q_stride_h, cache, block_table, seq_lens, out, lse, ws,
+                       static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int moe_mla_decode_tree(const moe_mla_config_t* cfg, int drafts, const void* q, int64_t q_stride_b,
+                                   int64_t q_stride_h, const void* cache, const int32_t* block_table, const int32_t* seq_lens,
+                                   const int32_t* draft_lens, const uint64_t* tree, void* out, float* lse, void* ws,
+                                   moe_stream_t stream) {
+  if (int r = validate_mla(cfg)) return r;
+  if (drafts < 1 || drafts > MOE_MLA_MAX_DRAFTS || mis(draft_lens, 4) || mis(tree, 8)) return MOE_ERR_INVALID_ARG;
+  if (int r = refuse_decode(cfg, q, q_stride_b, q_stride_h, cache, block_table, seq_lens, out, lse, ws, cfg->latent + cfg->rope))
+    return r;
+  // A sequence's rows in groups that one worker takes: up to 128 where the pair form does, else up to 64.
+  MlaArgs a{};
+  a.H = drafts * cfg->heads;
+  a.V = static_cast<int>(ceil_div(a.H, cfg->latent % 256 == 0 ? 2 * kMaxHeadsCta : kMaxHeadsCta));
+  a.hv = static_cast<int>(ceil_div(a.H, a.V));
+  // the count of tiles of all groups is 32-bit
+  const int64_t tiles = ceil_div(static_cast<int64_t>(cfg->max_pages) * cfg->page_size, kTile);
+  if (cfg->batch > 0 && tiles > ((1LL << 31) - 1) / (static_cast<int64_t>(cfg->batch) * a.V)) return MOE_ERR_INVALID_ARG;
+  if (!arch_ok()) return MOE_ERR_UNSUPPORTED_ARCH;
+  if (cfg->batch == 0) return MOE_OK;
+  a.heads = cfg->heads;
+  a.drafts = drafts;
+  a.draft_lens = draft_lens;
+  a.tree = tree;
+  return decode<true>(cfg, a, q, q_stride_b, q_stride_h, cache, block_table, seq_lens, out, lse, ws,
+                      static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int moe_mla_status(const moe_mla_config_t* cfg, void* ws, int* code, int* site, int clear,

@@ -136,6 +136,7 @@ __device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a, uint64_t b, uint
 
 // Warps: 0 loads for the first product, 11 reloads for the second; 1 and 10 (even CTA)
 // issue the first and second products; 2-9 softmax and epilogue.
+template <bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_decode_pair_kernel(const __grid_constant__ CUtensorMap tma_k, const __grid_constant__ CUtensorMap tma_r,
                            const __grid_constant__ CUtensorMap tma_q, const __grid_constant__ MlaArgs a) {
@@ -193,13 +194,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     pair::tmem_relinquish();
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");       // inputs and workspace of the stream's earlier kernels
-  const Range r = find_range<kThreads, kTile, kMinTiles>(a, c, w, blockIdx.x == 0);
+  const Range r = find_range<TREE, kThreads, kTile, kMinTiles>(a, c, w, blockIdx.x == 0);
   tc_fence_before();
   pair::cluster_sync();                                    // both CTAs' barriers are initialised
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;");       // the join's blocks may be placed; they wait for this grid's end
   const uint32_t tmem = c.tmem;
-  Walk<kTile> wk;
+  Walk<kTile, TREE> wk;
   wk.b = c.start_b;
   wk.t = c.start_t;
   wk.ahead = c.start_len;
@@ -222,7 +223,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && wk.next(a, started)) {
       const int b = __shfl_sync(0xffffffffu, wk.b, 0), len = __shfl_sync(0xffffffffu, wk.len, 0);
       const int t0 = __shfl_sync(0xffffffffu, wk.t0, 0), t1 = t0 + __shfl_sync(0xffffffffu, wk.n, 0);
-      rows.start(a, b, t0, t1, rank * kBlock, len);
+      const Item item = item_of<TREE>(a, b);
+      rows.start(a, item.seq, t0, t1, rank * kBlock, len);
       // The chunks of Q for TMEM pass through ring slots ahead of the piece's tiles.
 #pragma unroll 1
       for (int u = 0; u < nq && ok; ++u) {
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (rank == 0) mbar_arrive_expect_tx(&c.full[lr.slot], 2 * (k1 - u * hc) * kChunk);
 #pragma unroll 1
           for (int k = u * hc; k < k1; ++k)
-            pair_load_3d(lat + lr.slot * slot_bytes + (k - u * hc) * kChunk, &tma_q, k * 64, rank * a.hg, b, full0 + lr.slot * 8);
+            pair_load_3d(lat + lr.slot * slot_bytes + (k - u * hc) * kChunk, &tma_q, k * 64, item.row0 + rank * a.hg, item.seq, full0 + lr.slot * 8);
         }
         __syncwarp();
         lr.step(kSlots);
@@ -291,14 +293,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && wk.next(a, started)) {
       const int b = __shfl_sync(0xffffffffu, wk.b, 0), len = __shfl_sync(0xffffffffu, wk.len, 0);
       const int t0 = __shfl_sync(0xffffffffu, wk.t0, 0), t1 = t0 + __shfl_sync(0xffffffffu, wk.n, 0);
-      rows.start(a, b, t0, t1, blk * kBlock, len);
+      const Item item = item_of<TREE>(a, b);
+      rows.start(a, item.seq, t0, t1, blk * kBlock, len);
       // Chunks of Q in shared memory, once the previous piece's products have read the last ones.
       ok = warp_wait(&c.qe, qphase ^ 1u, a.status, 167);
       if (!ok) break;
       if (elect_one()) {
         if (rank == 0) mbar_arrive_expect_tx(&c.qf, 2 * nss * kChunk);
 #pragma unroll 1
-        for (int k = 0; k < nss; ++k) pair_load_3d(sq + k * kChunk, &tma_q, (a.nts + k) * 64, rank * a.hg, b, qf0);
+        for (int k = 0; k < nss; ++k) pair_load_3d(sq + k * kChunk, &tma_q, (a.nts + k) * 64, item.row0 + rank * a.hg, item.seq, qf0);
       }
       __syncwarp();
       qphase ^= 1u;
@@ -455,7 +458,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int blk = q >> 1;                                // this thread's tokens: 32 sub .. of this block
     const int hl = (q & 1) * 32 + lane;                    // and head of the CTA
     const int head0 = static_cast<int>(rank) * a.hg;       // first head of the CTA
-    const int nh = a.H - head0 < a.hg ? a.H - head0 : a.hg;
+    // heads that a CTA whose first is h0 has of an item
+    auto heads_of = [&](const Item& it, int h0) { return max(0, it.rows - h0 < a.hg ? it.rows - h0 : a.hg); };
     const int tl = sub * 128 + q * 32 + lane;              // a head's four threads: tl with bits 6 and 7 free
     const bool first = blk == 0 && sub == 0;               // the one that speaks for the head
     const uint32_t se0 = pair::map_rank(smem_u32(&c.se), 0), pf0 = pair::map_rank(smem_u32(&c.pf), 0);
@@ -499,6 +503,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (wk.next(a, started)) {
       for (int u = 0; u < nq; ++u) lr.step(kSlots);
       float ref = kNoRef, l = 0.0f, le = 0.0f;
+      const Item item = item_of<TREE>(a, wk.b);
+      const int nh = heads_of(item, head0);
+      Sight sight;                                         // of this thread's row
+      int prefix = 0;
+      if constexpr (TREE) {
+        const int drafted = drafts_of(a, item.seq, wk.len, st == 0);
+        prefix = wk.len - drafted;
+        sight = sight_of(a, item.seq, item.row0 + head0 + hl, drafted);
+      }
       // P of the scores x (a head, 32 tokens), packed, and its sums; the largest score above the reference.
       auto take = [&](const uint32_t* x, uint32_t* p, float& ls, float& les) {
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -530,7 +543,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 32; ++i) reg_fence(x[i]);
         tc_fence_before();
         arrive(se0);
-        if (valid < kTile) {
+        if constexpr (TREE) {
+          const int at = (wk.t0 + ti) * kTile + blk * kBlock + sub * 32;
+          if (at + 32 > prefix || !sight.live) {
+            const uint32_t see = static_cast<uint32_t>(sees(sight, prefix, at));
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((see >> i) & 1u)) x[i] = __float_as_uint(-INFINITY);
+          }
+        } else if (valid < kTile) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (blk * kBlock + sub * 32 + i >= valid) x[i] = __float_as_uint(-INFINITY);
@@ -627,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         norm = v == 0.0f ? 0.0f : 1.0f / v;
         if (whole) {
           if (a.lse != nullptr && hl < nh)
-            a.lse[static_cast<int64_t>(wk.b) * a.H + head0 + hl] = ve == 0.0f ? -INFINITY : (ref + log2f(ve)) * kLn2;
+            a.lse[static_cast<int64_t>(item.seq) * a.H + item.row0 + head0 + hl] = ve == 0.0f ? -INFINITY : (ref + log2f(ve)) * kLn2;
         } else {
           a.part_m[slot * 128 + h] = ref;
           a.part_l[slot * 128 + h] = v;
@@ -662,8 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                               pack_bf16x2(__uint_as_float(o[4 * i + 6]) * f1.x, __uint_as_float(o[4 * i + 7]) * f1.y));
           }
           __syncwarp();
-          const int g0 = grp * a.hg, gn = a.H - g0 < a.hg ? a.H - g0 : a.hg;
-          __nv_bfloat16* out = a.out + (static_cast<int64_t>(wk.b) * a.H + g0) * a.latent + rank * (a.latent / 2) +
+          const int g0 = grp * a.hg, gn = heads_of(item, g0);
+          __nv_bfloat16* out = a.out + (static_cast<int64_t>(item.seq) * a.H + item.row0 + g0) * a.latent + rank * (a.latent / 2) +
                                (mh >> 1) * 128 + q * 32 + (mh & 1) * 16;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -686,13 +707,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Sequences without tokens: zero rows, lse = -inf.
 #pragma unroll 1
     for (int b = w; b < a.B; b += a.W) {
-      if (seq_len(a, b, false) > 0) continue;
-      __nv_bfloat16* out = a.out + (static_cast<int64_t>(b) * a.H + head0) * a.latent;
+      if (seq_len<TREE>(a, b, false) > 0) continue;
+      const Item item = item_of<TREE>(a, b);
+      const int nh = heads_of(item, head0);
+      const int64_t at = static_cast<int64_t>(item.seq) * a.H + item.row0 + head0;
+      __nv_bfloat16* out = a.out + at * a.latent;
 #pragma unroll 1
       for (int i = st; i < nh * a.latent / 8; i += kSoft) reinterpret_cast<uint4*>(out)[i] = make_uint4(0, 0, 0, 0);
       if (a.lse != nullptr)
 #pragma unroll 1
-        for (int i = st; i < nh; i += kSoft) a.lse[static_cast<int64_t>(b) * a.H + head0 + i] = -INFINITY;
+        for (int i = st; i < nh; i += kSoft) a.lse[at + i] = -INFINITY;
+      if constexpr (TREE) {
+        if (st == 0) drafts_of(a, item.seq, 0, true);
+      }
     }
   }
   // Neither CTA leaves (or frees TMEM) while the other may still use its shared memory, its TMEM or its barriers. After
@@ -719,25 +746,28 @@ namespace mla {
 
 bool pair_form(int heads, int latent) { return heads > kMaxHeadsCta && latent % 256 == 0; }
 
+template <bool TREE>
 int run_decode_pair(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CUtensorMap& tq, int sms, cudaStream_t s) {
   static DevOnce once;
   if (!once.ready([] {
-        return cudaFuncSetAttribute(mla_decode_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+        return cudaFuncSetAttribute(mla_decode_pair_kernel<TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
       }))
     return MOE_ERR_CUDA;
   const int hc = a.latent / 128, nchunk = 2 * hc + 1;
   a.W = sms / 2;
-  a.hg = static_cast<int>(ceil_div(a.H, 2));
+  a.hg = static_cast<int>(ceil_div(TREE ? a.hv : a.H, 2));
   // a rope part under 64 columns is zero-filled by its TMA box only, so it stays in shared memory
   a.nts = kMaxTs < nchunk - 1 ? kMaxTs : (a.rope == 64 && kMaxTs >= nchunk ? nchunk : nchunk - 1);
   const size_t smem = 1024 + static_cast<size_t>(nchunk - a.nts + 2 + kSlots * hc + kRopeSlots) * kChunk + kBarBytes +
                       kFloats * sizeof(float);
-  launch_cluster_after("mla_decode_pair", mla_decode_pair_kernel, dim3(static_cast<unsigned>(2 * a.W)), 2, dim3(kThreads),
+  launch_cluster_after("mla_decode_pair", mla_decode_pair_kernel<TREE>, dim3(static_cast<unsigned>(2 * a.W)), 2, dim3(kThreads),
                        smem, s, tk, tr, tq, a);
   if (call_error() != cudaSuccess) return MOE_ERR_CUDA;
-  launch_join<128, true, kTile, kMinTiles>(a, sms, s);
+  launch_join<128, true, TREE, kTile, kMinTiles>(a, sms, s);
   return MOE_OK;
 }
+template int run_decode_pair<false>(MlaArgs, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
+template int run_decode_pair<true>(MlaArgs, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, int, cudaStream_t);
 
 }  // namespace mla
 

@@ -27,6 +27,7 @@ constexpr float kNoRef = -3.0e38f;
 
 struct MlaArgs {
   int B, H, latent, rope, page, num_pages, max_pages;
+                             // (with drafted tokens: B is sequences times row groups, H the rows of a sequence)
   int G, hg;                 // head groups, heads per group
   int nm, um, nu;            // latent / 128; 128-column tiles per ring slot; slots per token tile
   int nlat, nrope;           // ring slots: latent, rope
@@ -51,7 +52,62 @@ struct MlaArgs {
   float* part_m;             // [64] reference (log2 units)
   float* part_l;             // [64] sum of P as rounded for the product
   float* part_e;             // [64] sum of P in fp32 (for the lse)
+  // Drafted tokens. The rows of a sequence are its drafted tokens' heads, token by token, in V groups of hv rows, each of which is
+  // walked like a sequence of its own.
+  int V, hv, heads, drafts;  // heads of a token; most drafted tokens of a sequence
+  const int32_t* draft_lens; // [sequences], or null: `drafts` each
+  const uint64_t* tree;      // [sequences][drafts], or null: each sees the ones before it and itself
 };
+
+// What a walked item b is: a sequence, or (TREE) a group of a sequence's rows.
+struct Item {
+  int seq, row0, rows;       // sequence, first row, rows
+};
+template <bool TREE>
+__device__ __forceinline__ Item item_of(const MlaArgs& a, int b) {
+  if constexpr (TREE) {
+    const int s = b / a.V, r = (b - s * a.V) * a.hv;
+    return {s, r, a.H - r < a.hv ? a.H - r : a.hv};
+  } else {
+    return {b, 0, a.H};
+  }
+}
+// Drafted tokens of a sequence of len tokens: counts outside [0, min(drafts, len)] are clamped (and reported once).
+__device__ __forceinline__ int drafts_of(const MlaArgs& a, int seq, int len, bool report) {
+  const int n = a.draft_lens != nullptr ? ld_global_s32(a.draft_lens + seq) : (len > 0 ? a.drafts : 0);
+  const int most = a.drafts < len ? a.drafts : len;
+  if (n < 0 || n > most) {
+    if (report) report_error(a.status, kErrBounds, 68);
+    return n < 0 ? 0 : most;
+  }
+  return n;
+}
+// What a row sees of its sequence: all tokens before `prefix`, and of those from there on the ones whose bit is set; nothing
+// if its token is not one of the sequence's drafted ones.
+struct Sight {
+  uint64_t mask;
+  bool live;
+};
+__device__ __forceinline__ Sight sight_of(const MlaArgs& a, int seq, int row, int drafted) {
+  const int i = row / a.heads;
+  Sight s{0, i < drafted};
+  if (s.live) {
+    s.mask = 2ull * (1ull << i) - 1ull;                    // (i = 63: all bits)
+    if (a.tree != nullptr) {
+      const uint2 m = ld_global_u2(a.tree + static_cast<int64_t>(seq) * a.drafts + i);
+      s.mask = (static_cast<uint64_t>(m.y) << 32 | m.x) & (2ull * (1ull << (drafted - 1)) - 1ull);
+    }
+  }
+  return s;
+}
+// Bit j: the row sees token at + j, for 64 tokens.
+__device__ __forceinline__ uint64_t sees(const Sight& s, int prefix, int at) {
+  if (!s.live) return 0;
+  const int before = prefix - at;                          // tokens of the prefix from `at` on
+  if (before >= 64) return ~0ull;
+  if (before >= 0) return s.mask << before | ((1ull << before) - 1ull);
+  return before > -64 ? s.mask >> -before : 0;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -68,12 +124,15 @@ __device__ __forceinline__ int valid_len(const MlaArgs& a, int n, bool report) {
   }
   return n;
 }
-__device__ __forceinline__ int seq_len(const MlaArgs& a, int b, bool report) { return valid_len(a, ld_global_s32(a.lens + b), report); }
+template <bool TREE>
+__device__ __forceinline__ int given_len(const MlaArgs& a, int b) { return ld_global_s32(a.lens + (TREE ? b / a.V : b)); }
+template <bool TREE>
+__device__ __forceinline__ int seq_len(const MlaArgs& a, int b, bool report) { return valid_len(a, given_len<TREE>(a, b), report); }
 template <int TILE>
 __device__ __forceinline__ int tiles_of(int len) { return tiles_of(len, TILE); }
 
 // Work of one worker: contiguous pieces of sequences, walked the same way by every role.
-template <int TILE>
+template <int TILE, bool TREE>
 struct Walk {
   int b, t, left;            // next sequence, its next tile, tiles left in the range
   int len, nt;               // current piece's sequence: tokens, tiles
@@ -86,7 +145,7 @@ struct Walk {
     while (true) {
       if (b >= a.B) return false;
       len = valid_len(a, ahead, false);
-      ahead = b + 1 < a.B ? ld_global_s32(a.lens + b + 1) : 0;
+      ahead = b + 1 < a.B ? given_len<TREE>(a, b + 1) : 0;
       nt = tiles_of<TILE>(len);
       if (t < nt) break;
       ++b;
@@ -318,7 +377,7 @@ struct Ring {
 struct Range {
   int total, W, f0, f1;      // all tiles, workers that get tiles, this worker's [f0, f1)
 };
-template <int NT, int TILE, int MIN_TILES, typename Control>
+template <bool TREE, int NT, int TILE, int MIN_TILES, typename Control>
 __device__ __forceinline__ Range find_range(const MlaArgs& a, Control& c, int w, bool report) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (a.B + NT - 1) / NT;
@@ -326,7 +385,7 @@ __device__ __forceinline__ Range find_range(const MlaArgs& a, Control& c, int w,
   const int b1 = b0 + per < a.B ? b0 + per : a.B;
   int mine = 0;
 #pragma unroll 1
-  for (int b = b0; b < b1; ++b) mine += tiles_of<TILE>(seq_len(a, b, report));
+  for (int b = b0; b < b1; ++b) mine += tiles_of<TILE>(seq_len<TREE>(a, b, report));
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -351,7 +410,7 @@ __device__ __forceinline__ Range find_range(const MlaArgs& a, Control& c, int w,
   if (r.f0 >= at && r.f0 < at + mine)
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      const int len = seq_len(a, b, false), n = tiles_of<TILE>(len);
+      const int len = seq_len<TREE>(a, b, false), n = tiles_of<TILE>(len);
       if (r.f0 < at + n) {
         c.start_b = b;
         c.start_t = r.f0 - at;
@@ -425,7 +484,7 @@ struct JoinSum {
       }
   }
 };
-template <int N, bool PAIR>
+template <int N, bool PAIR, bool TREE>
 __global__ void __launch_bounds__(kJoinThreads, 2) mla_join_kernel(const __grid_constant__ MlaArgs a) {
   constexpr int NP = N / 8, kHeads = PAIR ? 2 * kMaxHeadsCta : kMaxHeadsCta;
   __shared__ int4 list[kMaxSms];           // entries with few pieces from the front, the others from the back
@@ -494,8 +553,9 @@ __global__ void __launch_bounds__(kJoinThreads, 2) mla_join_kernel(const __grid_
     const float2 l = acc.l, le = acc.le;
     const float ix = l.x == 0.0f ? 0.0f : 1.0f / l.x, iy = l.y == 0.0f ? 0.0f : 1.0f / l.y;
     const int hg = PAIR ? h >> 6 : g, hl = PAIR ? h & 63 : h;
-    const int head0 = hg * a.hg, nh = a.H - head0 < a.hg ? a.H - head0 : a.hg;
-    const int64_t row = static_cast<int64_t>(j.x) * a.H + head0 + hl;
+    const Item item = item_of<TREE>(a, j.x);
+    const int head0 = hg * a.hg, nh = item.rows - head0 < a.hg ? item.rows - head0 : a.hg;
+    const int64_t row = static_cast<int64_t>(item.seq) * a.H + item.row0 + head0 + hl;
     if (a.lse != nullptr && m == 0 && t < 4 && (!PAIR || g == 0)) {
       if (hl < nh) a.lse[row] = le.x == 0.0f ? -INFINITY : (acc.top.x + log2f(le.x)) * kLn2;
       if (hl + 1 < nh) a.lse[row + 1] = le.y == 0.0f ? -INFINITY : (acc.top.y + log2f(le.y)) * kLn2;
@@ -576,7 +636,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) mla_join_kernel(const __grid_
 
 // The join of a decode launch just made on the same stream. Its blocks start when the last decode CTAs leave room and
 // wait for their writes on the device.
-template <int N, bool PAIR, int TILE, int MIN_TILES>
+template <int N, bool PAIR, bool TREE, int TILE, int MIN_TILES>
 void launch_join(const MlaArgs& a, int sms, cudaStream_t s) {
   const int64_t each = (PAIR ? 2 : a.G) * (a.latent / (PAIR ? 256 : 128)) * (N / 8);
   const int64_t most = a.B < a.W ? a.B : a.W;               // sequences that can be cut
@@ -585,13 +645,14 @@ void launch_join(const MlaArgs& a, int sms, cudaStream_t s) {
   const int64_t pieces = tiles / MIN_TILES < a.W ? tiles / MIN_TILES : a.W;
   const int cluster = pieces > kJoinLong && most * each * kJoinCluster <= slots ? kJoinCluster : 1;
   const int64_t grid = most * each * cluster < slots ? most * each * cluster : slots;
-  launch_cluster_after("mla_join", mla_join_kernel<N, PAIR>, dim3(static_cast<unsigned>(grid)), cluster,
+  launch_cluster_after("mla_join", mla_join_kernel<N, PAIR, TREE>, dim3(static_cast<unsigned>(grid)), cluster,
                        dim3(kJoinThreads), (2 * cluster - 1) * sizeof(JoinPart), s, a);
 }
 
 // Decode with both head groups on one pair of CTAs (more than 64 heads, an even number of 128-column tiles), and
 // its condition. The maps' boxes hold half of a row's latent columns.
 bool pair_form(int heads, int latent);
+template <bool TREE>
 int run_decode_pair(MlaArgs a, const CUtensorMap& tk, const CUtensorMap& tr, const CUtensorMap& tq, int sms, cudaStream_t s);
 
 }  // namespace mla
