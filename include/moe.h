@@ -554,7 +554,7 @@ MOE_API int moe_pages_update(int batch, int page_size, int num_pages, int max_pa
 MOE_API int moe_pages_status(void* ws, int* code, int* site, int clear, moe_stream_t stream);
 
 /* The whole layer for a few tokens: moe_route, moe_schedule and moe_forward in one
- * call of three launches, for decoding steps and drafted tokens.
+ * call of two launches, for decoding steps and drafted tokens.
  *   logits = x Wr^T, the choice of moe_route (idx, w), and
  *   y = sum_j w_j MX(h_j) Wd_j^T + the shared expert's, h = silu(g) u, [g | u] = MX(x) Wgu^T,
  * with the quantised weights of moe_quantize_weights (the same blob: it does not

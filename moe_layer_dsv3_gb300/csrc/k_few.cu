@@ -1,9 +1,8 @@
-// The whole layer for up to 64 tokens: router, experts and combine in three
-// launches, each placed while the one before still runs.
+// The whole layer for up to 64 tokens: router, experts and combine in two
+// launches, the second placed while the first still runs.
 //
-//   route   logits = x Wr^T, the choice of every token (route.cuh), MX(x)
-//   up      [g | u] = Wgu MX(x)^T, h = silu(g) u, MX(h)
-//   down    o = Wd MX(h)^T, y = sum over a token's experts of w o
+//   route    logits = x Wr^T, the choice of every token (route.cuh), MX(x)
+//   experts  [g | u] = Wgu MX(x)^T, h = silu(g) u, o = Wd MX(h)^T, y = sum over a token's experts of w o
 //
 // Few tokens read many weights: one token of 9 experts with 7168 x 2048 matrices
 // reads 410 MB for 0.8 GFLOP, and HBM bounds it (0.4 us of products, 60 us of
@@ -12,25 +11,27 @@
 // through shared memory once, for all tokens, and nothing has to be converted,
 // gathered or padded to 128 rows.
 //
-// Each of the two expert kernels streams the weight tiles of all experts in use,
-// laid end to end, cut into equal contiguous ranges, one per CTA. A range may begin and end
-// inside a reduction: the pieces of a cut one are left in the workspace, and the
-// CTA that arrives last adds them in the order of the ranges, so the result does
-// not depend on who that is. No CTA waits for another.
+// The work is a list of pieces, which CTAs take from its front one after another:
+//   up    256 interleaved gate and up rows of one expert, all of K = d or a part of it.
+//         All T tokens are columns, also those that did not choose the expert: a product of
+//         16 columns takes the tensor pipe a tenth of the time its weights take to arrive,
+//         and X needs no gather. Parts leave g and u in the workspace, and the CTA that
+//         stores the last part adds them in their order, forms h and quantises it.
+//   down  256 rows of one expert, all of K = I or a part; the expert's tokens are columns.
+//         The rows of o go to the workspace in fp32.
+// All up pieces come first, and down pieces of an expert wait until its h is
+// complete; their weights are loaded without waiting. At the end every CTA waits for the last
+// piece and sums a share of y. What a CTA waits for was taken before by a
+// CTA that runs and waits for nothing later, so no wait needs all CTAs to be resident. Which CTA
+// takes a piece changes no result: parts and sums have a fixed order.
 //
-//   up    unit: 128 gate rows and their 128 up rows of one expert (K = d). All T
-//         tokens are columns, also those that did not choose the expert: a
-//         product of 16 columns takes the tensor pipe a tenth of the time its
-//         weights take to arrive, and X needs no gather.
-//   down  unit: 128 rows of one expert (K = I), the tokens of the expert as columns.
-//         Units of the same rows follow one another, expert by expert, so that
-//         their weighted sum stays in shared memory and only rows that a range cuts pass
-//         through the workspace.
-// `down` starts on its weights before `up` is done: they do not depend on it.
+// Taken from a list, pieces keep every SM loading to the end. Equal ranges fixed in
+// advance, in a kernel for each projection, left some SMs 15 % behind the others (HBM does
+// not serve all alike), and HBM idle for 9 us between the kernels: 106 us for one
+// token, 403 for 16 and 544 for 64, where the list takes NEWFIG.
 #include <cudaTypedefs.h>
 
 #include "gemm.cuh"
-#include "mla_split.h"
 #include "prof.h"
 #include "route.cuh"
 
@@ -38,20 +39,17 @@ namespace moe {
 
 namespace {
 
-using mla::cut_of;
-using mla::owner_of;
-using mla::range_begin;
-using mla::workers_of;
-
 constexpr int kMaxT = MOE_FEW_MAX_T;
 constexpr int kMaxEp = 513;                // experts, a shared one included
-constexpr int kMaxRows = kMaxT * 9;        // (token, expert) pairs
-constexpr int kThreads = 192;
+constexpr int kMaxPicks = kMaxT * 8;       // routed (token, expert) pairs
+constexpr int kThreads = 224;
 constexpr int kMaxStages = 12;
 constexpr int kTileBytes = 128 * 128;      // a weight tile: 128 rows x 128 values
 constexpr int kSmemMax = 232448;
 constexpr int kSfCol = 256;                // TMEM: accumulators below, scales of the ring's stages from here on
-constexpr int kMinSteps = 4;               // fewest steps of a CTA
+constexpr int kQueue = 4;                  // pieces on their way from the warp that takes them to the others
+constexpr int kUpPieces = 4, kDownPieces = 8;   // pieces of a CTA that K is cut for, where there are fewer
+constexpr int kMinSteps = 2;               // fewest 128-wide steps of a part
 static_assert(kMaxT == 64, "a token is a bit of an expert's 64-bit mask");
 
 struct FewArgs {
@@ -66,17 +64,25 @@ struct FewArgs {
   float* logits;                           // [T][E]
   uint8_t* xq;                             // [64][d]
   uint8_t* xsf;                            // [d / 128] atoms
-  const uint8_t* wsf;                      // scales of the kernel's weights
+  const uint8_t* w1sf;                     // scales of the weights
+  const uint8_t* w2sf;
   uint8_t* hq;                             // [rows][I], an expert's tokens one after another
   uint8_t* hsf;                            // [experts in use][I / 128] atoms
-  float* part;                             // pieces of cut units, two per CTA
+  float* gu;                               // [rows][I / 128][parts][256]: parts of g and u
+  float* o;                                // [rows][parts][d]
   int* cnt_route;                          // per token group: CTAs done
-  int* cnt_up;                             // per unit: pieces done
-  int* cnt_down;                           // per 128 rows: pieces done
-  int ncnt;                                // of the last two, which lie together
+  int* cnt;                                // counters of `experts`, cleared by `route`: pieces taken, pieces of down done,
+  int ncnt;                                // then per expert slot its blocks of h done, then per block its parts done
   __nv_bfloat16* y;
   int* status;
 };
+
+// Parts that K (`steps` steps) of `units` units is cut into, so that each of `ctas` CTAs gets `want` pieces.
+__host__ __device__ __forceinline__ int parts_of(int units, int steps, int ctas, int want) {
+  const int most = steps / kMinSteps > 1 ? steps / kMinSteps : 1;
+  const int n = (ctas * want + units - 1) / units;
+  return n < most ? n : most;
+}
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -89,6 +95,19 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int site) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, site));
+}
+// Barrier over the epilogue's 128 threads that also gives the OR of their flags.
+__device__ __forceinline__ bool epilogue_or(bool flag) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(flag))
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -117,7 +136,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
 constexpr int kRouteThreads = 256;
 constexpr int kRowWarps = 4;
 
-template <int TG, int ER>
+template <int TG, int ER, int PER>
 __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_constant__ FewArgs a) {
   constexpr int kSets = 8 / kRowWarps;
   constexpr int kDeep = TG == 1 ? 4 : 1;                   // chunks whose loads are under way together
@@ -139,7 +158,7 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_c
       for (int q = 0; q < 4; ++q) unpack_bf16x8(ld_global_u4(a.x + at + 8 * q), v + 8 * q);
       emit_rowq(v, a.xq + at, a.xsf + sf_off(t, b, a.d >> 7));
     }
-    for (int i = (bid - NE * NG) * kRouteThreads + tid; i < a.ncnt; i += step) a.cnt_up[i] = 0;
+    for (int i = (bid - NE * NG) * kRouteThreads + tid; i < a.ncnt; i += step) a.cnt[i] = 0;
     return;
   }
   const int g = bid / NE, set = warp / kRowWarps, part = warp % kRowWarps;
@@ -208,7 +227,7 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_c
     if (t >= a.T) break;
     int e;
     float s, tot;
-    choose_experts<16>([&](int n) { return __ldcg(a.logits + static_cast<int64_t>(t) * a.E + n); },
+    choose_experts<PER, BestByRedux>([&](int n) { return __ldcg(a.logits + static_cast<int64_t>(t) * a.E + n); },
                        [&](int n) { return __int_as_float(ld_global_s32(reinterpret_cast<const int*>(a.bias + n))); }, a.E, a.k,
                        a.G, a.gtop, sv_all + warp * a.E, lane, e, s, tot);
     if (lane < a.k) {
@@ -226,8 +245,8 @@ struct FewPlan {
   uint16_t expert[kMaxEp];                 // of a slot
   uint16_t slot[kMaxEp];                   // of an expert in use
   uint16_t first[kMaxEp + 1];              // row of a slot's first token
-  uint8_t token[kMaxRows];                 // of a row
-  float gate[kMaxRows];
+  uint16_t row[kMaxPicks];                 // of a token's pick
+  float gate[kMaxPicks];
   uint32_t bad[2];                         // tokens without a valid choice: their scores are NaN
   uint32_t scan[kThreads / 32];
   int slots;
@@ -284,32 +303,29 @@ __device__ __forceinline__ void make_plan(const FewArgs& a, FewPlan& p, bool rep
     p.first[all >> 16] = static_cast<uint16_t>(all & 0xffffu);
   }
   __syncthreads();
-  auto place = [&](int e, int t, float w) {
+  for (int i = tid; i < n; i += kThreads) {
+    const int e = ld_global_s32(a.idx + i), t = i / a.k;
+    if (e < 0 || e >= a.E) continue;
     const uint32_t below = t < 32 ? __popc(p.mask[e][0] & ((1u << t) - 1u))
                                   : __popc(p.mask[e][0]) + __popc(p.mask[e][1] & ((1u << (t - 32)) - 1u));
-    const int row = p.first[p.slot[e]] + static_cast<int>(below);
-    p.token[row] = static_cast<uint8_t>(t);
-    p.gate[row] = w;
-  };
-  for (int i = tid; i < n; i += kThreads) {
-    const int e = ld_global_s32(a.idx + i);
-    if (e >= 0 && e < a.E) place(e, i / a.k, __int_as_float(ld_global_s32(reinterpret_cast<const int*>(a.w + i))));
+    p.row[i] = static_cast<uint16_t>(p.first[p.slot[e]] + below);
+    p.gate[i] = __int_as_float(ld_global_s32(reinterpret_cast<const int*>(a.w + i)));
   }
-  if (a.S > 0)
-    for (int t = tid; t < a.T; t += kThreads) place(a.E, t, 1.0f);
   __syncthreads();
 }
 
 struct FewSmem {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t accf[4], acce[4];
+  uint64_t accf[2], acce[2];
+  uint64_t qf[kQueue], qe[kQueue];
+  int queue[kQueue];                       // pieces, -1 after the last
   uint32_t tmem;
   int last;
   FewPlan plan;
 };
 constexpr int kControl = (sizeof(FewSmem) + 1023) / 1024 * 1024;
 
-// Place in the ring of stages.
+// Place in a ring.
 struct Stage {
   int i = 0;
   uint32_t phase = 0;
@@ -321,151 +337,222 @@ struct Stage {
   }
 };
 
-// The steps of a range, unit by unit. A step is one 128-wide piece of K of a unit with K / 128 = len steps.
-struct Walk {
-  int unit, at, left, len;
-  __device__ __forceinline__ Walk(int f0, int f1, int len_) : unit(f0 / len_), at(f0 - f0 / len_ * len_), left(f1 - f0), len(len_) {}
-  __device__ __forceinline__ int steps() const { return left < len - at ? left : len - at; }   // in the current unit
-  __device__ __forceinline__ void next() {
-    left -= steps();
-    ++unit;
-    at = 0;
-  }
+// The list of pieces.
+struct Work {
+  int KA, KI, NB, RP, slots;               // steps of d and of I, blocks of 256 up and of 256 down rows, experts in use
+  int PU, PD, nup, total;                  // parts, pieces
 };
-
-// The worker that arrives last at a cut sum adds its pieces. Called by the 128 epilogue threads after their piece is stored;
-// true in all of them if every piece is there.
-__device__ __forceinline__ bool last_piece(FewSmem& c, int* cnt, int pieces) {
-  __threadfence();
-  named_barrier(1, 128);
-  if (threadIdx.x == 64) c.last = atomicAdd(cnt, 1) == pieces - 1;
-  named_barrier(1, 128);
-  if (c.last == 0) return false;
-  __threadfence();
-  return true;
+struct Piece {
+  bool up;
+  int s, b, part, k0, k1;                  // expert slot, block of rows, part of K, its steps
+};
+__device__ __forceinline__ Piece piece_of(const Work& w, int id) {
+  Piece p;
+  p.up = id < w.nup;
+  if (p.up) {
+    const int u = id / w.PU;
+    p.part = id - u * w.PU;
+    p.s = u / w.NB;
+    p.b = u - p.s * w.NB;
+    p.k0 = w.KA * p.part / w.PU;
+    p.k1 = w.KA * (p.part + 1) / w.PU;
+  } else {
+    const int q = id - w.nup, u = q / w.RP;
+    p.b = q - u * w.RP;
+    p.s = u / w.PD;
+    p.part = u - p.s * w.PD;
+    p.k0 = w.KI * p.part / w.PD;
+    p.k1 = w.KI * (p.part + 1) / w.PD;
+  }
+  return p;
 }
 
-__device__ __forceinline__ void few_setup(FewSmem& c, int nst, const CUtensorMap* a, const CUtensorMap* b) {
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < nst; ++i) {
-      mbar_init(&c.full[i], 1);
-      mbar_init(&c.empty[i], 1);
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&c.accf[i], 1);
-      mbar_init(&c.acce[i], 128);
-    }
-    fence_barrier_init();
-    fence_proxy_async();
-    tma_prefetch(a);
-    tma_prefetch(b);
-  }
-  if (threadIdx.x >> 5 == 1) {
-    tmem_alloc(&c.tmem, 512);
-    tmem_relinquish();
-  }
-}
-__device__ __forceinline__ void few_finish(uint32_t tmem, bool ok) {
-  tc_fence_before();
-  if (__syncthreads_or(!ok)) drain_pause();
-  if (threadIdx.x >> 5 == 1) {
-    tc_fence_after();
-    __syncwarp();
-    tmem_dealloc(tmem, 512);
-  }
-}
-
-// The copies of the last stages that were issued have landed.
-__device__ __forceinline__ bool land(FewSmem& c, Stage st, int issued, int nst, int* status, int site) {
-  bool ok = true;
-  for (int i = 0, n = issued < nst ? issued : nst; i < n; ++i) {
-    if (--st.i < 0) {
-      st.i = nst - 1;
-      st.phase ^= 1u;
-    }
-    ok = warp_wait(&c.full[st.i], st.phase, status, site) && ok;
-  }
-  return ok;
-}
-
-// ---------------------------------------------------------------- gate and up projections
-// Warps: 0 loads, 1 issues the products, 2-5 epilogue (row = TMEM lane).
-// Stage: [256 rows of weights][N rows of X], and the scale atoms of gate, up and X.
+// Warps: 0 takes pieces and loads weights, 6 loads X and H, 1 issues the products, 2-5 epilogue (row = TMEM lane).
+// Stage: [256 rows of weights][N rows of X or H], and three scale atoms.
 __global__ void __launch_bounds__(kThreads, 1)
-    few_up_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUtensorMap tma_x,
-                  const __grid_constant__ FewArgs a) {
+    few_experts_kernel(const __grid_constant__ CUtensorMap tma_w1, const __grid_constant__ CUtensorMap tma_w2,
+                       const __grid_constant__ CUtensorMap tma_x, const __grid_constant__ CUtensorMap tma_h,
+                       const __grid_constant__ FewArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   FewSmem& c = *reinterpret_cast<FewSmem*>(smem);
   uint8_t* ring = smem + kControl;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  few_setup(c, a.nst, &tma_w, &tma_x);
+  uint8_t* scales = ring + a.nst * a.stage_bytes;          // three atoms a stage
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < a.nst; ++i) {
+      mbar_init(&c.full[i], 2);                            // the two loading warps
+      mbar_init(&c.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.accf[i], 1);
+      mbar_init(&c.acce[i], 128);
+    }
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(&c.qf[i], 1);
+      mbar_init(&c.qe[i], 6);                              // the other warps
+    }
+    fence_barrier_init();
+    fence_proxy_async();
+    tma_prefetch(&tma_w1);
+    tma_prefetch(&tma_w2);
+    tma_prefetch(&tma_x);
+    tma_prefetch(&tma_h);
+  }
+  if (warp == 1) {
+    tmem_alloc(&c.tmem, 512);
+    tmem_relinquish();
+  }
   grid_wait();
   grid_launch();
   tc_fence_before();
   make_plan(a, c.plan, blockIdx.x == 0);                   // (ends with a barrier)
   tc_fence_after();
   const uint32_t tmem = c.tmem;
-  const int KA = a.d >> 7, NB = a.I >> 7;
-  const int total = c.plan.slots * NB * KA;
-  const int W = workers_of(total, static_cast<int>(gridDim.x), kMinSteps), w = static_cast<int>(blockIdx.x);
-  const int f0 = w < W ? range_begin(total, w, W) : total, f1 = w < W ? range_begin(total, w + 1, W) : total;
+  Work w;
+  w.KA = a.d >> 7;
+  w.KI = a.I >> 7;
+  w.NB = a.I >> 7;
+  w.RP = ((a.d >> 7) + 1) >> 1;
+  w.slots = c.plan.slots;
+  const int ctas = static_cast<int>(gridDim.x);
+  w.PU = w.slots > 0 ? parts_of(w.slots * w.NB, w.KA, ctas, kUpPieces) : 1;
+  w.PD = w.slots > 0 ? parts_of(w.slots * w.RP, w.KI, ctas, kDownPieces) : 1;
+  w.nup = w.slots * w.NB * w.PU;
+  w.total = w.nup + w.slots * w.RP * w.PD;
+  int* taken = a.cnt;
+  int* done = a.cnt + 1;
+  int* ready = a.cnt + 2;
+  int* parts = ready + w.slots;
   bool ok = true;
-  uint8_t* scales = ring + a.nst * a.stage_bytes;          // three atoms a stage
+  // The next piece, for the warps that follow warp 0.
+  Stage q;
+  auto next_piece = [&]() {
+    ok = warp_wait(&c.qf[q.i], q.phase, a.status, 201);
+    if (!ok) return -1;
+    const int id = *reinterpret_cast<volatile int*>(&c.queue[q.i]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c.qe[q.i]);
+    q.step(kQueue);
+    return __shfl_sync(0xffffffffu, id, 0);
+  };
+  // Every copy that this warp issued has landed.
+  auto land = [&](Stage st, int issued) {
+    for (int i = 0, n = issued < a.nst ? issued : a.nst; i < n; ++i) {
+      if (--st.i < 0) {
+        st.i = a.nst - 1;
+        st.phase ^= 1u;
+      }
+      ok = warp_wait(&c.full[st.i], st.phase, a.status, 202) && ok;
+    }
+  };
   if (warp == 0) {
     Stage st;
     int issued = 0;
-    for (Walk wk(f0, f1, KA); wk.left > 0 && ok; wk.next()) {
-      const int s = wk.unit / NB, b = wk.unit - s * NB, e = c.plan.expert[s];
-      const int row = __shfl_sync(0xffffffffu, e * 2 * a.I + b * 256, 0);
-      const uint8_t* sf = a.wsf + static_cast<int64_t>(row >> 7) * KA * 512;
-      const int k1 = __shfl_sync(0xffffffffu, wk.at + wk.steps(), 0);
+    int id = static_cast<int>(blockIdx.x);
+    while (ok) {
+      const bool more = id < w.total;
+      ok = warp_wait(&c.qe[q.i], q.phase ^ 1u, a.status, 203);
+      if (!ok) break;
+      int ahead = 0;
+      if (lane == 0) {
+        *reinterpret_cast<volatile int*>(&c.queue[q.i]) = more ? id : -1;
+        mbar_arrive(&c.qf[q.i]);
+        if (more) ahead = atomicAdd(taken, 1);             // its latency passes behind this piece's loads
+      }
+      __syncwarp();
+      q.step(kQueue);
+      if (!more) break;
+      const Piece p = piece_of(w, id);
+      const int e = c.plan.expert[p.s], K = p.up ? w.KA : w.KI;
+      const int row = __shfl_sync(0xffffffffu, p.up ? e * 2 * a.I + p.b * 256 : e * a.d + p.b * 256, 0);
+      const int tiles = p.up || 2 * p.b + 1 < w.KA ? 2 : 1;
+      const CUtensorMap* map = p.up ? &tma_w1 : &tma_w2;
+      const uint8_t* sf = (p.up ? a.w1sf : a.w2sf) + static_cast<int64_t>(row >> 7) * K * 512;
 #pragma unroll 1
-      for (int k = __shfl_sync(0xffffffffu, wk.at, 0); k < k1; ++k) {
-        ok = warp_wait(&c.empty[st.i], st.phase ^ 1u, a.status, 201);
+      for (int k = p.k0; k < p.k1; ++k) {
+        ok = warp_wait(&c.empty[st.i], st.phase ^ 1u, a.status, 204);
         if (!ok) break;
         if (elect_one()) {
           uint8_t* dst = ring + st.i * a.stage_bytes;
-          uint64_t* bar = &c.full[st.i];
-          mbar_arrive_expect_tx(bar, 2 * kTileBytes + a.N * 128 + 3 * 512);
-          tma_load_2d(dst, &tma_w, k * 128, row, bar);
-          tma_load_2d(dst + 2 * kTileBytes, &tma_x, k * 128, 0, bar);
           uint8_t* sfd = scales + st.i * (3 * 512);
+          uint64_t* bar = &c.full[st.i];
+          mbar_arrive_expect_tx(bar, tiles * (kTileBytes + 512));
+          tma_load_2d(dst, map, k * 128, row, bar);
+          if (tiles == 2) tma_load_2d(dst + kTileBytes, map, k * 128, row + 128, bar);
           bulk_load(sfd, sf + static_cast<int64_t>(k) * 512, 512, bar);
-          bulk_load(sfd + 512, sf + static_cast<int64_t>(KA + k) * 512, 512, bar);
-          bulk_load(sfd + 1024, a.xsf + static_cast<int64_t>(k) * 512, 512, bar);
+          if (tiles == 2) bulk_load(sfd + 512, sf + static_cast<int64_t>(K + k) * 512, 512, bar);
+        }
+        __syncwarp();
+        st.step(a.nst);
+        ++issued;
+      }
+      id = ctas + __shfl_sync(0xffffffffu, ahead, 0);
+    }
+    land(st, issued);
+  } else if (warp == 6) {
+    Stage st;
+    int issued = 0;
+    int have = -1;                                         // the last expert whose h was found complete
+    for (int id; ok && (id = next_piece()) >= 0;) {
+      const Piece p = piece_of(w, id);
+      const int row = p.up ? 0 : c.plan.first[p.s];
+      const int boxes = p.up ? a.N >> 4 : (c.plan.first[p.s + 1] - row + 15) >> 4;
+      const CUtensorMap* map = p.up ? &tma_x : &tma_h;
+      const uint8_t* sf = p.up ? a.xsf : a.hsf + static_cast<int64_t>(p.s) * w.KI * 512;
+      if (!p.up && p.s != have) {
+        ok = __all_sync(0xffffffffu, wait_counter(ready + p.s, w.NB, a.status, 205));
+        if (!ok) break;
+        fence_proxy_async_global();
+        have = p.s;
+      }
+#pragma unroll 1
+      for (int k = p.k0; k < p.k1; ++k) {
+        ok = warp_wait(&c.empty[st.i], st.phase ^ 1u, a.status, 206);
+        if (!ok) break;
+        if (elect_one()) {
+          uint8_t* dst = ring + st.i * a.stage_bytes + 2 * kTileBytes;
+          uint64_t* bar = &c.full[st.i];
+          mbar_arrive_expect_tx(bar, boxes * 2048 + 512);
+#pragma unroll 1
+          for (int j = 0; j < boxes; ++j) tma_load_2d(dst + j * 2048, map, k * 128, row + j * 16, bar);
+          bulk_load(scales + st.i * (3 * 512) + 1024, sf + static_cast<int64_t>(k) * 512, 512, bar);
         }
         __syncwarp();
         st.step(a.nst);
         ++issued;
       }
     }
-    ok = land(c, st, issued, a.nst, a.status, 202) && ok;
+    land(st, issued);
   } else if (warp == 1) {
     Stage st, acc;
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t idesc = idesc_mxf8(128, a.N), sf0 = smem_u32(scales);
-    for (Walk wk(f0, f1, KA); wk.left > 0 && ok; wk.next()) {
-      ok = warp_wait(&c.acce[acc.i], acc.phase ^ 1u, a.status, 203);
-      const int n = __shfl_sync(0xffffffffu, wk.steps(), 0);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sf0 = smem_u32(scales);
+    for (int id; ok && (id = next_piece()) >= 0;) {
+      const Piece p = piece_of(w, id);
+      const int tiles = p.up || 2 * p.b + 1 < w.KA ? 2 : 1;
+      const int cols = __shfl_sync(0xffffffffu, p.up ? a.N : (c.plan.first[p.s + 1] - c.plan.first[p.s] + 15) & ~15, 0);
+      const uint32_t idesc = idesc_mxf8(128, 0) | (static_cast<uint32_t>(cols >> 3) << 17);
+      ok = warp_wait(&c.acce[acc.i], acc.phase ^ 1u, a.status, 207);
       const uint32_t d = tm + acc.i * 128;
 #pragma unroll 1
-      for (int k = 0; k < n && ok; ++k) {
-        ok = warp_wait(&c.full[st.i], st.phase, a.status, 204);
+      for (int k = p.k0; k < p.k1 && ok; ++k) {
+        ok = warp_wait(&c.full[st.i], st.phase, a.status, 208);
         tc_fence_after();
         if (ok && elect_one()) {
-          const uint32_t base = smem_u32(ring + st.i * a.stage_bytes), sf = tm + kSfCol + st.i * 12;
+          const uint32_t base = smem_u32(ring + st.i * a.stage_bytes), sf = tm + kSfCol + st.i * 12, sfs = sf0 + st.i * (3 * 512);
+          tc_cp_sf(sf + 8, desc_sf_chunk(sfs + 1024));
 #pragma unroll
-          for (int j = 0; j < 3; ++j) tc_cp_sf(sf + 4 * j, desc_sf_chunk(sf0 + st.i * (3 * 512) + 512 * j));
+          for (int j = 0; j < 2; ++j)
+            if (j < tiles) {
+              tc_cp_sf(sf + 4 * j, desc_sf_chunk(sfs + 512 * j));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              tc_mma_mxf8(d + 64 * j, desc_kmajor_sw128(base + j * kTileBytes + kk * 32),
-                          desc_kmajor_sw128(base + 2 * kTileBytes + kk * 32), idesc_mxf8_sf(idesc, kk, kk), sf + 4 * j, sf + 8,
-                          (k | kk) != 0);
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_mxf8(d + 64 * j, desc_kmajor_sw128(base + j * kTileBytes + kk * 32),
+                            desc_kmajor_sw128(base + 2 * kTileBytes + kk * 32), idesc_mxf8_sf(idesc, kk, kk), sf + 4 * j, sf + 8,
+                            k > p.k0 || kk > 0);
+            }
           tc_commit(&c.empty[st.i]);
-          if (k == n - 1) tc_commit(&c.accf[acc.i]);
+          if (k == p.k1 - 1) tc_commit(&c.accf[acc.i]);
         }
         __syncwarp();
         st.step(a.nst);
@@ -473,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       acc.step(2);
     }
   } else {
-    const int q = warp & 3, row = q * 32 + lane;
+    const int lq = warp & 3, row = lq * 32 + lane;
     Stage acc;
     // MX(h) of a token: its 32 values lie in the warp's lanes.
     auto emit = [&](int s, int r, int b, float g, float u) {
@@ -482,266 +569,161 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int sb = mx_scale_byte(__uint_as_float(top));
       const uint32_t code = e4m3x2(h * mx_inv_scale(sb), 0.0f) & 0xffu;
       a.hq[static_cast<int64_t>(c.plan.first[s] + r) * a.I + b * 128 + row] = static_cast<uint8_t>(code);
-      if (lane == 0) a.hsf[(static_cast<int64_t>(s) * NB + b) * 512 + (r & 31) * 16 + (r >> 5) * 4 + q] = static_cast<uint8_t>(sb);
+      if (lane == 0) a.hsf[(static_cast<int64_t>(s) * w.KI + b) * 512 + (r & 31) * 16 + (r >> 5) * 4 + lq] = static_cast<uint8_t>(sb);
     };
-    for (Walk wk(f0, f1, KA); wk.left > 0 && ok; wk.next()) {
-      const int s = wk.unit / NB, b = wk.unit - s * NB, e = c.plan.expert[s];
-      const bool whole = wk.steps() == KA;
-      const int u0 = wk.unit * KA;
-      float* mine = a.part + static_cast<int64_t>(2 * w + (u0 < f0 || wk.left == f1 - f0 ? 0 : 1)) * a.T * 256 + row;
-      ok = __all_sync(0xffffffffu, mbar_wait(&c.accf[acc.i], acc.phase, a.status, 205));
-      if (!ok) break;
+    while (true) {
+      const int id = next_piece();
+      if (id >= 0) ok = mbar_wait(&c.accf[acc.i], acc.phase, a.status, 209);
+      // Whether a wait gave up is the answer of all four warps, which meet at barriers below.
+      ok = !epilogue_or(!ok);
+      if (!ok || id < 0) break;
       tc_fence_after();
-      const uint32_t tacc = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc.i * 128;
-      int r = 0;
+      const Piece p = piece_of(w, id);
+      const int row0 = c.plan.first[p.s], n = c.plan.first[p.s + 1] - row0;
+      const uint32_t tacc = tmem + (static_cast<uint32_t>(lq * 32) << 16) + acc.i * 128;
+      if (p.up) {
+        const int e = c.plan.expert[p.s];
+        const bool whole = w.PU == 1;
+        // parts of row r: gu + r * gu_step, the next part 256 floats on
+        const int64_t gu_step = static_cast<int64_t>(w.NB) * w.PU * 256;
+        float* gu = a.gu + (static_cast<int64_t>(row0) * w.NB + p.b) * w.PU * 256 + row;
+        int r = 0;
 #pragma unroll 1
-      for (int t0 = 0; t0 < a.T; t0 += 16) {
-        const uint32_t m = (c.plan.mask[e][t0 >> 5] >> (t0 & 31)) & 0xffffu;
-        if (m == 0) continue;
-        uint32_t g[16], u[16];
-        tmem_ld16(tacc + t0, g);
-        tmem_ld16(tacc + 64 + t0, u);
-        tmem_wait_ld();
+        for (int t0 = 0; t0 < a.T; t0 += 16) {
+          const uint32_t m = (c.plan.mask[e][t0 >> 5] >> (t0 & 31)) & 0xffffu;
+          if (m == 0) continue;
+          uint32_t g[16], u[16];
+          tmem_ld16(tacc + t0, g);
+          tmem_ld16(tacc + 64 + t0, u);
+          tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          reg_fence(g[i]);
-          reg_fence(u[i]);
-        }
+          for (int i = 0; i < 16; ++i) {
+            reg_fence(g[i]);
+            reg_fence(u[i]);
+          }
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if ((m >> i) & 1u) {
-            if (whole) {
-              emit(s, r, b, __uint_as_float(g[i]), __uint_as_float(u[i]));
-            } else {
-              mine[r * 256] = __uint_as_float(g[i]);
-              mine[r * 256 + 128] = __uint_as_float(u[i]);
+          for (int i = 0; i < 16; ++i)
+            if ((m >> i) & 1u) {
+              if (whole) {
+                emit(p.s, r, p.b, __uint_as_float(g[i]), __uint_as_float(u[i]));
+              } else {
+                float* to = gu + r * gu_step + p.part * 256;
+                to[0] = __uint_as_float(g[i]);
+                to[128] = __uint_as_float(u[i]);
+              }
+              ++r;
             }
-            ++r;
-          }
-      }
-      tc_fence_before();
-      mbar_arrive(&c.acce[acc.i]);
-      acc.step(2);
-      if (whole) continue;
-      const int last = owner_of(total, u0 + KA - 1, W);
-      const mla::Cut cut = cut_of(total, W, u0, last);
-      if (!last_piece(c, a.cnt_up + wk.unit, cut.pieces)) continue;
-#pragma unroll 1
-      for (int i = 0; i < r; ++i) {
-        float g = 0.0f, u = 0.0f;
-        for (int p = 0; p < cut.pieces; ++p) {
-          const float* src = a.part + static_cast<int64_t>(2 * (cut.worker + p) + (p == 0 ? cut.slot : 0)) * a.T * 256 + row + i * 256;
-          g += __ldcg(src);
-          u += __ldcg(src + 128);
         }
-        emit(s, i, b, g, u);
-      }
-    }
-  }
-  few_finish(tmem, ok);
-}
-
-// ---------------------------------------------------------------- down projection and combine
-// Stage: [128 rows of weights][up to N rows of H], and the scale atoms of both.
-__global__ void __launch_bounds__(kThreads, 1)
-    few_down_kernel(const __grid_constant__ CUtensorMap tma_w, const __grid_constant__ CUtensorMap tma_h,
-                    const __grid_constant__ FewArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  FewSmem& c = *reinterpret_cast<FewSmem*>(smem);
-  uint8_t* ring = smem + kControl;
-  uint8_t* scales = ring + a.nst * a.stage_bytes;          // two atoms a stage
-  float* sum = reinterpret_cast<float*>(scales + a.nst * 2 * 512);   // [T][128]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  few_setup(c, a.nst, &tma_w, &tma_h);
-  grid_launch();
-  tc_fence_before();
-  // The router's choice is complete: the kernel before this one let it start after its own wait for the router.
-  make_plan(a, c.plan, false);
-  tc_fence_after();
-  const uint32_t tmem = c.tmem;
-  const int KI = a.I >> 7, RT = a.d >> 7, ns = c.plan.slots;
-  const int row_steps = ns * KI;                           // steps of 128 output rows
-  const int total = RT * row_steps;
-  const int W = workers_of(total, static_cast<int>(gridDim.x), kMinSteps), w = static_cast<int>(blockIdx.x);
-  const int f0 = w < W ? range_begin(total, w, W) : total, f1 = w < W ? range_begin(total, w + 1, W) : total;
-  bool ok = true;
-  if (warp == 0) {
-    // Where a step is: expert slot s, rows r, piece k of K.
-    struct Step {
-      int r, s, k, boxes;
-    };
-    auto boxes_of = [&](int s) { return (c.plan.first[s + 1] - c.plan.first[s] + 15) >> 4; };
-    auto start = [&](int f) {
-      const int u = f / KI;
-      Step p;
-      p.k = f - u * KI;
-      p.r = u / ns;
-      p.s = u - p.r * ns;
-      p.boxes = boxes_of(p.s);
-      return p;
-    };
-    auto next = [&](Step& p) {
-      if (++p.k < KI) return;
-      p.k = 0;
-      if (++p.s == ns) {
-        p.s = 0;
-        ++p.r;
-      }
-      p.boxes = boxes_of(p.s);
-    };
-    auto load_w = [&](const Step& p, int i) {
-      uint8_t* dst = ring + i * a.stage_bytes;
-      uint64_t* bar = &c.full[i];
-      const int row = c.plan.expert[p.s] * a.d + p.r * 128;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(bar, kTileBytes + p.boxes * 2048 + 2 * 512);
-        tma_load_2d(dst, &tma_w, p.k * 128, row, bar);
-        bulk_load(scales + i * 1024, a.wsf + (static_cast<int64_t>(row >> 7) * KI + p.k) * 512, 512, bar);
-      }
-      __syncwarp();
-    };
-    auto load_h = [&](const Step& p, int i) {
-      uint8_t* dst = ring + i * a.stage_bytes + kTileBytes;
-      uint64_t* bar = &c.full[i];
-      const int row = c.plan.first[p.s];
-      if (elect_one()) {
+        tc_fence_before();
+        mbar_arrive(&c.acce[acc.i]);
+        acc.step(2);
+        if (!whole) {
+          // The CTA that stores a block's last part adds all of them.
+          __threadfence();
+          named_barrier(1, 128);
+          if (tid == 64) c.last = atomicAdd(parts + p.s * w.NB + p.b, 1) == w.PU - 1;
+          named_barrier(1, 128);
+          if (c.last == 0) continue;
+          __threadfence();
 #pragma unroll 1
-        for (int j = 0; j < p.boxes; ++j) tma_load_2d(dst + j * 2048, &tma_h, p.k * 128, row + j * 16, bar);
-        bulk_load(scales + i * 1024 + 512, a.hsf + (static_cast<int64_t>(p.s) * KI + p.k) * 512, 512, bar);
-      }
-      __syncwarp();
-    };
-    const int n = f1 - f0;
-    if (n > 0) {
-      const int ahead = n < a.nst ? n : a.nst;
-      Step p = start(f0), h = p;
-      for (int i = 0; i < ahead; ++i) {
-        load_w(p, i);
-        if (i + 1 < n) next(p);
-      }
-      grid_wait();
-      fence_proxy_async_global();
-      for (int i = 0; i < ahead; ++i) {
-        load_h(h, i);
-        if (i + 1 < n) next(h);
-      }
-      Stage st;
-      st.i = ahead == a.nst ? 0 : ahead;
-      st.phase = ahead == a.nst ? 1u : 0u;
-      int issued = ahead;
-#pragma unroll 1
-      for (int i = ahead; i < n; ++i) {
-        ok = warp_wait(&c.empty[st.i], st.phase ^ 1u, a.status, 211);
-        if (!ok) break;
-        load_w(p, st.i);
-        load_h(p, st.i);
-        if (i + 1 < n) next(p);
-        st.step(a.nst);
-        ++issued;
-      }
-      ok = land(c, st, issued, a.nst, a.status, 212) && ok;
-    }
-  } else if (warp == 1) {
-    Stage st, acc;
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sf0 = smem_u32(scales);
-    for (Walk wk(f0, f1, KI); wk.left > 0 && ok; wk.next()) {
-      const int s = wk.unit % ns;
-      const int rows = __shfl_sync(0xffffffffu, (c.plan.first[s + 1] - c.plan.first[s] + 15) & ~15, 0);
-      const uint32_t idesc = idesc_mxf8(128, 0) | (static_cast<uint32_t>(rows >> 3) << 17);
-      ok = warp_wait(&c.acce[acc.i], acc.phase ^ 1u, a.status, 213);
-      const int n = __shfl_sync(0xffffffffu, wk.steps(), 0);
-      const uint32_t d = tm + acc.i * 64;
-#pragma unroll 1
-      for (int k = 0; k < n && ok; ++k) {
-        ok = warp_wait(&c.full[st.i], st.phase, a.status, 214);
-        tc_fence_after();
-        if (ok && elect_one()) {
-          const uint32_t base = smem_u32(ring + st.i * a.stage_bytes), sf = tm + kSfCol + st.i * 8;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) tc_cp_sf(sf + 4 * j, desc_sf_chunk(sf0 + st.i * 1024 + 512 * j));
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_mxf8(d, desc_kmajor_sw128(base + kk * 32), desc_kmajor_sw128(base + kTileBytes + kk * 32),
-                        idesc_mxf8_sf(idesc, kk, kk), sf, sf + 4, (k | kk) != 0);
-          tc_commit(&c.empty[st.i]);
-          if (k == n - 1) tc_commit(&c.accf[acc.i]);
-        }
-        __syncwarp();
-        st.step(a.nst);
-      }
-      acc.step(4);
-    }
-  } else {
-    const int q = warp & 3, row = q * 32 + lane;
-    Stage acc;
-    // A token without a valid choice has NaN scores, and so has its sum.
-    auto fresh = [&](int t) { return (c.plan.bad[t >> 5] >> (t & 31)) & 1u ? __int_as_float(0x7fffffff) : 0.0f; };
-    auto put = [&](int r, int t, float v) { a.y[static_cast<int64_t>(t) * a.d + r * 128 + row] = __float2bfloat16(v); };
-    int r = -1;                                            // rows whose sum is under way
-    for (Walk wk(f0, f1, KI); wk.left > 0 && ok; wk.next()) {
-      const int ur = wk.unit / ns, s = wk.unit - ur * ns;
-      if (ur != r) {
-        r = ur;
-        for (int t = 0; t < a.T; ++t) sum[t * 128 + row] = fresh(t);
-      }
-      const int row0 = c.plan.first[s], n = c.plan.first[s + 1] - row0;
-      ok = __all_sync(0xffffffffu, mbar_wait(&c.accf[acc.i], acc.phase, a.status, 215));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t tacc = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc.i * 64;
-#pragma unroll 1
-      for (int c0 = 0; c0 < n; c0 += 16) {
-        uint32_t o[16];
-        tmem_ld16(tacc + c0, o);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          reg_fence(o[i]);
-          if (c0 + i < n) {
-            float& v = sum[c.plan.token[row0 + c0 + i] * 128 + row];
-            v = fmaf(c.plan.gate[row0 + c0 + i], __uint_as_float(o[i]), v);
-          }
-        }
-      }
-      tc_fence_before();
-      mbar_arrive(&c.acce[acc.i]);
-      acc.step(4);
-      const int r0 = r * row_steps, at = f1 - wk.left + wk.steps();   // steps done so far
-      if (at < f1 && at < r0 + row_steps) continue;        // more of these rows to come
-      if (f0 <= r0 && at == r0 + row_steps) {
-        for (int t = 0; t < a.T; ++t) put(r, t, sum[t * 128 + row]);
-        continue;
-      }
-      const int last = owner_of(total, r0 + row_steps - 1, W);
-      const mla::Cut cut = cut_of(total, W, r0, last);
-      float* mine = a.part + static_cast<int64_t>(2 * w + (r0 <= f0 ? 0 : 1)) * a.T * 128 + row;
-      for (int t = 0; t < a.T; ++t) mine[t * 128] = sum[t * 128 + row];
-      if (!last_piece(c, a.cnt_down + r, cut.pieces)) continue;
+          for (int i = 0; i < n; i += 2) {
+            float g[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
+            const float* src = gu + i * gu_step;
+            const int64_t two = i + 1 < n ? gu_step : 0;
 #pragma unroll 4
-      for (int t = 0; t < a.T; ++t) {
-        float v = 0.0f;
-        for (int p = 0; p < cut.pieces; ++p)
-          v += __ldcg(a.part + static_cast<int64_t>(2 * (cut.worker + p) + (p == 0 ? cut.slot : 0)) * a.T * 128 + t * 128 + row);
-        put(r, t, v);
+            for (int k = 0; k < w.PU; ++k) {
+              g[0] += __ldcg(src + k * 256);
+              u[0] += __ldcg(src + k * 256 + 128);
+              g[1] += __ldcg(src + two + k * 256);
+              u[1] += __ldcg(src + two + k * 256 + 128);
+            }
+            emit(p.s, i, p.b, g[0], u[0]);
+            if (i + 1 < n) emit(p.s, i + 1, p.b, g[1], u[1]);
+          }
+        }
+        // h is read by copies of other CTAs.
+        fence_proxy_async_global();
+        __threadfence();
+        named_barrier(1, 128);
+        if (tid == 64) red_release_add(ready + p.s, 1);
+      } else {
+        const int tiles = 2 * p.b + 1 < w.KA ? 2 : 1;
+        float* o = a.o + (static_cast<int64_t>(row0) * w.PD + p.part) * a.d + p.b * 256 + row;
+        const int64_t o_step = static_cast<int64_t>(w.PD) * a.d;
+#pragma unroll 1
+        for (int c0 = 0; c0 < n; c0 += 16) {
+          uint32_t v[2][16];
+          tmem_ld16(tacc + c0, v[0]);
+          tmem_ld16(tacc + 64 + c0, v[1]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              reg_fence(v[j][i]);
+              if (j < tiles && c0 + i < n) o[(c0 + i) * o_step + j * 128] = __uint_as_float(v[j][i]);
+            }
+        }
+        tc_fence_before();
+        mbar_arrive(&c.acce[acc.i]);
+        acc.step(2);
+        __threadfence();
+        named_barrier(1, 128);
+        if (tid == 64) red_release_add(done, 1);
       }
     }
-    // No expert at all: every token's scores are NaN.
-    if (total == 0) {
-      grid_wait();
-      for (int u = w; u < RT; u += static_cast<int>(gridDim.x))
-        for (int t = 0; t < a.T; ++t) put(u, t, fresh(t));
+    // ---- y, when all rows of o are there: every CTA takes a share, four columns of a token a thread
+    if (ok) {
+      if (tid == 64) c.last = wait_counter(done, w.total - w.nup, a.status, 210);
+      named_barrier(1, 128);
+      ok = c.last != 0;
+    }
+    if (ok) {
+      __threadfence();
+      const int vec = a.d >> 2, items = a.T * vec;
+      const int shared0 = a.S > 0 ? c.plan.first[c.plan.slot[a.E]] : 0;
+      for (int i = static_cast<int>(blockIdx.x) * 128 + tid - 64; i < items; i += ctas * 128) {
+        const int t = i / vec, col = (i - t * vec) * 4;
+        // A token without a valid choice has NaN scores, and so has its sum.
+        const bool bad = (c.plan.bad[t >> 5] >> (t & 31)) & 1u;
+        const float zero = bad ? __int_as_float(0x7fffffff) : 0.0f;
+        float4 y = make_float4(zero, zero, zero, zero);
+#pragma unroll
+        for (int j = 0; j < 9; ++j) {
+          const bool shared = j == a.k;
+          if (j > a.k || (shared && a.S == 0) || (bad && !shared)) continue;
+          const int r = shared ? shared0 + t : c.plan.row[t * a.k + j];
+          const float gate = shared ? 1.0f : c.plan.gate[t * a.k + j];
+          const float4* o = reinterpret_cast<const float4*>(a.o + static_cast<int64_t>(r) * w.PD * a.d + col);
+          float4 v = __ldcg(o);
+#pragma unroll 4
+          for (int k = 1; k < w.PD; ++k) {
+            const float4 x = __ldcg(o + static_cast<int64_t>(k) * vec);
+            v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+          }
+          y = make_float4(fmaf(gate, v.x, y.x), fmaf(gate, v.y, y.y), fmaf(gate, v.z, y.z), fmaf(gate, v.w, y.w));
+        }
+        *reinterpret_cast<uint2*>(a.y + static_cast<int64_t>(t) * a.d + col) =
+            make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+      }
     }
   }
-  few_finish(tmem, ok);
+  tc_fence_before();
+  if (__syncthreads_or(!ok)) drain_pause();
+  if (warp == 1) {
+    tc_fence_after();
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 struct FewLayout {
-  size_t status, cnt_route, cnt_up, cnt_down, logits, xq, xsf, hq, hsf, part, total;
+  size_t status, cnt_route, cnt, logits, xq, xsf, hq, hsf, gu, o, total;
   int64_t ncnt;
 };
 
-int64_t slots_of(const moe_config_t* c) {
+// Most and fewest experts in use.
+int64_t most_slots(const moe_config_t* c) {
   const int64_t chosen = static_cast<int64_t>(c->T) * c->k;
   return (chosen < c->E ? chosen : c->E) + c->n_shared;
 }
@@ -754,18 +736,27 @@ FewLayout few_layout(const moe_config_t* c) {
     cur += (n + 1023) / 1024 * 1024;
     return at;
   };
-  const size_t T = c->T, slots = slots_of(c);
-  L.ncnt = static_cast<int64_t>(slots) * (c->I / 128) + c->d / 128;
+  const size_t T = c->T, slots = most_slots(c), rows = T * (c->k + c->n_shared), d = c->d, I = c->I;
+  L.ncnt = static_cast<int64_t>(2 + slots + slots * (I / 128));
   L.status = add(16 + sizeof(int) * kMaxT);
   L.cnt_route = L.status + 16;
-  L.cnt_up = add(sizeof(int) * L.ncnt);
-  L.cnt_down = L.cnt_up + sizeof(int) * slots * (c->I / 128);
+  L.cnt = add(sizeof(int) * L.ncnt);
   L.logits = add(sizeof(float) * T * c->E);
-  L.xq = add(static_cast<size_t>(kMaxT) * c->d);
-  L.xsf = add(static_cast<size_t>(c->d / 128) * 512);
-  L.hq = add((T * (c->k + c->n_shared) + 16) * c->I);
-  L.hsf = add(slots * (c->I / 128) * 512);
-  L.part = add(2 * sizeof(float) * kMaxSms * T * 256);
+  L.xq = add(kMaxT * d);
+  L.xsf = add(d / 128 * 512);
+  L.hq = add((rows + 16) * I);
+  L.hsf = add(slots * (I / 128) * 512);
+  // Rows times parts are bounded whatever the choice: with s experts in use rows are at most T min(s, k + n_shared), and
+  // parts at most ctas want / (s blocks) + 1.
+  const size_t I128 = I / 128, d128 = d / 128;
+  auto bound = [&](size_t steps, size_t blocks, size_t want) {
+    const size_t most = steps / kMinSteps > 1 ? steps / kMinSteps : 1;
+    const size_t all = T * (ceil_div(kMaxSms * want, blocks) + c->k + c->n_shared);
+    return all < rows * most ? all : rows * most;
+  };
+  const size_t gu = bound(d128, I128, kUpPieces), o = bound(I128, (d128 + 1) / 2, kDownPieces);
+  L.gu = add(gu * I128 * 256 * sizeof(float));
+  L.o = add(o * d * sizeof(float));
   L.total = cur;
   return L;
 }
@@ -775,7 +766,7 @@ int validate_few(const moe_config_t* c) {
   if (c->T > kMaxT || (c->flags & MOE_FLAG_X_QUANTIZED)) return MOE_ERR_INVALID_ARG;
   // rows of the weights and steps of an expert kernel are counted in 32 bits
   const int64_t lim = (1LL << 31) - 1, Ep = c->E + c->n_shared;
-  if (Ep * 2 * c->I > lim || Ep * c->d > lim || Ep * (c->I / 128) * (c->d / 128) > lim) return MOE_ERR_INVALID_ARG;
+  if (Ep * 2 * c->I > lim || Ep * c->d > lim || 4 * Ep * (c->I / 128) * (c->d / 128) > lim) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
@@ -807,10 +798,7 @@ extern "C" int moe_few_forward(const moe_config_t* cfg, const void* x, const voi
   if (none) return MOE_OK;
   if (!get_encode()) return MOE_ERR_CUDA;
   static DevOnce once;
-  if (!once.ready([] {
-        const cudaError_t e = cudaFuncSetAttribute(few_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-        return e != cudaSuccess ? e : cudaFuncSetAttribute(few_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-      }))
+  if (!once.ready([] { return cudaFuncSetAttribute(few_experts_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax); }))
     return MOE_ERR_CUDA;
   const FewLayout L = few_layout(cfg);
   const WLayout WL = make_wlayout(cfg);
@@ -837,18 +825,20 @@ extern "C" int moe_few_forward(const moe_config_t* cfg, const void* x, const voi
   a.xsf = reinterpret_cast<uint8_t*>(base + L.xsf);
   a.hq = reinterpret_cast<uint8_t*>(base + L.hq);
   a.hsf = reinterpret_cast<uint8_t*>(base + L.hsf);
-  a.part = reinterpret_cast<float*>(base + L.part);
+  a.gu = reinterpret_cast<float*>(base + L.gu);
+  a.o = reinterpret_cast<float*>(base + L.o);
   a.cnt_route = reinterpret_cast<int*>(base + L.cnt_route);
-  a.cnt_up = reinterpret_cast<int*>(base + L.cnt_up);
-  a.cnt_down = reinterpret_cast<int*>(base + L.cnt_down);
+  a.cnt = reinterpret_cast<int*>(base + L.cnt);
   a.ncnt = static_cast<int>(L.ncnt);
   a.y = static_cast<__nv_bfloat16*>(y);
   a.status = reinterpret_cast<int*>(base + L.status);
   const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
+  a.w1sf = wq_ptr<uint8_t>(WL, w, MOE_WQ_W1F_SF);
+  a.w2sf = wq_ptr<uint8_t>(WL, w, MOE_WQ_W2F_SF);
   CUtensorMap tw1, tw2, tx, th;
-  if (!make_tmap(&tw1, wq_ptr<uint8_t>(WL, w, MOE_WQ_W1F), static_cast<int64_t>(a.Ep) * 2 * a.I, a.d, 256, false) ||
+  if (!make_tmap(&tw1, wq_ptr<uint8_t>(WL, w, MOE_WQ_W1F), static_cast<int64_t>(a.Ep) * 2 * a.I, a.d, 128, false) ||
       !make_tmap(&tw2, wq_ptr<uint8_t>(WL, w, MOE_WQ_W2F), static_cast<int64_t>(a.Ep) * a.d, a.I, 128, false) ||
-      !make_tmap(&tx, a.xq, kMaxT, a.d, a.N, false) ||
+      !make_tmap(&tx, a.xq, kMaxT, a.d, 16, false) ||
       !make_tmap(&th, a.hq, static_cast<int64_t>(a.T) * (a.k + a.S) + 16, a.I, 16, false))
     return MOE_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -857,25 +847,17 @@ extern "C" int moe_few_forward(const moe_config_t* cfg, const void* x, const voi
     const int blocks = static_cast<int>(ceil_div(a.E, 2 * er) * ceil_div(a.T, tg)) + quant;
     launch_kernel_after("few_route", kern, dim3(static_cast<unsigned>(blocks)), dim3(kRouteThreads), 8 * a.E * sizeof(float), s, a);
   };
+  const int per = static_cast<int>(ceil_div(a.E, 32));     // experts a lane of the choosing warp
   if (a.T == 1)
-    route(few_route_kernel<1, 1>, 1, 1);
+    per <= 2 ? route(few_route_kernel<1, 1, 2>, 1, 1) : per <= 8 ? route(few_route_kernel<1, 1, 8>, 1, 1) : route(few_route_kernel<1, 1, 16>, 1, 1);
   else
-    route(few_route_kernel<8, 2>, 8, 2);
+    per <= 2 ? route(few_route_kernel<8, 2, 2>, 8, 2) : per <= 8 ? route(few_route_kernel<8, 2, 8>, 8, 2) : route(few_route_kernel<8, 2, 16>, 8, 2);
   if (int r = call.status()) return r;
-  const int room = kSmemMax - 1024 - kControl;
-  auto ring = [&](int tiles, int atoms, int more) {
-    a.stage_bytes = tiles * kTileBytes + a.N * 128;
-    a.nst = (room - more) / (a.stage_bytes + atoms * 512);
-    if (a.nst > kMaxStages) a.nst = kMaxStages;
-    return 1024 + kControl + a.nst * (a.stage_bytes + atoms * 512) + more;
-  };
-  int smem = ring(2, 3, 0);
-  a.wsf = wq_ptr<uint8_t>(WL, w, MOE_WQ_W1F_SF);
-  launch_kernel_after("few_up", few_up_kernel, dim3(static_cast<unsigned>(sms)), dim3(kThreads), smem, s, tw1, tx, a);
-  if (int r = call.status()) return r;
-  smem = ring(1, 2, a.T * 128 * static_cast<int>(sizeof(float)));
-  a.wsf = wq_ptr<uint8_t>(WL, w, MOE_WQ_W2F_SF);
-  launch_kernel_after("few_down", few_down_kernel, dim3(static_cast<unsigned>(sms)), dim3(kThreads), smem, s, tw2, th, a);
+  a.stage_bytes = 2 * kTileBytes + a.N * 128;
+  a.nst = (kSmemMax - 1024 - kControl) / (a.stage_bytes + 3 * 512);
+  if (a.nst > kMaxStages) a.nst = kMaxStages;
+  launch_kernel_after("few_experts", few_experts_kernel, dim3(static_cast<unsigned>(sms)), dim3(kThreads),
+                      1024 + kControl + a.nst * (a.stage_bytes + 3 * 512), s, tw1, tw2, tx, th, a);
   return call.status();
 }
 

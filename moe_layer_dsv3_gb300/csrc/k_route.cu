@@ -23,7 +23,7 @@ __global__ void router_topk_kernel(const float* __restrict__ logits, const float
   if (t >= T) return;
   int my_e;
   float my_s, tot;
-  choose_experts<kMaxPerLane>([&](int e) { return logits[static_cast<int64_t>(t) * E + e]; }, [&](int e) { return bias[e]; }, E, k,
+  choose_experts<kMaxPerLane, BestByShuffles>([&](int e) { return logits[static_cast<int64_t>(t) * E + e]; }, [&](int e) { return bias[e]; }, E, k,
                               G, gtop, sv, lane, my_e, my_s, tot);
   if (lane < k) {
     const int64_t o = static_cast<int64_t>(t) * k + lane;

@@ -54,12 +54,26 @@ __device__ __forceinline__ void warp_best(float& v, int& e) {
   }
 }
 
+// The best pair of a warp, in every lane's e, by shuffles or by warp-wide integer reductions: the same choice among numbers. The
+// reductions take a third of the latency, which is what a kernel with few tokens waits for.
+struct BestByShuffles {
+  static __device__ __forceinline__ void of(float& v, int& e) { warp_best(v, e); }
+};
+struct BestByRedux {
+  static __device__ __forceinline__ void of(float& v, int& e) {
+    const uint32_t bits = __float_as_uint(v + 0.0f);       // (-0 counts as 0)
+    const uint32_t key = v != v ? 0u : bits ^ (bits >> 31 ? 0xffffffffu : 0x80000000u);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+    e = static_cast<int>(__reduce_min_sync(0xffffffffu, key == top ? static_cast<uint32_t>(e) : 0x7fffffffu));
+  }
+};
+
 // One warp chooses for one token. Lane l owns experts e = l + 32 i, i < kMaxPerLane
 // (a compile-time bound on ceil(E / 32), so the per-lane loops have no dead
 // iterations at the common expert counts). logit(e) and bias(e) read the token's
 // values; sv is scratch of E floats in shared memory. Lane j < k gets slot j: its
 // expert, its score s, and the sum of all slots' scores.
-template <int kMaxPerLane, typename Logit, typename Bias>
+template <int kMaxPerLane, typename Best, typename Logit, typename Bias>
 __device__ __forceinline__ void choose_experts(Logit logit, Bias bias, int E, int k, int G, int gtop, float* sv, int lane,
                                                int& my_e, float& my_s, float& tot) {
   float s[kMaxPerLane], v[kMaxPerLane];
@@ -93,7 +107,7 @@ __device__ __forceinline__ void choose_experts(Logit logit, Bias bias, int E, in
     for (int r = 0; r < gtop; ++r) {
       float bv = (lane < G && !((kept >> lane) & 1u)) ? gs : -INFINITY;
       int be = lane < G && !((kept >> lane) & 1u) ? lane : 0x7fffffff;
-      warp_best(bv, be);
+      Best::of(bv, be);
       kept |= 1u << be;
     }
   }
@@ -121,7 +135,7 @@ __device__ __forceinline__ void choose_experts(Logit logit, Bias bias, int E, in
         if (better(v[i], e, bv, be)) { bv = v[i]; be = e; }
       }
     }
-    warp_best(bv, be);
+    Best::of(bv, be);
     if ((be & 31) == lane) taken |= 1u << (be >> 5);
     float sw = 0.0f;
 #pragma unroll
