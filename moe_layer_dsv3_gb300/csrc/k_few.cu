@@ -129,22 +129,21 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
 }
 
 // ---------------------------------------------------------------- route
-// Logits: four warps share an expert's row, ER rows at once for TG tokens, in fp32
-// on the CUDA cores (a row of Wr is read once per token group; the tensor cores
-// would wait for one CTA's chain of 7168 / 64 stages). The CTA that finishes a group of tokens last
+// Logits: the eight warps of a CTA share the columns of ER rows of Wr, for TG tokens, in
+// fp32 on the CUDA cores: two rounds of loads at 7168 columns, where the tensor cores would wait for
+// one CTA's chain of 112 stages. The CTA that finishes a group of tokens last
 // chooses for them. Further CTAs quantise x and clear the counters of the kernels that follow.
 constexpr int kRouteThreads = 256;
-constexpr int kRowWarps = 4;
+constexpr int kRowWarps = kRouteThreads / 32;
 
 template <int TG, int ER, int PER>
 __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_constant__ FewArgs a) {
-  constexpr int kSets = 8 / kRowWarps;
-  constexpr int kDeep = TG == 1 ? 4 : 1;                   // chunks whose loads are under way together
-  __shared__ float red[kSets][kRowWarps][ER * TG];
+  constexpr int kDeep = TG == 1 ? 4 : 2;                   // chunks of 256 columns whose loads are under way together
+  __shared__ float red[kRowWarps][ER * TG];
   __shared__ int last;
   extern __shared__ float sv_all[];                        // [8][E]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int NE = (a.E + kSets * ER - 1) / (kSets * ER), NG = (a.T + TG - 1) / TG;
+  const int NE = (a.E + ER - 1) / ER, NG = (a.T + TG - 1) / TG;
   grid_wait();
   grid_launch();
   const int bid = static_cast<int>(blockIdx.x);
@@ -161,15 +160,14 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_c
     for (int i = (bid - NE * NG) * kRouteThreads + tid; i < a.ncnt; i += step) a.cnt[i] = 0;
     return;
   }
-  const int g = bid / NE, set = warp / kRowWarps, part = warp % kRowWarps;
-  const int e0 = ((bid - g * NE) * kSets + set) * ER;
+  const int g = bid / NE, e0 = (bid - g * NE) * ER;
   float acc[ER][TG];
 #pragma unroll
   for (int r = 0; r < ER; ++r)
 #pragma unroll
     for (int t = 0; t < TG; ++t) acc[r][t] = 0.0f;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int c0 = part * 256; c0 < a.d; c0 += kDeep * kRowWarps * 256) {
+  for (int c0 = warp * 256; c0 < a.d; c0 += kDeep * kRowWarps * 256) {
     uint4 uw[kDeep][ER], ux[kDeep][TG];
 #pragma unroll
     for (int u = 0; u < kDeep; ++u) {
@@ -203,15 +201,14 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_c
     for (int t = 0; t < TG; ++t) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) acc[r][t] += __shfl_xor_sync(0xffffffffu, acc[r][t], o);
-      if (lane == 0) red[set][part][r * TG + t] = acc[r][t];
+      if (lane == 0) red[warp][r * TG + t] = acc[r][t];
     }
   __syncthreads();
-  if (tid < kSets * ER * TG) {
-    const int s = tid / (ER * TG), i = tid - s * (ER * TG);
-    const int e = ((bid - g * NE) * kSets + s) * ER + i / TG, t = g * TG + i % TG;
-    float v = red[s][0][i];
+  if (tid < ER * TG) {
+    const int e = e0 + tid / TG, t = g * TG + tid % TG;
+    float v = red[0][tid];
 #pragma unroll
-    for (int p = 1; p < kRowWarps; ++p) v += red[s][p][i];
+    for (int p = 1; p < kRowWarps; ++p) v += red[p][tid];
     if (e < a.E && t < a.T) a.logits[static_cast<int64_t>(t) * a.E + e] = v;
     __threadfence();
   }
@@ -681,6 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       __threadfence();
       const int vec = a.d >> 2, items = a.T * vec;
+      const int picks = a.k + a.S;
       const int shared0 = a.S > 0 ? c.plan.first[c.plan.slot[a.E]] : 0;
       for (int i = static_cast<int>(blockIdx.x) * 128 + tid - 64; i < items; i += ctas * 128) {
         const int t = i / vec, col = (i - t * vec) * 4;
@@ -688,21 +686,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool bad = (c.plan.bad[t >> 5] >> (t & 31)) & 1u;
         const float zero = bad ? __int_as_float(0x7fffffff) : 0.0f;
         float4 y = make_float4(zero, zero, zero, zero);
+        float4 v[9];                                       // all rows' loads under way together
 #pragma unroll
-        for (int j = 0; j < 9; ++j) {
-          const bool shared = j == a.k;
-          if (j > a.k || (shared && a.S == 0) || (bad && !shared)) continue;
-          const int r = shared ? shared0 + t : c.plan.row[t * a.k + j];
-          const float gate = shared ? 1.0f : c.plan.gate[t * a.k + j];
-          const float4* o = reinterpret_cast<const float4*>(a.o + static_cast<int64_t>(r) * w.PD * a.d + col);
-          float4 v = __ldcg(o);
-#pragma unroll 4
-          for (int k = 1; k < w.PD; ++k) {
-            const float4 x = __ldcg(o + static_cast<int64_t>(k) * vec);
-            v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+        for (int j = 0; j < 9; ++j) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+        for (int k = 0; k < w.PD; ++k) {
+          float4 x[9];
+#pragma unroll
+          for (int j = 0; j < 9; ++j) {
+            x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (j < picks && !(bad && j < a.k)) {
+              const int r = j < a.k ? c.plan.row[t * a.k + j] : shared0 + t;
+              x[j] = __ldcg(reinterpret_cast<const float4*>(a.o + (static_cast<int64_t>(r) * w.PD + k) * a.d + col));
+            }
           }
-          y = make_float4(fmaf(gate, v.x, y.x), fmaf(gate, v.y, y.y), fmaf(gate, v.z, y.z), fmaf(gate, v.w, y.w));
+#pragma unroll
+          for (int j = 0; j < 9; ++j) v[j] = make_float4(v[j].x + x[j].x, v[j].y + x[j].y, v[j].z + x[j].z, v[j].w + x[j].w);
         }
+#pragma unroll
+        for (int j = 0; j < 9; ++j)
+          if (j < picks && !(bad && j < a.k)) {
+            const float gate = j < a.k ? c.plan.gate[t * a.k + j] : 1.0f;
+            y = make_float4(fmaf(gate, v[j].x, y.x), fmaf(gate, v[j].y, y.y), fmaf(gate, v[j].z, y.z), fmaf(gate, v[j].w, y.w));
+          }
         *reinterpret_cast<uint2*>(a.y + static_cast<int64_t>(t) * a.d + col) =
             make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
       }
@@ -844,7 +850,7 @@ extern "C" int moe_few_forward(const moe_config_t* cfg, const void* x, const voi
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int quant = static_cast<int>(ceil_div(static_cast<int64_t>(a.T) * (a.d / 32), kRouteThreads));
   auto route = [&](auto kern, int tg, int er) {
-    const int blocks = static_cast<int>(ceil_div(a.E, 2 * er) * ceil_div(a.T, tg)) + quant;
+    const int blocks = static_cast<int>(ceil_div(a.E, er) * ceil_div(a.T, tg)) + quant;
     launch_kernel_after("few_route", kern, dim3(static_cast<unsigned>(blocks)), dim3(kRouteThreads), 8 * a.E * sizeof(float), s, a);
   };
   const int per = static_cast<int>(ceil_div(a.E, 32));     // experts a lane of the choosing warp

@@ -57,9 +57,11 @@ __device__ __forceinline__ void warp_best(float& v, int& e) {
 // The best pair of a warp, in every lane's e, by shuffles or by warp-wide integer reductions: the same choice among numbers. The
 // reductions take a third of the latency, which is what a kernel with few tokens waits for.
 struct BestByShuffles {
+  static constexpr int kRounds = 8;        // selection rounds unrolled
   static __device__ __forceinline__ void of(float& v, int& e) { warp_best(v, e); }
 };
 struct BestByRedux {
+  static constexpr int kRounds = 1;        // (one launch for a few tokens fetches the code once: a round's code again costs more than a loop)
   static __device__ __forceinline__ void of(float& v, int& e) {
     const uint32_t bits = __float_as_uint(v + 0.0f);       // (-0 counts as 0)
     const uint32_t key = v != v ? 0u : bits ^ (bits >> 31 ? 0xffffffffu : 0x80000000u);
@@ -121,11 +123,11 @@ __device__ __forceinline__ void choose_experts(Logit logit, Bias bias, int E, in
     if (i < per_lane && e < E && ((kept >> (e / per)) & 1u)) cand |= 1u << i;
   }
   uint32_t taken = 0;
-  int sel_e[8];          // k <= 8 (checked by the API); unrolled, so both stay in registers
-  float sel_s[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (j >= k) break;   // k is the same in every lane
+  tot = my_s = 0.0f;
+  my_e = 0;
+#pragma unroll(Best::kRounds)
+  for (int j = 0; j < 8; ++j) {            // k <= 8 (checked by the API)
+    if (j >= k) break;                     // k is the same in every lane
     float bv = -INFINITY;
     int be = 0x7fffffff;
 #pragma unroll
@@ -141,19 +143,14 @@ __device__ __forceinline__ void choose_experts(Logit logit, Bias bias, int E, in
 #pragma unroll
     for (int i = 0; i < kMaxPerLane; ++i)
       if (i == (be >> 5)) sw = s[i];
-    sel_s[j] = __shfl_sync(0xffffffffu, sw, be & 31);
-    sel_e[j] = be;
+    const float sj = __shfl_sync(0xffffffffu, sw, be & 31);
+    // every lane sums the selected scores in slot order; lane j holds slot j
+    tot = j == 0 ? sj : __fadd_rn(tot, sj);
+    if (lane == j) {
+      my_s = sj;
+      my_e = be;
+    }
   }
-  // Every lane sums the selected scores in slot order; lane j writes slot j.
-  tot = sel_s[0];
-#pragma unroll
-  for (int j = 1; j < 8; ++j)
-    if (j < k) tot = __fadd_rn(tot, sel_s[j]);
-  my_s = 0.0f;
-  my_e = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j == lane && j < k) { my_s = sel_s[j]; my_e = sel_e[j]; }
 }
 
 }  // namespace moe

@@ -8,8 +8,8 @@ and the product. So h is known within dh, and MX(h) may be any value that a bloc
 within dh quantises to: the largest distance of those from MX(h) times |Wd|, summed
 over I, bounds what that does to o. The sums over I and over the experts are fp32
 again, gates carry 2^-21 (a sum of at most 8 scores and a quotient), and y is rounded
-to bf16 once: 2^-8. A logit is summed by 128 threads, 8 products of every 1024 columns
-each, and joined by 5 + 3 additions: that many roundings of 2^-24, through a sigmoid of slope 1/4.
+to bf16 once: 2^-8. A logit is summed by 256 threads, 8 products of every 2048 columns
+each, and joined by 5 + 7 additions: that many roundings of 2^-24, through a sigmoid of slope 1/4.
 """
 import numpy as np
 import pytest
@@ -83,7 +83,7 @@ class Case:
     def choice(self):
         """The choice in 64 bits and, a token at a time, whether no comparison it rests on is closer than the scores' error."""
         logits = self.x.to(F) @ self.w_router.to(F).T
-        err = (-(-self.d // 1024) * 8 + 8) * 2.0 ** -24 * (self.x.to(F).abs() @ self.w_router.to(F).abs().T).amax(1) / 4 + 2.0 ** -21
+        err = (-(-self.d // 2048) * 8 + 12) * 2.0 ** -24 * (self.x.to(F).abs() @ self.w_router.to(F).abs().T).amax(1) / 4 + 2.0 ** -21
         s = torch.sigmoid(logits)
         v = s + self.bias.to(F)
         sure = torch.ones(self.T, dtype=torch.bool, device="cuda")
