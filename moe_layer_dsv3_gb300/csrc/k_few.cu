@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_c
   constexpr int kDeep = TG == 1 ? 4 : 2;                   // chunks of 256 columns whose loads are under way together
   __shared__ float red[kRowWarps][ER * TG];
   __shared__ int last;
-  extern __shared__ float sv_all[];                        // [8][E]
+  extern __shared__ float sv_all[];                        // [8][E] for the choosing warps, [E] bias
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int NE = (a.E + ER - 1) / ER, NG = (a.T + TG - 1) / TG;
   grid_wait();
@@ -161,6 +161,8 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_c
     return;
   }
   const int g = bid / NE, e0 = (bid - g * NE) * ER;
+  float* bias = sv_all + 8 * a.E;                          // read ahead: the choice then waits for the logits alone
+  for (int e = tid; e < a.E; e += kRouteThreads) bias[e] = __int_as_float(ld_global_s32(reinterpret_cast<const int*>(a.bias + e)));
   float acc[ER][TG];
 #pragma unroll
   for (int r = 0; r < ER; ++r)
@@ -225,8 +227,7 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_c
     int e;
     float s, tot;
     choose_experts<PER, BestByRedux>([&](int n) { return __ldcg(a.logits + static_cast<int64_t>(t) * a.E + n); },
-                       [&](int n) { return __int_as_float(ld_global_s32(reinterpret_cast<const int*>(a.bias + n))); }, a.E, a.k,
-                       a.G, a.gtop, sv_all + warp * a.E, lane, e, s, tot);
+                       [&](int n) { return bias[n]; }, a.E, a.k, a.G, a.gtop, sv_all + warp * a.E, lane, e, s, tot);
     if (lane < a.k) {
       a.idx[t * a.k + lane] = e;
       a.w[t * a.k + lane] = __fdiv_rn(s, tot);
@@ -354,10 +355,11 @@ __device__ __forceinline__ Piece piece_of(const Work& w, int id) {
     p.k0 = w.KA * p.part / w.PU;
     p.k1 = w.KA * (p.part + 1) / w.PU;
   } else {
-    const int q = id - w.nup, u = q / w.RP;
-    p.b = q - u * w.RP;
-    p.s = u / w.PD;
-    p.part = u - p.s * w.PD;
+    // (parts of the same rows side by side: with all CTAs on the same quarter of every 2 KB row HBM gave 4.3 TB/s)
+    const int q = id - w.nup, u = q / w.PD;
+    p.part = q - u * w.PD;
+    p.s = u / w.RP;
+    p.b = u - p.s * w.RP;
     p.k0 = w.KI * p.part / w.PD;
     p.k1 = w.KI * (p.part + 1) / w.PD;
   }
@@ -677,38 +679,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok) {
       __threadfence();
-      const int vec = a.d >> 2, items = a.T * vec;
-      const int picks = a.k + a.S;
+      const int picks = a.k + a.S, vecs = a.d >> 2, items = a.T * vecs;
       const int shared0 = a.S > 0 ? c.plan.first[c.plan.slot[a.E]] : 0;
-      for (int i = static_cast<int>(blockIdx.x) * 128 + tid - 64; i < items; i += ctas * 128) {
-        const int t = i / vec, col = (i - t * vec) * 4;
+      // warps of 32 neighbouring items, spread over the CTAs
+      for (int i = ((warp - 2) * ctas + static_cast<int>(blockIdx.x)) * 32 + lane; i < items; i += 4 * ctas * 32) {
+        const int t = i / vecs, col = (i - t * vecs) * 4;
         // A token without a valid choice has NaN scores, and so has its sum.
         const bool bad = (c.plan.bad[t >> 5] >> (t & 31)) & 1u;
-        const float zero = bad ? __int_as_float(0x7fffffff) : 0.0f;
-        float4 y = make_float4(zero, zero, zero, zero);
-        float4 v[9];                                       // all rows' loads under way together
+        // All rows' loads are under way together: those that the token lacks read row 0 and count as 0.
+        const float4* src[9];
+        float gate[9];
+        bool live[9];
+#pragma unroll
+        for (int j = 0; j < 9; ++j) {
+          live[j] = j < a.k ? !bad : j < picks;
+          const int r = !live[j] ? 0 : (j < a.k ? c.plan.row[t * a.k + j] : shared0 + t);
+          gate[j] = j < a.k && live[j] ? c.plan.gate[t * a.k + j] : 1.0f;
+          src[j] = reinterpret_cast<const float4*>(a.o + static_cast<int64_t>(r) * w.PD * a.d + col);
+        }
+        float4 v[9];
 #pragma unroll
         for (int j = 0; j < 9; ++j) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
         for (int k = 0; k < w.PD; ++k) {
           float4 x[9];
 #pragma unroll
-          for (int j = 0; j < 9; ++j) {
-            x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (j < picks && !(bad && j < a.k)) {
-              const int r = j < a.k ? c.plan.row[t * a.k + j] : shared0 + t;
-              x[j] = __ldcg(reinterpret_cast<const float4*>(a.o + (static_cast<int64_t>(r) * w.PD + k) * a.d + col));
-            }
-          }
+          for (int j = 0; j < 9; ++j) x[j] = ld_global_f4(src[j] + static_cast<int64_t>(k) * vecs);
 #pragma unroll
           for (int j = 0; j < 9; ++j) v[j] = make_float4(v[j].x + x[j].x, v[j].y + x[j].y, v[j].z + x[j].z, v[j].w + x[j].w);
         }
+        const float zero = bad ? __int_as_float(0x7fffffff) : 0.0f;
+        float4 y = make_float4(zero, zero, zero, zero);
 #pragma unroll
         for (int j = 0; j < 9; ++j)
-          if (j < picks && !(bad && j < a.k)) {
-            const float gate = j < a.k ? c.plan.gate[t * a.k + j] : 1.0f;
-            y = make_float4(fmaf(gate, v[j].x, y.x), fmaf(gate, v[j].y, y.y), fmaf(gate, v[j].z, y.z), fmaf(gate, v[j].w, y.w));
-          }
+          if (live[j]) y = make_float4(fmaf(gate[j], v[j].x, y.x), fmaf(gate[j], v[j].y, y.y), fmaf(gate[j], v[j].z, y.z), fmaf(gate[j], v[j].w, y.w));
         *reinterpret_cast<uint2*>(a.y + static_cast<int64_t>(t) * a.d + col) =
             make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
       }
@@ -851,13 +855,20 @@ extern "C" int moe_few_forward(const moe_config_t* cfg, const void* x, const voi
   const int quant = static_cast<int>(ceil_div(static_cast<int64_t>(a.T) * (a.d / 32), kRouteThreads));
   auto route = [&](auto kern, int tg, int er) {
     const int blocks = static_cast<int>(ceil_div(a.E, er) * ceil_div(a.T, tg)) + quant;
-    launch_kernel_after("few_route", kern, dim3(static_cast<unsigned>(blocks)), dim3(kRouteThreads), 8 * a.E * sizeof(float), s, a);
+    launch_kernel_after("few_route", kern, dim3(static_cast<unsigned>(blocks)), dim3(kRouteThreads), 9 * a.E * sizeof(float), s, a);
   };
   const int per = static_cast<int>(ceil_div(a.E, 32));     // experts a lane of the choosing warp
-  if (a.T == 1)
-    per <= 2 ? route(few_route_kernel<1, 1, 2>, 1, 1) : per <= 8 ? route(few_route_kernel<1, 1, 8>, 1, 1) : route(few_route_kernel<1, 1, 16>, 1, 1);
-  else
-    per <= 2 ? route(few_route_kernel<8, 2, 2>, 8, 2) : per <= 8 ? route(few_route_kernel<8, 2, 8>, 8, 2) : route(few_route_kernel<8, 2, 16>, 8, 2);
+  if (a.T == 1) {
+    if (per <= 2) route(few_route_kernel<1, 1, 2>, 1, 1);
+    else if (per <= 4) route(few_route_kernel<1, 1, 4>, 1, 1);
+    else if (per <= 8) route(few_route_kernel<1, 1, 8>, 1, 1);
+    else route(few_route_kernel<1, 1, 16>, 1, 1);
+  } else {
+    if (per <= 2) route(few_route_kernel<8, 2, 2>, 8, 2);
+    else if (per <= 4) route(few_route_kernel<8, 2, 4>, 8, 2);
+    else if (per <= 8) route(few_route_kernel<8, 2, 8>, 8, 2);
+    else route(few_route_kernel<8, 2, 16>, 8, 2);
+  }
   if (int r = call.status()) return r;
   a.stage_bytes = 2 * kTileBytes + a.N * 128;
   a.nst = (kSmemMax - 1024 - kControl) / (a.stage_bytes + 3 * 512);
