@@ -31,6 +31,8 @@
 // token, 403 for 16 and 544 for 64, where the list takes NEWFIG.
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "gemm.cuh"
 #include "prof.h"
 #include "route.cuh"
@@ -49,6 +51,7 @@ constexpr int kSmemMax = 232448;
 constexpr int kSfCol = 256;                // TMEM: accumulators below, scales of the ring's stages from here on
 constexpr int kQueue = 4;                  // pieces on their way from the warp that takes them to the others
 constexpr int kUpPieces = 4, kDownPieces = 8;   // pieces of a CTA that K is cut for, where there are fewer
+constexpr int kPrefetch = 16384;           // bytes of a prefetch
 constexpr int kMinSteps = 2;               // fewest 128-wide steps of a part
 static_assert(kMaxT == 64, "a token is a bit of an expert's 64-bit mask");
 
@@ -64,7 +67,9 @@ struct FewArgs {
   float* logits;                           // [T][E]
   uint8_t* xq;                             // [64][d]
   uint8_t* xsf;                            // [d / 128] atoms
-  const uint8_t* w1sf;                     // scales of the weights
+  const uint8_t* w1;                       // weights
+  const uint8_t* w2;
+  const uint8_t* w1sf;                     // and their scales
   const uint8_t* w2sf;
   uint8_t* hq;                             // [rows][I], an expert's tokens one after another
   uint8_t* hsf;                            // [experts in use][I / 128] atoms
@@ -237,7 +242,8 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_c
 
 // ---------------------------------------------------------------- the experts in use
 // Which tokens chose which expert, made by every CTA for itself from the router's choice: a 64-bit mask of tokens per
-// expert, the experts in use in ascending order, and their tokens' rows one after another.
+// expert, the experts in use in ascending order, and their tokens' rows one after another. A shared expert is number 0, and
+// expert e number e + n_shared: what is known to be used comes first.
 struct FewPlan {
   uint32_t mask[kMaxEp][2];
   uint16_t expert[kMaxEp];                 // of a slot
@@ -259,10 +265,10 @@ __device__ __forceinline__ void make_plan(const FewArgs& a, FewPlan& p, bool rep
   for (int i = tid; i < n; i += kThreads) {
     const int e = ld_global_s32(a.idx + i), t = i / a.k;
     const bool ok = e >= 0 && e < a.E;
-    atomicOr(ok ? &p.mask[e][t >> 5] : &p.bad[t >> 5], 1u << (t & 31));
+    atomicOr(ok ? &p.mask[e + a.S][t >> 5] : &p.bad[t >> 5], 1u << (t & 31));
     if (!ok && report) report_error(a.status, kErrBounds, 200);
   }
-  if (a.S > 0 && tid < 2) p.mask[a.E][tid] = tid * 32 >= a.T ? 0u : (a.T - tid * 32 >= 32 ? 0xffffffffu : (1u << (a.T - tid * 32)) - 1u);
+  if (a.S > 0 && tid < 2) p.mask[0][tid] = tid * 32 >= a.T ? 0u : (a.T - tid * 32 >= 32 ? 0xffffffffu : (1u << (a.T - tid * 32)) - 1u);
   __syncthreads();
   const int per = (a.Ep + kThreads - 1) / kThreads;
   uint32_t mine = 0;                       // experts in use << 16 | their tokens
@@ -304,9 +310,9 @@ __device__ __forceinline__ void make_plan(const FewArgs& a, FewPlan& p, bool rep
   for (int i = tid; i < n; i += kThreads) {
     const int e = ld_global_s32(a.idx + i), t = i / a.k;
     if (e < 0 || e >= a.E) continue;
-    const uint32_t below = t < 32 ? __popc(p.mask[e][0] & ((1u << t) - 1u))
-                                  : __popc(p.mask[e][0]) + __popc(p.mask[e][1] & ((1u << (t - 32)) - 1u));
-    p.row[i] = static_cast<uint16_t>(p.first[p.slot[e]] + below);
+    const uint32_t* m = p.mask[e + a.S];
+    const uint32_t below = t < 32 ? __popc(m[0] & ((1u << t) - 1u)) : __popc(m[0]) + __popc(m[1] & ((1u << (t - 32)) - 1u));
+    p.row[i] = static_cast<uint16_t>(p.first[p.slot[e + a.S]] + below);
     p.gate[i] = __int_as_float(ld_global_s32(reinterpret_cast<const int*>(a.w + i)));
   }
   __syncthreads();
@@ -402,6 +408,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&c.tmem, 512);
     tmem_relinquish();
   }
+  // The shared expert's weights are read whatever the router chooses: on their way into L2 while it works.
+  if (a.S > 0 && warp == 0) {
+    const int64_t n1 = static_cast<int64_t>(a.d) * a.I * 2, n2 = n1 / 2, at1 = a.E * n1, at2 = a.E * n2;
+    auto fetch = [&](const uint8_t* p, int64_t n) {
+      for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * kPrefetch; i < n; i += static_cast<int64_t>(gridDim.x) * 32 * kPrefetch)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p + i), "r"(static_cast<uint32_t>(n - i < kPrefetch ? n - i : kPrefetch))
+                     : "memory");
+    };
+    fetch(a.w1 + at1, n1);
+    fetch(a.w1sf + at1 / 32, n1 / 32);
+    fetch(a.w2 + at2, n2);
+    fetch(a.w2sf + at2 / 32, n2 / 32);
+  }
   grid_wait();
   grid_launch();
   tc_fence_before();
@@ -463,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       q.step(kQueue);
       if (!more) break;
       const Piece p = piece_of(w, id);
-      const int e = c.plan.expert[p.s], K = p.up ? w.KA : w.KI;
+      const int n = c.plan.expert[p.s], e = n < a.S ? a.E : n - a.S, K = p.up ? w.KA : w.KI;   // (e: its place in the weights)
       const int row = __shfl_sync(0xffffffffu, p.up ? e * 2 * a.I + p.b * 256 : e * a.d + p.b * 256, 0);
       const int tiles = p.up || 2 * p.b + 1 < w.KA ? 2 : 1;
       const CUtensorMap* map = p.up ? &tma_w1 : &tma_w2;
@@ -680,42 +699,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       __threadfence();
       const int picks = a.k + a.S, vecs = a.d >> 2, items = a.T * vecs;
-      const int shared0 = a.S > 0 ? c.plan.first[c.plan.slot[a.E]] : 0;
-      // warps of 32 neighbouring items, spread over the CTAs
-      for (int i = ((warp - 2) * ctas + static_cast<int>(blockIdx.x)) * 32 + lane; i < items; i += 4 * ctas * 32) {
-        const int t = i / vecs, col = (i - t * vecs) * 4;
-        // A token without a valid choice has NaN scores, and so has its sum.
-        const bool bad = (c.plan.bad[t >> 5] >> (t & 31)) & 1u;
-        // All rows' loads are under way together: those that the token lacks read row 0 and count as 0.
-        const float4* src[9];
-        float gate[9];
-        bool live[9];
+      // IT items (four columns of a token each) and PT parts of their rows at once: 18 loads under way. Loads that a token lacks
+      // read row 0 and count as 0.
+      auto sum = [&](auto it_, auto pt_, int i0, int step) {
+        constexpr int IT = decltype(it_)::value, PT = decltype(pt_)::value;
+        const float4* src[IT][9];
+        float gate[IT][9];
+        uint32_t live[IT];
+        float4 v[IT][9];
 #pragma unroll
-        for (int j = 0; j < 9; ++j) {
-          live[j] = j < a.k ? !bad : j < picks;
-          const int r = !live[j] ? 0 : (j < a.k ? c.plan.row[t * a.k + j] : shared0 + t);
-          gate[j] = j < a.k && live[j] ? c.plan.gate[t * a.k + j] : 1.0f;
-          src[j] = reinterpret_cast<const float4*>(a.o + static_cast<int64_t>(r) * w.PD * a.d + col);
+        for (int n = 0; n < IT; ++n) {
+          const int i = i0 + n * step < items ? i0 + n * step : i0;
+          const int t = i / vecs, col = (i - t * vecs) * 4;
+          const bool bad = (c.plan.bad[t >> 5] >> (t & 31)) & 1u;
+          live[n] = 0;
+#pragma unroll
+          for (int j = 0; j < 9; ++j) {
+            const bool has = j < a.k ? !bad : j < picks;
+            const int r = !has ? 0 : (j < a.k ? c.plan.row[t * a.k + j] : t);        // (the shared expert's rows are the first)
+            gate[n][j] = has && j < a.k ? c.plan.gate[t * a.k + j] : 1.0f;
+            if (has) live[n] |= 1u << j;
+            src[n][j] = reinterpret_cast<const float4*>(a.o + static_cast<int64_t>(r) * w.PD * a.d + col);
+            v[n][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          }
         }
-        float4 v[9];
-#pragma unroll
-        for (int j = 0; j < 9; ++j) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-        for (int k = 0; k < w.PD; ++k) {
-          float4 x[9];
+        for (int k = 0; k < w.PD; k += PT) {
+          float4 x[IT][PT][9];
 #pragma unroll
-          for (int j = 0; j < 9; ++j) x[j] = ld_global_f4(src[j] + static_cast<int64_t>(k) * vecs);
+          for (int n = 0; n < IT; ++n)
 #pragma unroll
-          for (int j = 0; j < 9; ++j) v[j] = make_float4(v[j].x + x[j].x, v[j].y + x[j].y, v[j].z + x[j].z, v[j].w + x[j].w);
+            for (int u = 0; u < PT; ++u)
+#pragma unroll
+              for (int j = 0; j < 9; ++j) x[n][u][j] = ld_global_f4(src[n][j] + static_cast<int64_t>(k + u < w.PD ? k + u : k) * vecs);
+          __syncwarp();                                    // all of them are issued before the first is added (items are whole warps)
+#pragma unroll
+          for (int n = 0; n < IT; ++n)
+#pragma unroll
+            for (int u = 0; u < PT; ++u)
+              if (k + u < w.PD) {
+#pragma unroll
+                for (int j = 0; j < 9; ++j) {
+                  const float4& y = x[n][u][j];
+                  v[n][j] = make_float4(v[n][j].x + y.x, v[n][j].y + y.y, v[n][j].z + y.z, v[n][j].w + y.w);
+                }
+              }
         }
-        const float zero = bad ? __int_as_float(0x7fffffff) : 0.0f;
-        float4 y = make_float4(zero, zero, zero, zero);
 #pragma unroll
-        for (int j = 0; j < 9; ++j)
-          if (live[j]) y = make_float4(fmaf(gate[j], v[j].x, y.x), fmaf(gate[j], v[j].y, y.y), fmaf(gate[j], v[j].z, y.z), fmaf(gate[j], v[j].w, y.w));
-        *reinterpret_cast<uint2*>(a.y + static_cast<int64_t>(t) * a.d + col) =
-            make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-      }
+        for (int n = 0; n < IT; ++n) {
+          const int i = i0 + n * step;
+          if (i >= items) break;
+          const int t = i / vecs, col = (i - t * vecs) * 4;
+          // A token without a valid choice has NaN scores, and so has its sum.
+          const float zero = (c.plan.bad[t >> 5] >> (t & 31)) & 1u ? __int_as_float(0x7fffffff) : 0.0f;
+          float4 y = make_float4(zero, zero, zero, zero);
+#pragma unroll
+          for (int j = 0; j < 9; ++j)
+            if ((live[n] >> j) & 1u)
+              y = make_float4(fmaf(gate[n][j], v[n][j].x, y.x), fmaf(gate[n][j], v[n][j].y, y.y), fmaf(gate[n][j], v[n][j].z, y.z),
+                              fmaf(gate[n][j], v[n][j].w, y.w));
+          *reinterpret_cast<uint2*>(a.y + static_cast<int64_t>(t) * a.d + col) =
+              make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+        }
+      };
+      // warps of 32 neighbouring items, spread over the CTAs
+      const int step = 4 * ctas * 32, i0 = ((warp - 2) * ctas + static_cast<int>(blockIdx.x)) * 32 + lane;
+      using One = std::integral_constant<int, 1>;
+      using Two = std::integral_constant<int, 2>;
+      if (w.PD == 1)
+        for (int i = i0; i < items; i += 2 * step) sum(Two{}, One{}, i, step);
+      else
+        for (int i = i0; i < items; i += step) sum(One{}, Two{}, i, step);
     }
   }
   tc_fence_before();
@@ -843,11 +897,13 @@ extern "C" int moe_few_forward(const moe_config_t* cfg, const void* x, const voi
   a.y = static_cast<__nv_bfloat16*>(y);
   a.status = reinterpret_cast<int*>(base + L.status);
   const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
+  a.w1 = wq_ptr<uint8_t>(WL, w, MOE_WQ_W1F);
+  a.w2 = wq_ptr<uint8_t>(WL, w, MOE_WQ_W2F);
   a.w1sf = wq_ptr<uint8_t>(WL, w, MOE_WQ_W1F_SF);
   a.w2sf = wq_ptr<uint8_t>(WL, w, MOE_WQ_W2F_SF);
   CUtensorMap tw1, tw2, tx, th;
-  if (!make_tmap(&tw1, wq_ptr<uint8_t>(WL, w, MOE_WQ_W1F), static_cast<int64_t>(a.Ep) * 2 * a.I, a.d, 128, false) ||
-      !make_tmap(&tw2, wq_ptr<uint8_t>(WL, w, MOE_WQ_W2F), static_cast<int64_t>(a.Ep) * a.d, a.I, 128, false) ||
+  if (!make_tmap(&tw1, a.w1, static_cast<int64_t>(a.Ep) * 2 * a.I, a.d, 128, false) ||
+      !make_tmap(&tw2, a.w2, static_cast<int64_t>(a.Ep) * a.d, a.I, 128, false) ||
       !make_tmap(&tx, a.xq, kMaxT, a.d, 16, false) ||
       !make_tmap(&th, a.hq, static_cast<int64_t>(a.T) * (a.k + a.S) + 16, a.I, 16, false))
     return MOE_ERR_CUDA;
