@@ -31,8 +31,6 @@
 // token, 403 for 16 and 544 for 64, where the list takes NEWFIG.
 #include <cudaTypedefs.h>
 
-#include <type_traits>
-
 #include "gemm.cuh"
 #include "prof.h"
 #include "route.cuh"
@@ -50,7 +48,7 @@ constexpr int kTileBytes = 128 * 128;      // a weight tile: 128 rows x 128 valu
 constexpr int kSmemMax = 232448;
 constexpr int kSfCol = 256;                // TMEM: accumulators below, scales of the ring's stages from here on
 constexpr int kQueue = 4;                  // pieces on their way from the warp that takes them to the others
-constexpr int kUpPieces = 4, kDownPieces = 8;   // pieces of a CTA that K is cut for, where there are fewer
+constexpr int kUpPieces = 1, kDownPieces = 2;   // pieces of a CTA that K is cut for, where there are fewer
 constexpr int kPrefetch = 16384;           // bytes of a prefetch
 constexpr int kMinSteps = 2;               // fewest 128-wide steps of a part
 static_assert(kMaxT == 64, "a token is a bit of an expert's 64-bit mask");
@@ -89,6 +87,12 @@ __host__ __device__ __forceinline__ int parts_of(int units, int steps, int ctas,
   return n < most ? n : most;
 }
 
+// First step of part i of n: an even one, since two steps of a row (256 bytes) come from HBM together.
+__device__ __forceinline__ int cut_at(int steps, int i, int n) {
+  const int at = ((steps + 1) >> 1) * i / n * 2;
+  return at < steps ? at : steps;
+}
+
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
@@ -125,12 +129,21 @@ __device__ __forceinline__ void drain_pause() {
   }
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+// One column of two accumulators, and four.
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
+// Counts an arrival after a CTA barrier: what the CTA's threads wrote before the barrier is released with it, and what earlier
+// arrivals released is acquired. (A fence by every thread before the barrier took 4 to 8 us while the rings are loading.)
+__device__ __forceinline__ int atom_add_acq_rel(int* p, int v) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
 }
 
 // ---------------------------------------------------------------- route
@@ -217,13 +230,11 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_c
 #pragma unroll
     for (int p = 1; p < kRowWarps; ++p) v += red[p][tid];
     if (e < a.E && t < a.T) a.logits[static_cast<int64_t>(t) * a.E + e] = v;
-    __threadfence();
   }
   __syncthreads();
-  if (tid == 0) last = atomicAdd(a.cnt_route + g, 1) == NE - 1;
+  if (tid == 0) last = atom_add_acq_rel(a.cnt_route + g, 1) == NE - 1;
   __syncthreads();
   if (!last) return;
-  __threadfence();
   if (tid == 0) a.cnt_route[g] = 0;
 #pragma unroll 1
   for (int i = warp; i < TG; i += 8) {
@@ -358,16 +369,16 @@ __device__ __forceinline__ Piece piece_of(const Work& w, int id) {
     p.part = id - u * w.PU;
     p.s = u / w.NB;
     p.b = u - p.s * w.NB;
-    p.k0 = w.KA * p.part / w.PU;
-    p.k1 = w.KA * (p.part + 1) / w.PU;
+    p.k0 = cut_at(w.KA, p.part, w.PU);
+    p.k1 = cut_at(w.KA, p.part + 1, w.PU);
   } else {
     // (parts of the same rows side by side: with all CTAs on the same quarter of every 2 KB row HBM gave 4.3 TB/s)
     const int q = id - w.nup, u = q / w.PD;
     p.part = q - u * w.PD;
     p.s = u / w.RP;
     p.b = u - p.s * w.RP;
-    p.k0 = w.KI * p.part / w.PD;
-    p.k1 = w.KI * (p.part + 1) / w.PD;
+    p.k0 = cut_at(w.KI, p.part, w.PD);
+    p.k1 = cut_at(w.KI, p.part + 1, w.PD);
   }
   return p;
 }
@@ -605,44 +616,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         // parts of row r: gu + r * gu_step, the next part 256 floats on
         const int64_t gu_step = static_cast<int64_t>(w.NB) * w.PU * 256;
         float* gu = a.gu + (static_cast<int64_t>(row0) * w.NB + p.b) * w.PU * 256 + row;
-        int r = 0;
+        // A token at a time, in a loop: its code is fetched while the rings are loading, 5 us a miss, and unrolled it took 15 us.
+        uint64_t m = static_cast<uint64_t>(c.plan.mask[e][1]) << 32 | c.plan.mask[e][0];
 #pragma unroll 1
-        for (int t0 = 0; t0 < a.T; t0 += 16) {
-          const uint32_t m = (c.plan.mask[e][t0 >> 5] >> (t0 & 31)) & 0xffffu;
-          if (m == 0) continue;
-          uint32_t g[16], u[16];
-          tmem_ld16(tacc + t0, g);
-          tmem_ld16(tacc + 64 + t0, u);
+        for (int r = 0; m != 0; ++r, m &= m - 1) {
+          const int t = __ffsll(static_cast<long long>(m)) - 1;
+          uint32_t g, u;
+          tmem_ld1(tacc + t, g);
+          tmem_ld1(tacc + 64 + t, u);
           tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            reg_fence(g[i]);
-            reg_fence(u[i]);
+          reg_fence(g);
+          reg_fence(u);
+          if (whole) {
+            emit(p.s, r, p.b, __uint_as_float(g), __uint_as_float(u));
+          } else {
+            float* to = gu + r * gu_step + p.part * 256;
+            to[0] = __uint_as_float(g);
+            to[128] = __uint_as_float(u);
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if ((m >> i) & 1u) {
-              if (whole) {
-                emit(p.s, r, p.b, __uint_as_float(g[i]), __uint_as_float(u[i]));
-              } else {
-                float* to = gu + r * gu_step + p.part * 256;
-                to[0] = __uint_as_float(g[i]);
-                to[128] = __uint_as_float(u[i]);
-              }
-              ++r;
-            }
         }
         tc_fence_before();
         mbar_arrive(&c.acce[acc.i]);
         acc.step(2);
         if (!whole) {
           // The CTA that stores a block's last part adds all of them.
-          __threadfence();
           named_barrier(1, 128);
-          if (tid == 64) c.last = atomicAdd(parts + p.s * w.NB + p.b, 1) == w.PU - 1;
+          if (tid == 64) c.last = atom_add_acq_rel(parts + p.s * w.NB + p.b, 1) == w.PU - 1;
           named_barrier(1, 128);
           if (c.last == 0) continue;
-          __threadfence();
 #pragma unroll 1
           for (int i = 0; i < n; i += 2) {
             float g[2] = {0.0f, 0.0f}, u[2] = {0.0f, 0.0f};
@@ -661,7 +662,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // h is read by copies of other CTAs.
         fence_proxy_async_global();
-        __threadfence();
         named_barrier(1, 128);
         if (tid == 64) red_release_add(ready + p.s, 1);
       } else {
@@ -669,15 +669,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* o = a.o + (static_cast<int64_t>(row0) * w.PD + p.part) * a.d + p.b * 256 + row;
         const int64_t o_step = static_cast<int64_t>(w.PD) * a.d;
 #pragma unroll 1
-        for (int c0 = 0; c0 < n; c0 += 16) {
-          uint32_t v[2][16];
-          tmem_ld16(tacc + c0, v[0]);
-          tmem_ld16(tacc + 64 + c0, v[1]);
+        for (int c0 = 0; c0 < n; c0 += 4) {
+          uint32_t v[2][4];
+          tmem_ld4(tacc + c0, v[0]);
+          tmem_ld4(tacc + 64 + c0, v[1]);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 4; ++i) {
               reg_fence(v[j][i]);
               if (j < tiles && c0 + i < n) o[(c0 + i) * o_step + j * 128] = __uint_as_float(v[j][i]);
             }
@@ -685,91 +685,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(&c.acce[acc.i]);
         acc.step(2);
-        __threadfence();
         named_barrier(1, 128);
         if (tid == 64) red_release_add(done, 1);
       }
     }
-    // ---- y, when all rows of o are there: every CTA takes a share, four columns of a token a thread
+    // ---- y, when all rows of o are there: every CTA takes blocks of 128 columns of a token, four at once. A warp adds every fourth
+    // of the token's experts, and the four sums are added in order.
     if (ok) {
       if (tid == 64) c.last = wait_counter(done, w.total - w.nup, a.status, 210);
       named_barrier(1, 128);
       ok = c.last != 0;
     }
     if (ok) {
-      __threadfence();
-      const int picks = a.k + a.S, vecs = a.d >> 2, items = a.T * vecs;
-      // IT items (four columns of a token each) and PT parts of their rows at once: 18 loads under way. Loads that a token lacks
-      // read row 0 and count as 0.
-      auto sum = [&](auto it_, auto pt_, int i0, int step) {
-        constexpr int IT = decltype(it_)::value, PT = decltype(pt_)::value;
-        const float4* src[IT][9];
-        float gate[IT][9];
-        uint32_t live[IT];
-        float4 v[IT][9];
+      const int picks = a.k + a.S, units = a.T * w.KA;
+      float4 (*sums)[4][32] = reinterpret_cast<float4 (*)[4][32]>(ring);   // (every copy into the ring has been used)
+#pragma unroll 1
+      for (int u0 = static_cast<int>(blockIdx.x); u0 < units; u0 += 4 * ctas) {
+        const float4* src[4][3];
+        float gate[4][3];
+        float4 v[4][3];
 #pragma unroll
-        for (int n = 0; n < IT; ++n) {
-          const int i = i0 + n * step < items ? i0 + n * step : i0;
-          const int t = i / vecs, col = (i - t * vecs) * 4;
+        for (int n = 0; n < 4; ++n) {
+          const bool some = u0 + n * ctas < units;
+          const int u = some ? u0 + n * ctas : u0, t = u / w.KA, col = (u - t * w.KA) * 128 + lane * 4;
           const bool bad = (c.plan.bad[t >> 5] >> (t & 31)) & 1u;
-          live[n] = 0;
 #pragma unroll
-          for (int j = 0; j < 9; ++j) {
-            const bool has = j < a.k ? !bad : j < picks;
+          for (int i = 0; i < 3; ++i) {
+            const int j = warp - 2 + 4 * i;
+            const bool has = some && (j < a.k ? !bad : j < picks);
             const int r = !has ? 0 : (j < a.k ? c.plan.row[t * a.k + j] : t);        // (the shared expert's rows are the first)
-            gate[n][j] = has && j < a.k ? c.plan.gate[t * a.k + j] : 1.0f;
-            if (has) live[n] |= 1u << j;
-            src[n][j] = reinterpret_cast<const float4*>(a.o + static_cast<int64_t>(r) * w.PD * a.d + col);
-            v[n][j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            gate[n][i] = !has ? 0.0f : (j < a.k ? c.plan.gate[t * a.k + j] : 1.0f);
+            src[n][i] = has ? reinterpret_cast<const float4*>(a.o + static_cast<int64_t>(r) * w.PD * a.d + col) : nullptr;
+            v[n][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           }
         }
 #pragma unroll 1
-        for (int k = 0; k < w.PD; k += PT) {
-          float4 x[IT][PT][9];
+        for (int k = 0; k < w.PD; ++k) {
+          float4 x[4][3];
 #pragma unroll
-          for (int n = 0; n < IT; ++n)
+          for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int u = 0; u < PT; ++u)
+            for (int i = 0; i < 3; ++i) {
+              x[n][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (src[n][i] != nullptr) x[n][i] = ld_global_f4(src[n][i] + static_cast<int64_t>(k) * (a.d >> 2));
+            }
+          __syncwarp();                                    // all twelve are issued before the first is added
 #pragma unroll
-              for (int j = 0; j < 9; ++j) x[n][u][j] = ld_global_f4(src[n][j] + static_cast<int64_t>(k + u < w.PD ? k + u : k) * vecs);
-          __syncwarp();                                    // all of them are issued before the first is added (items are whole warps)
+          for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int n = 0; n < IT; ++n)
-#pragma unroll
-            for (int u = 0; u < PT; ++u)
-              if (k + u < w.PD) {
-#pragma unroll
-                for (int j = 0; j < 9; ++j) {
-                  const float4& y = x[n][u][j];
-                  v[n][j] = make_float4(v[n][j].x + y.x, v[n][j].y + y.y, v[n][j].z + y.z, v[n][j].w + y.w);
-                }
-              }
+            for (int i = 0; i < 3; ++i)
+              v[n][i] = make_float4(v[n][i].x + x[n][i].x, v[n][i].y + x[n][i].y, v[n][i].z + x[n][i].z, v[n][i].w + x[n][i].w);
         }
 #pragma unroll
-        for (int n = 0; n < IT; ++n) {
-          const int i = i0 + n * step;
-          if (i >= items) break;
-          const int t = i / vecs, col = (i - t * vecs) * 4;
+        for (int n = 0; n < 4; ++n) {
+          float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            if (src[n][i] != nullptr)
+              y = make_float4(fmaf(gate[n][i], v[n][i].x, y.x), fmaf(gate[n][i], v[n][i].y, y.y), fmaf(gate[n][i], v[n][i].z, y.z),
+                              fmaf(gate[n][i], v[n][i].w, y.w));
+          sums[n][warp - 2][lane] = y;
+        }
+        named_barrier(1, 128);
+        if (u0 + (warp - 2) * ctas < units) {               // a warp finishes a block
+          const int u = u0 + (warp - 2) * ctas, t = u / w.KA, col = (u - t * w.KA) * 128 + lane * 4;
           // A token without a valid choice has NaN scores, and so has its sum.
           const float zero = (c.plan.bad[t >> 5] >> (t & 31)) & 1u ? __int_as_float(0x7fffffff) : 0.0f;
           float4 y = make_float4(zero, zero, zero, zero);
 #pragma unroll
-          for (int j = 0; j < 9; ++j)
-            if ((live[n] >> j) & 1u)
-              y = make_float4(fmaf(gate[n][j], v[n][j].x, y.x), fmaf(gate[n][j], v[n][j].y, y.y), fmaf(gate[n][j], v[n][j].z, y.z),
-                              fmaf(gate[n][j], v[n][j].w, y.w));
-          *reinterpret_cast<uint2*>(a.y + static_cast<int64_t>(t) * a.d + col) =
-              make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+          for (int i = 0; i < 4; ++i) {
+            const float4 x = sums[warp - 2][i][lane];
+            y = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+          }
+          *reinterpret_cast<uint2*>(a.y + static_cast<int64_t>(t) * a.d + col) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
         }
-      };
-      // warps of 32 neighbouring items, spread over the CTAs
-      const int step = 4 * ctas * 32, i0 = ((warp - 2) * ctas + static_cast<int>(blockIdx.x)) * 32 + lane;
-      using One = std::integral_constant<int, 1>;
-      using Two = std::integral_constant<int, 2>;
-      if (w.PD == 1)
-        for (int i = i0; i < items; i += 2 * step) sum(Two{}, One{}, i, step);
-      else
-        for (int i = i0; i < items; i += step) sum(One{}, Two{}, i, step);
+        named_barrier(1, 128);
+      }
     }
   }
   tc_fence_before();
