@@ -541,8 +541,8 @@ MOE_API int moe_mla_status(const moe_mla_config_t* cfg, void* ws, int* code, int
  * no tokens; the status tells. A page out of range in the table or the pool sets the
  * status to MOE_ERR_BOUNDS; its tokens get slot -1. Pages must not be shared by sequences
  * that may leave them. Everything is read on the device, so a captured call replays.
- * batch 0..MOE_PAGES_MAX_BATCH; num_pages * page_size and (max_pages + 1) * page_size below
- * 2^31 - 1; seq, pos, slot and ws on 16-byte boundaries. ws: 16 bytes, zero before the
+ * batch 0..MOE_PAGES_MAX_BATCH; num_pages and max_new below 2^30, num_pages * page_size and
+ * (max_pages + 1) * page_size below 2^31 - 1; seq, pos, slot and ws on 16-byte boundaries. ws: 16 bytes, zero before the
  * first call (moe_pages_status clears them too); calls that share it must be ordered. */
 #define MOE_PAGES_MAX_BATCH 8192
 MOE_API int moe_pages_update(int batch, int page_size, int num_pages, int max_pages, int max_new, const int32_t* seq_lens,

@@ -328,10 +328,11 @@ def moe_pages_update(batch, page_size, num_pages, max_pages, max_new, seq_lens, 
                      lens_out, count_out, seq, pos, slot, starts, ws, stream=0):
     if (batch | page_size | num_pages | max_pages | max_new) >> 31:
         _int32("moe_pages_update", batch, page_size, num_pages, max_pages, max_new)
-    _check("moe_pages_update",
-           _lib.moe_pages_update(batch, page_size, num_pages, max_pages, max_new, _p(seq_lens), _p(target), _p(block_table),
-                                 _p(free_pages), _p(free_count), _p(lens_out), _p(count_out), _p(seq), _p(pos), _p(slot),
-                                 _p(starts), _p(ws), _p(stream)))
+    # addresses as they are: ctypes takes an int (0: null) or None for a pointer
+    rc = _lib.moe_pages_update(batch, page_size, num_pages, max_pages, max_new, seq_lens, target, block_table, free_pages,
+                               free_count, lens_out, count_out, seq, pos, slot, starts, ws, stream)
+    if rc != MOE_OK:
+        raise MoeError("moe_pages_update", rc)
 
 
 def moe_pages_status(ws, clear=True, stream=0):

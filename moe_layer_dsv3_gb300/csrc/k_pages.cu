@@ -27,6 +27,7 @@ constexpr int kTokens = 4;                 // consecutive tokens of a thread: th
 
 struct PagesArgs {
   int B, page, num_pages, max_pages, max_new;
+  int page_ctas;                           // CTAs, the first ones, that write pages; the others write tokens
   const int32_t* lens;
   const int32_t* target;
   int32_t* table;
@@ -41,13 +42,15 @@ struct PagesArgs {
   int* ws;                                 // {code, site, -, CTAs done}
 };
 
-// Sums over sequences in 64 bits: lengths may be anything.
+// Sums over sequences. Lengths may be anything, so a sum stays at kMost once it gets there: past every buffer, and two of
+// them still fit in 32 bits.
+constexpr int kMost = 1 << 30;
 struct Sums {
-  long long add, grow, drop;
+  int add, grow, drop;
   __device__ __forceinline__ void operator+=(const Sums& o) {
-    add += o.add;
-    grow += o.grow;
-    drop += o.drop;
+    add = min(add + o.add, kMost);
+    grow = min(grow + o.grow, kMost);
+    drop = min(drop + o.drop, kMost);
   }
 };
 
@@ -89,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
   const int per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   auto sums_of = [&](int b) {
     const int n = len[b], m = want[b], o = pages_of(n), w = pages_of(m);
-    return Sums{m > n ? m - n : 0, w > o ? w - o : 0, o > w ? o - w : 0};
+    return Sums{m > n ? min(m - n, kMost) : 0, max(w - o, 0), max(o - w, 0)};
   };
   if (!bad)
     for (int b = b0; b < b1; ++b) mine += sums_of(b);
@@ -101,6 +104,8 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
     if (lane >= o) at += v;
   }
   if (lane == 31) scan[warp] = at;
+  // (before this thread's run, within its warp; only used when no sum has reached kMost)
+  at = Sums{at.add - mine.add, at.grow - mine.grow, at.drop - mine.drop};
   __syncthreads();
   Sums all{0, 0, 0};
 #pragma unroll
@@ -110,23 +115,19 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
   }
   // A step that cannot be made as a whole is not made at all.
   int code = MOE_OK;
-  if (bad || all.add > a.max_new || count + all.drop > a.num_pages) code = MOE_ERR_BOUNDS;
+  if (bad || all.add > a.max_new || all.drop > a.num_pages - count) code = MOE_ERR_BOUNDS;
   else if (all.grow > count + all.drop) code = MOE_ERR_PAGES;
   if (code != MOE_OK) {
     if (blockIdx.x == 0 && tid == 0) report_error(a.ws, code, 220);
-    at = mine = all = Sums{0, 0, 0};
+    at = all = Sums{0, 0, 0};
   }
-  // Prefix sums before each sequence of this thread's run
-  at.add -= mine.add;
-  at.grow -= mine.grow;
-  at.drop -= mine.drop;
   for (int b = b0; b < b1; ++b) {
-    starts[b] = static_cast<int>(at.add);
-    taken[b] = static_cast<int>(at.grow);
-    left[b] = static_cast<int>(at.drop);
+    starts[b] = at.add;
+    taken[b] = at.grow;
+    left[b] = at.drop;
     if (code == MOE_OK) at += sums_of(b);
   }
-  const int N = static_cast<int>(all.add), G = static_cast<int>(all.grow), F = static_cast<int>(all.drop);
+  const int N = all.add, G = all.grow, F = all.drop;
   if (tid == 0) {
     starts[a.B] = N;
     taken[a.B] = G;
@@ -138,55 +139,60 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
     if (page < 0 || page >= a.num_pages) report_error(a.ws, MOE_ERR_BOUNDS, 221);
     return page;
   };
-  // The i-th page that is left, and the i-th that is taken.
-  auto left_page = [&](int i) {
+  // Where the i-th page that is left, and the i-th that is taken, is written.
+  auto left_at = [&](int i) {
     const int b = owner(left, a.B, i);
-    return checked(ld_global_s32(a.table + static_cast<int64_t>(b) * a.max_pages + pages_of(want[b]) + i - left[b]));
+    return a.table + static_cast<int64_t>(b) * a.max_pages + pages_of(want[b]) + i - left[b];
   };
-  auto taken_page = [&](int i) { return i < F ? left_page(F - 1 - i) : checked(ld_global_s32(a.free_pages + count + F - 1 - i)); };
-  const int all_threads = static_cast<int>(gridDim.x) * kThreads, me = static_cast<int>(blockIdx.x) * kThreads + tid;
-  for (int i = me; i < G; i += all_threads) {
-    const int b = owner(taken, a.B, i);
-    a.table[static_cast<int64_t>(b) * a.max_pages + pages_of(len[b]) + i - taken[b]] = taken_page(i);
-  }
-  for (int i = me; i < F - G; i += all_threads) a.free_pages[count + i] = left_page(i);
-  for (int b = me; b <= a.B; b += all_threads) a.starts[b] = starts[b];
-
-  for (int64_t i0 = static_cast<int64_t>(me) * kTokens; i0 < a.max_new; i0 += static_cast<int64_t>(all_threads) * kTokens) {
-    int s[kTokens], p[kTokens], w[kTokens];
-    int b = i0 < N ? owner(starts, a.B, static_cast<int>(i0)) : 0, pi = -1, page = 0;
-#pragma unroll
-    for (int k = 0; k < kTokens; ++k) {
-      const int i = static_cast<int>(i0) + k;
-      s[k] = 0;
-      p[k] = w[k] = -1;
-      if (i0 + k >= N) continue;
-      while (starts[b + 1] <= i) {         // (sequences without new tokens lie between)
-        ++b;
-        pi = -1;
-      }
-      s[k] = b;
-      p[k] = len[b] + i - starts[b];
-      const int j = p[k] / a.page;
-      if (j != pi) {
-        pi = j;
-        const int old = pages_of(len[b]);
-        page = j < old ? checked(ld_global_s32(a.table + static_cast<int64_t>(b) * a.max_pages + j)) : taken_page(taken[b] + j - old);
-      }
-      if (page >= 0 && page < a.num_pages) w[k] = page * a.page + p[k] - j * a.page;
+  auto taken_at = [&](int i) { return i < F ? left_at(F - 1 - i) : a.free_pages + count + F - 1 - i; };
+  const int bid = static_cast<int>(blockIdx.x);
+  if (bid < a.page_ctas) {
+    const int step = a.page_ctas * kThreads, me = bid * kThreads + tid;
+    for (int i = me; i < G; i += step) {
+      const int b = owner(taken, a.B, i);
+      a.table[static_cast<int64_t>(b) * a.max_pages + pages_of(len[b]) + i - taken[b]] = checked(ld_global_s32(taken_at(i)));
     }
-    if (i0 + kTokens <= a.max_new) {
-      *reinterpret_cast<int4*>(a.seq + i0) = make_int4(s[0], s[1], s[2], s[3]);
-      *reinterpret_cast<int4*>(a.pos + i0) = make_int4(p[0], p[1], p[2], p[3]);
-      *reinterpret_cast<int4*>(a.slot + i0) = make_int4(w[0], w[1], w[2], w[3]);
-    } else {
+    for (int i = me; i < F - G; i += step) a.free_pages[count + i] = checked(ld_global_s32(left_at(i)));
+    for (int b = me; b <= a.B; b += step) a.starts[b] = starts[b];
+  } else {
+    const int64_t step = static_cast<int64_t>(gridDim.x - a.page_ctas) * kThreads * kTokens;
+    for (int64_t i0 = (static_cast<int64_t>(bid - a.page_ctas) * kThreads + tid) * kTokens; i0 < a.max_new; i0 += step) {
+      int s[kTokens], p[kTokens], w[kTokens], in[kTokens];
+      const int32_t* at_page[kTokens];
+      int b = i0 < N ? owner(starts, a.B, static_cast<int>(i0)) : 0;
+#pragma unroll
+      for (int k = 0; k < kTokens; ++k) {
+        const int i = static_cast<int>(i0) + k;
+        s[k] = 0;
+        p[k] = w[k] = -1;
+        at_page[k] = nullptr;
+        if (i0 + k >= N) continue;
+        while (starts[b + 1] <= i) ++b;    // (sequences without new tokens lie between)
+        s[k] = b;
+        p[k] = len[b] + i - starts[b];
+        const int j = p[k] / a.page, old = pages_of(len[b]);
+        in[k] = p[k] - j * a.page;
+        at_page[k] = j < old ? a.table + static_cast<int64_t>(b) * a.max_pages + j : taken_at(taken[b] + j - old);
+      }
+      int page[kTokens];
+#pragma unroll
+      for (int k = 0; k < kTokens; ++k) page[k] = at_page[k] != nullptr ? ld_global_s32(at_page[k]) : -1;
 #pragma unroll
       for (int k = 0; k < kTokens; ++k)
-        if (i0 + k < a.max_new) {
-          a.seq[i0 + k] = s[k];
-          a.pos[i0 + k] = p[k];
-          a.slot[i0 + k] = w[k];
-        }
+        if (at_page[k] != nullptr && checked(page[k]) >= 0 && page[k] < a.num_pages) w[k] = page[k] * a.page + in[k];
+      if (i0 + kTokens <= a.max_new) {
+        *reinterpret_cast<int4*>(a.seq + i0) = make_int4(s[0], s[1], s[2], s[3]);
+        *reinterpret_cast<int4*>(a.pos + i0) = make_int4(p[0], p[1], p[2], p[3]);
+        *reinterpret_cast<int4*>(a.slot + i0) = make_int4(w[0], w[1], w[2], w[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k)
+          if (i0 + k < a.max_new) {
+            a.seq[i0 + k] = s[k];
+            a.pos[i0 + k] = p[k];
+            a.slot[i0 + k] = w[k];
+          }
+      }
     }
   }
   // Every thread of this CTA has read lengths and count.
@@ -216,7 +222,8 @@ extern "C" int moe_pages_update(int batch, int page_size, int num_pages, int max
                                 int32_t* lens_out, int32_t* count_out, int32_t* seq, int32_t* pos, int32_t* slot,
                                 int32_t* starts, void* ws, moe_stream_t stream) {
   const int64_t lim = (1LL << 31) - 1;
-  if (batch < 0 || batch > MOE_PAGES_MAX_BATCH || page_size < 1 || num_pages < 1 || max_pages < 1 || max_new < 0)
+  if (batch < 0 || batch > MOE_PAGES_MAX_BATCH || page_size < 1 || num_pages < 1 || max_pages < 1 || max_new < 0 ||
+      max_new >= kMost || num_pages >= kMost)
     return MOE_ERR_INVALID_ARG;
   if (static_cast<int64_t>(num_pages) * page_size >= lim || static_cast<int64_t>(max_pages + 1LL) * page_size >= lim)
     return MOE_ERR_INVALID_ARG;
@@ -229,8 +236,8 @@ extern "C" int moe_pages_update(int batch, int page_size, int num_pages, int max
   if (!arch_ok()) return MOE_ERR_UNSUPPORTED_ARCH;
   CallScope call;
   static DevOnce once;
-  constexpr int kMost = (5 * MOE_PAGES_MAX_BATCH + 3) * static_cast<int>(sizeof(int));
-  if (!once.ready([] { return cudaFuncSetAttribute(pages_update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost); }))
+  constexpr int kSmemMost = (5 * MOE_PAGES_MAX_BATCH + 3) * static_cast<int>(sizeof(int));
+  if (!once.ready([] { return cudaFuncSetAttribute(pages_update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost); }))
     return MOE_ERR_CUDA;
   PagesArgs a{};
   a.B = batch;
@@ -250,9 +257,13 @@ extern "C" int moe_pages_update(int batch, int page_size, int num_pages, int max
   a.slot = slot;
   a.starts = starts;
   a.ws = static_cast<int*>(ws);
-  const int64_t blocks = ceil_div(max_new, kThreads * kTokens), most = 2LL * num_sms();
-  launch_kernel_after("pages_update", pages_update_kernel, dim3(static_cast<unsigned>(blocks < 1 ? 1 : (blocks < most ? blocks : most))),
-                      dim3(kThreads), (5 * batch + 3) * sizeof(int), static_cast<cudaStream_t>(stream), a);
+  // Pages and tokens by CTAs of their own: one after the other in the same threads cost 2 us of 8 (512 sequences).
+  const int64_t most = num_sms(), pages = ceil_div(max_new / page_size + batch + 1, kThreads);
+  const int64_t tokens = ceil_div(max_new, kThreads * kTokens);
+  a.page_ctas = static_cast<int>(pages < most ? pages : most);
+  const int grid = a.page_ctas + static_cast<int>(tokens < 4 * most ? tokens : 4 * most);
+  launch_kernel_after("pages_update", pages_update_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+                      (5 * batch + 3) * sizeof(int), static_cast<cudaStream_t>(stream), a);
   return call.status();
 }
 
