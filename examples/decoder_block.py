@@ -3,8 +3,9 @@
 Serving: a prompt's latent rows are appended to a paged cache, then each step
 appends one token a sequence, attends over the cache (absorbed latent
 attention), and runs add + RMSNorm -> MoE layer, the layer reading the norm's
-MXFP8 codes from its workspace. Training: the norm and the layer forward and
-backward. Projections are plain torch products; weights are random.
+MXFP8 codes from its workspace. Drafted tokens: pages taken for them, a tree of them
+attended at once, the MoE layer of the few tokens, and the rejected ones' pages left again.
+Training: the norm and the layer forward and backward. Projections are plain torch products; weights are random.
 
     python examples/decoder_block.py [--steps 4]
 
@@ -23,8 +24,10 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from moe_layer_dsv3_gb300 import MOE_FLAG_X_QUANTIZED  # noqa: E402
 from moe_layer_dsv3_gb300.attention import LatentAttention  # noqa: E402
+from moe_layer_dsv3_gb300.few import FewTokenMoE  # noqa: E402
 from moe_layer_dsv3_gb300.layer import MoELayer  # noqa: E402
 from moe_layer_dsv3_gb300.norm import AddRMSNorm  # noqa: E402
+from moe_layer_dsv3_gb300.pages import PagePlan  # noqa: E402
 
 EPS = 1e-6
 
@@ -46,7 +49,7 @@ class DecoderBlock:
     """norm -> latent attention -> add + norm -> MoE, one new token a sequence."""
 
     def __init__(self, batch, d=1024, heads=16, nope=128, rope=64, latent=512, experts=16, topk=4, inner=256,
-                 page_size=64, num_pages=64, max_pages=8, seed=0):
+                 page_size=64, num_pages=64, max_pages=8, seed=0, drafts=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
         w = lambda *s: (torch.randn(*s, generator=g, device="cuda") * s[-1] ** -0.5).to(torch.bfloat16)
         self.B, self.d, self.H, self.nope, self.rope, self.latent = batch, d, heads, nope, rope, latent
@@ -58,11 +61,15 @@ class DecoderBlock:
         self.w_o = w(d, heads * nope)
         self.cos_sin = rope_table(page_size * max_pages, rope)
         self.norm_in, self.norm_out = AddRMSNorm(batch, d, EPS), AddRMSNorm(batch, d, EPS)
-        self.att = LatentAttention(batch, heads, latent, rope, page_size, num_pages, max_pages, (nope + rope) ** -0.5)
+        self.att = LatentAttention(batch, heads, latent, rope, page_size, num_pages, max_pages, (nope + rope) ** -0.5,
+                                 drafts=drafts)
         self.cache = self.att.new_cache()
         self.moe = MoELayer(batch, d, experts, topk, 1, 1, inner, 1, 128, flags=MOE_FLAG_X_QUANTIZED)
         self.w_router, self.bias = w(experts, d), torch.zeros(experts, device="cuda")
         self.moe.quantize_weights(w(experts, 2 * inner, d), w(experts, d, inner), w(1, 2 * inner, d), w(1, d, inner))
+        if drafts:                                             # the same weights, for a step's drafted tokens
+            self.few = FewTokenMoE(batch * drafts, d, experts, topk, 1, 1, inner, 1, wq=self.moe.wq)
+            self.tree_in, self.tree_out = AddRMSNorm(batch * drafts, d, EPS), AddRMSNorm(batch * drafts, d, EPS)
 
     def prefill(self, x, block_table, seq, pos):
         """Cache the tokens x [n][d] (the input stream) at positions pos of sequences seq."""
@@ -83,6 +90,23 @@ class DecoderBlock:
         attn = torch.einsum("bhc,hnc->bhn", o, self.w_uv).reshape(B, -1) @ self.w_o.T
         z = self.norm_out.forward(attn, self.g_out, residual=x, layer=self.moe)
         return self.norm_out.h + self.moe.forward(z, self.w_router, self.bias)
+
+    def draft(self, x, block_table, lens, seq, pos, angle, tree):
+        """Drafted tokens x [batch][n][d], the last ones of lens tokens: at places pos of sequences seq [batch * n], rotated by
+        angle [batch][n] (a token's depth in its sequence: not its place, where a tree branches). Returns the block's output."""
+        B, n, H = x.shape[0], x.shape[1], self.H
+        cs = self.cos_sin[angle.long()]                        # [B][n][rope]
+        y = self.tree_in.forward(x.view(B * n, -1), self.g_in)
+        kv = y @ self.w_kv.T
+        kv[:, self.latent:] = rotate(kv[:, self.latent:].float(), cs.view(B * n, -1)).to(torch.bfloat16)
+        self.att.append(kv, self.cache, block_table, seq, pos, gamma=self.g_kv, eps=EPS)
+        q = (y @ self.w_q.T).view(B, n, H, self.nope + self.rope)
+        q_lat = torch.einsum("bihn,hnc->bihc", q[..., :self.nope], self.w_uk)
+        q_rot = rotate(q[..., self.nope:].float(), cs[:, :, None]).to(torch.bfloat16)
+        o = self.att.decode_tree(torch.cat([q_lat, q_rot], 3), self.cache, block_table, lens, tree=tree)
+        attn = torch.einsum("bihc,hnc->bihn", o, self.w_uv).reshape(B * n, -1) @ self.w_o.T
+        z = self.tree_out.forward(attn, self.g_out, residual=x.view(B * n, -1))
+        return self.tree_out.h + self.few.forward(z, self.w_router, self.bias)
 
     def reference(self, x, streams, pos):
         """The block's residual stream after attention and the MoE's input in 64 bits, from each sequence's whole stream."""
@@ -130,6 +154,49 @@ def serve(steps, verbose=True):
     return worst
 
 
+def speculate(steps, verbose=True):
+    """Steps with five drafted tokens a sequence: a chain 0-1-2 with a branch 3-4 at its first token. Some of the chain is kept."""
+    B, n, page, max_pages, pool = 5, 5, 16, 24, 70
+    parent = [-1, 0, 1, 0, 3]
+    paths = []
+    for i, p in enumerate(parent):
+        paths.append((paths[p] if p >= 0 else []) + [i])
+    blk = DecoderBlock(B, page_size=page, max_pages=max_pages, num_pages=pool, drafts=n)
+    plan = PagePlan(B, page, pool, max_pages, 700)
+    table, free, count, lens = plan.new_pool()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    start = [1, 63, 64, 200, 130]
+    streams = [torch.randn(k, blk.d, generator=g, device="cuda").to(torch.bfloat16) for k in start]
+    target = torch.tensor(start, dtype=torch.int32, device="cuda")
+    plan.update(lens, target, table, free, count)
+    total = sum(start)
+    blk.prefill(torch.cat(streams), table, plan.seq[:total], plan.pos[:total])
+    tree = torch.tensor([[sum(1 << j for j in p) for p in paths]] * B, dtype=torch.int64, device="cuda")
+    depth = torch.tensor([len(p) - 1 for p in paths], device="cuda")
+    worst = 0.0
+    for step in range(steps):
+        x = torch.randn(B, n, blk.d, generator=g, device="cuda").to(torch.bfloat16)
+        angle = lens[:, None] + depth
+        plan.update(lens, lens + n, table, free, count)
+        out = blk.draft(x, table, lens, plan.seq[:B * n], plan.pos[:B * n], angle, tree)
+        torch.cuda.synchronize()
+        for part in (plan, blk.att, blk.few):
+            part.check_status()
+        assert torch.isfinite(out).all()
+        h, z = blk.tree_out.h.view(B, n, -1).double(), blk.tree_out.y.view(B, n, -1).double()
+        for i, path in enumerate(paths):                       # each drafted token is the last of its own stream
+            own = [torch.cat([s, x[b, path]]) for b, s in enumerate(streams)]
+            rh, rz = blk.reference(x[:, i], own, angle[:, i])
+            worst = max(worst, float((h[:, i] - rh).norm() / rh.norm()), float((z[:, i] - rz).norm() / rz.norm()))
+        kept = [(step + b) % 4 for b in range(B)]              # of the chain; the others' places are free again
+        streams = [torch.cat([s, x[b, :k]]) for b, (s, k) in enumerate(zip(streams, kept))]
+        plan.update(lens, lens - n + torch.tensor(kept, dtype=torch.int32, device="cuda"), table, free, count)
+        assert lens.tolist() == [len(s) for s in streams]
+    if verbose:
+        print("served %d steps of %d drafted tokens a sequence, largest relative error %.1e" % (steps, n, worst))
+    return worst
+
+
 def train(verbose=True):
     """add + norm -> MoE forward and backward; the gradients of the norm's inputs join the residual path's."""
     T, d = 256, 512
@@ -159,4 +226,5 @@ if __name__ == "__main__":
     ap.add_argument("--steps", type=int, default=4)
     a = ap.parse_args()
     serve(a.steps)
+    speculate(a.steps)
     train()

@@ -569,7 +569,8 @@ MOE_API int moe_pages_status(void* ws, int* code, int* site, int clear, moe_stre
  *   topk_w fp32 [T][k] are written.
  *   ws: moe_few_workspace_size bytes, zero before the first call; calls that share it
  *   must be ordered by the caller. It grows with T, so that of a larger T serves too.
- * A token whose scores are NaN gets y = NaN and sets the status to MOE_ERR_BOUNDS.
+ * A token with a NaN gets y = NaN, and so does one that has fewer than k experts to
+ * choose from because their biases are NaN, which sets the status to MOE_ERR_BOUNDS.
  * An expert that no token chose is not read, and a token's y does not depend on the
  * other tokens' values (its last bits may depend on how many there are and on what
  * they chose, since sums are cut where the work is). x, w_router, wq, y and ws on

@@ -10,7 +10,7 @@ import torch
 
 from . import (MOE_ERR_INVALID_ARG, MoeError, mla_config, moe_mla_append, moe_mla_decode, moe_mla_decode_tree,
                moe_mla_status, moe_mla_workspace_size)
-from .norm import check_tensor
+from .norm import check_device, check_tensor
 
 
 class LatentAttention:
@@ -102,6 +102,7 @@ class LatentAttention:
             check_tensor("drafts", drafts, torch.int32, (self.batch,))
         check_tensor("out", out, torch.bfloat16, (self.batch, n, self.heads, self.latent))
         check_tensor("lse", lse, torch.float32, (self.batch, n, self.heads))
+        check_device(q, cache, block_table, seq_lens, tree, drafts, out, lse, self.ws)
         moe_mla_decode_tree(self.cfg, n, q.data_ptr(), sb, sh, cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
                             drafts.data_ptr() if drafts is not None else 0, tree.data_ptr() if tree is not None else 0,
                             out.data_ptr(), lse.data_ptr(), self.ws.data_ptr(), stream)

@@ -262,7 +262,7 @@ struct FewPlan {
   uint16_t first[kMaxEp + 1];              // row of a slot's first token
   uint16_t row[kMaxPicks];                 // of a token's pick
   float gate[kMaxPicks];
-  uint32_t bad[2];                         // tokens without a valid choice: their scores are NaN
+  uint32_t bad[2];                         // tokens without a valid choice (biases of NaN)
   uint32_t scan[kThreads / 32];
   int slots;
 };
@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_barrier(1, 128);
         if (u0 + (warp - 2) * ctas < units) {               // a warp finishes a block
           const int u = u0 + (warp - 2) * ctas, t = u / w.KA, col = (u - t * w.KA) * 128 + lane * 4;
-          // A token without a valid choice has NaN scores, and so has its sum.
+          // A token without a valid choice: NaN.
           const float zero = (c.plan.bad[t >> 5] >> (t & 31)) & 1u ? __int_as_float(0x7fffffff) : 0.0f;
           float4 y = make_float4(zero, zero, zero, zero);
 #pragma unroll

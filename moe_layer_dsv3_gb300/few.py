@@ -9,7 +9,7 @@ import torch
 
 from . import (MOE_ERR_INVALID_ARG, MoeError, config, moe_few_forward, moe_few_status, moe_few_workspace_size,
                moe_quantize_weights, moe_weights_size)
-from .norm import check_tensor
+from .norm import check_device, check_tensor
 
 
 class FewTokenMoE:
@@ -56,6 +56,7 @@ class FewTokenMoE:
         if y is None:
             y = self.y[:t]
         check_tensor("y", y, torch.bfloat16, (t, self.d))
+        check_device(x, w_router, bias, y, self.ws)
         cfg = self._cfgs.get(t)
         if cfg is None:
             cfg = self._cfgs[t] = config(t, *self._shape)

@@ -18,6 +18,14 @@ def check_tensor(name, t, dtype, shape):
                        MOE_ERR_INVALID_ARG)
 
 
+def check_device(*tensors):
+    """All of them on the current device, where the library launches (it sees only addresses)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise MoeError("a tensor of device %d while device %d is current" % (t.get_device(), dev), MOE_ERR_INVALID_ARG)
+
+
 class AddRMSNorm:
     """h = x + residual, y = h rstd gamma; with mx=True also MX(y) as codes and row-major scales."""
 

@@ -8,7 +8,7 @@ from __future__ import annotations
 import torch
 
 from . import MoeError, moe_pages_status, moe_pages_update
-from .norm import check_tensor
+from .norm import check_device, check_tensor
 
 
 class PagePlan:
@@ -39,10 +39,14 @@ class PagePlan:
         count_out = free_count if count_out is None else count_out
         b, t, n, one = self._shapes
         # (a step takes a few microseconds on the GPU: one plain loop costs half of what seven calls of check_tensor do)
+        dev = self.ws.get_device()
+        if dev != torch.cuda.current_device():
+            check_device(self.ws)
         for x, shape in ((seq_lens, b), (target, b), (block_table, t), (free_pages, n), (free_count, one), (lens_out, b),
                          (count_out, one)):
-            if x.dtype is not torch.int32 or x.shape != shape or not x.is_cuda or not x.is_contiguous():
+            if x.dtype is not torch.int32 or x.shape != shape or x.get_device() != dev or not x.is_contiguous():
                 check_tensor("one of the arrays", x, torch.int32, shape)
+                check_device(x)
         moe_pages_update(self.batch, self.page_size, self.num_pages, self.max_pages, self.max_new, seq_lens.data_ptr(),
                          target.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
                          lens_out.data_ptr(), count_out.data_ptr(), self.seq.data_ptr(), self.pos.data_ptr(),
