@@ -28,7 +28,8 @@
 // Taken from a list, pieces keep every SM loading to the end. Equal ranges fixed in
 // advance, in a kernel for each projection, left some SMs 15 % behind the others (HBM does
 // not serve all alike), and HBM idle for 9 us between the kernels: 106 us for one
-// token, 403 for 16 and 544 for 64, where the list takes NEWFIG.
+// token of 9 such experts, 403 for 16 tokens and 47 experts, 544 for 64 and 61, where the list takes
+// 77, 339 and 416: 5.3, 6.3 and 6.7 TB/s of the weights read.
 #include <cudaTypedefs.h>
 
 #include "gemm.cuh"
@@ -434,6 +435,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_wait();
   grid_launch();
+  // The first piece, on its way while the plan is made. It is taken like all others: given by a CTA's number it could be one
+  // that others wait for while its CTA has no SM (two such kernels at once).
+  int first = 0;
+  if (tid == 0) first = atomicAdd(a.cnt, 1);
   tc_fence_before();
   make_plan(a, c.plan, blockIdx.x == 0);                   // (ends with a barrier)
   tc_fence_after();
@@ -449,7 +454,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   w.PD = w.slots > 0 ? parts_of(w.slots * w.RP, w.KI, ctas, kDownPieces) : 1;
   w.nup = w.slots * w.NB * w.PU;
   w.total = w.nup + w.slots * w.RP * w.PD;
-  int* taken = a.cnt;
   int* done = a.cnt + 1;
   int* ready = a.cnt + 2;
   int* parts = ready + w.slots;
@@ -472,13 +476,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         st.i = a.nst - 1;
         st.phase ^= 1u;
       }
-      ok = warp_wait(&c.full[st.i], st.phase, a.status, 202) && ok;
+      ok = ok && warp_wait(&c.full[st.i], st.phase, a.status, 202);   // (the CTA stays a while after a wait that gave up)
     }
   };
   if (warp == 0) {
     Stage st;
     int issued = 0;
-    int id = static_cast<int>(blockIdx.x);
+    int id = __shfl_sync(0xffffffffu, first, 0);
     while (ok) {
       const bool more = id < w.total;
       ok = warp_wait(&c.qe[q.i], q.phase ^ 1u, a.status, 203);
@@ -487,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         *reinterpret_cast<volatile int*>(&c.queue[q.i]) = more ? id : -1;
         mbar_arrive(&c.qf[q.i]);
-        if (more) ahead = atomicAdd(taken, 1);             // its latency passes behind this piece's loads
+        if (more) ahead = atomicAdd(a.cnt, 1);             // its latency passes behind this piece's loads
       }
       __syncwarp();
       q.step(kQueue);
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         st.step(a.nst);
         ++issued;
       }
-      id = ctas + __shfl_sync(0xffffffffu, ahead, 0);
+      id = __shfl_sync(0xffffffffu, ahead, 0);
     }
     land(st, issued);
   } else if (warp == 6) {

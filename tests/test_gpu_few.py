@@ -361,3 +361,18 @@ def test_refused_tensors(lib):
     bad(c.x, c.w_router, c.bias, y=wide)
     with pytest.raises(lib.MoeError):
         f.quantize_weights(c.gu[:7], c.down[:8])
+
+
+def test_two_layers_at_once(lib):
+    """Calls on two streams, each with a workspace of its own: their CTAs share the SMs, and neither waits for one that has none."""
+    a, b = Case(16, 2048, 24, 4, 1, 1, 512, 1, seed=17), Case(30, 1024, 24, 4, 1, 1, 1024, 0, seed=18)
+    want = [a.run().clone(), b.run().clone()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for c, s in zip((a, b), streams):
+            c.few.forward(c.x, c.w_router, c.bias, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    for c, w in zip((a, b), want):
+        assert c.few.status() == (0, 0)
+        assert torch.equal(c.few.y, w)
