@@ -384,6 +384,86 @@ __device__ __forceinline__ Piece piece_of(const Work& w, int id) {
   return p;
 }
 
+// y from the rows of o, by the epilogue's four warps: blocks of 128 columns of a token, IT at once. A warp adds every fourth of the
+// token's experts, and the four sums (in `sums`, shared memory) are added in order.
+// Not inlined, so that a first call which only goes through it (`real` false: it reads and writes no global memory) fetches
+// the code while the router works: at the end of the list, one miss after another, that took 6 of few_small's 54 us.
+template <int IT>
+__device__ __noinline__ void sum_blocks(const FewArgs& a, const FewPlan& p, float4* sums_, int PD, bool real) {
+  float4 (*sums)[4][32] = reinterpret_cast<float4 (*)[4][32]>(sums_);
+  const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
+  const int cols = a.d >> 7, ctas = static_cast<int>(gridDim.x), picks = a.k + a.S;
+  const int begin = static_cast<int>(blockIdx.x), units = real ? a.T * cols : begin + 1;
+#pragma unroll 1
+  for (int u0 = begin; u0 < units; u0 += IT * ctas) {
+    const float4* src[IT][3];
+    float gate[IT][3];
+    float4 v[IT][3];
+#pragma unroll
+    for (int n = 0; n < IT; ++n) {
+      const bool some = real && u0 + n * ctas < units;
+      const int u = some ? u0 + n * ctas : 0, t = u / cols, col = (u - t * cols) * 128 + lane * 4;
+      const bool bad = (p.bad[t >> 5] >> (t & 31)) & 1u;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int j = warp + 4 * i;
+        const bool has = some && (j < a.k ? !bad : j < picks);
+        const int r = !has ? 0 : (j < a.k ? p.row[t * a.k + j] : t);                 // (the shared expert's rows are the first)
+        gate[n][i] = !has ? 0.0f : (j < a.k ? p.gate[t * a.k + j] : 1.0f);
+        src[n][i] = has ? reinterpret_cast<const float4*>(a.o + static_cast<int64_t>(r) * PD * a.d + col) : nullptr;
+        v[n][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+    }
+#pragma unroll 1
+    for (int k = 0; k < PD; ++k) {
+      float4 x[IT][3];
+#pragma unroll
+      for (int n = 0; n < IT; ++n)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          x[n][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (src[n][i] != nullptr) x[n][i] = ld_global_f4(src[n][i] + static_cast<int64_t>(k) * (a.d >> 2));
+        }
+      __syncwarp();                                        // all of them are issued before the first is added
+#pragma unroll
+      for (int n = 0; n < IT; ++n)
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          v[n][i] = make_float4(v[n][i].x + x[n][i].x, v[n][i].y + x[n][i].y, v[n][i].z + x[n][i].z, v[n][i].w + x[n][i].w);
+    }
+#pragma unroll
+    for (int n = 0; n < IT; ++n) {
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (src[n][i] != nullptr)
+          y = make_float4(fmaf(gate[n][i], v[n][i].x, y.x), fmaf(gate[n][i], v[n][i].y, y.y), fmaf(gate[n][i], v[n][i].z, y.z),
+                          fmaf(gate[n][i], v[n][i].w, y.w));
+      sums[n][warp][lane] = y;
+    }
+    named_barrier(1, 128);
+    if (warp < IT) {                                       // a warp finishes a block
+      const int u = u0 + warp * ctas, t = u / cols, col = (u - t * cols) * 128 + lane * 4;
+      // A token without a valid choice: NaN.
+      const float zero = u < units && (p.bad[(t >> 5) & 1] >> (t & 31)) & 1u ? __int_as_float(0x7fffffff) : 0.0f;
+      float4 y = make_float4(zero, zero, zero, zero);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 x = sums[warp][i][lane];
+        y = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+      }
+      if (real && u < units)
+        *reinterpret_cast<uint2*>(a.y + static_cast<int64_t>(t) * a.d + col) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+    }
+    named_barrier(1, 128);
+  }
+}
+// One block at once where there is no more than one a CTA: less code to fetch.
+__device__ __forceinline__ void sum_y(const FewArgs& a, const FewPlan& p, float4* sums, int PD, bool real) {
+  if (a.T * (a.d >> 7) <= static_cast<int>(gridDim.x)) sum_blocks<1>(a, p, sums, PD, real);
+  else sum_blocks<4>(a, p, sums, PD, real);
+}
+
 // Warps: 0 takes pieces and loads weights, 6 loads X and H, 1 issues the products, 2-5 epilogue (row = TMEM lane).
 // Stage: [256 rows of weights][N rows of X or H], and three scale atoms.
 __global__ void __launch_bounds__(kThreads, 1)
@@ -432,6 +512,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     fetch(a.w1sf + at1 / 32, n1 / 32);
     fetch(a.w2 + at2, n2);
     fetch(a.w2sf + at2 / 32, n2 / 32);
+  }
+  if (warp >= 2 && warp < 6) {
+    sum_y(a, c.plan, reinterpret_cast<float4*>(ring), 1, false);
+    fence_proxy_async();                                   // (copies into the ring come after its stores)
   }
   grid_wait();
   grid_launch();
@@ -693,79 +777,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid == 64) red_release_add(done, 1);
       }
     }
-    // ---- y, when all rows of o are there: every CTA takes blocks of 128 columns of a token, four at once. A warp adds every fourth
-    // of the token's experts, and the four sums are added in order.
+    // ---- y, when all rows of o are there: every CTA takes a share
     if (ok) {
       if (tid == 64) c.last = wait_counter(done, w.total - w.nup, a.status, 210);
       named_barrier(1, 128);
       ok = c.last != 0;
     }
-    if (ok) {
-      const int picks = a.k + a.S, units = a.T * w.KA;
-      float4 (*sums)[4][32] = reinterpret_cast<float4 (*)[4][32]>(ring);   // (every copy into the ring has been used)
-#pragma unroll 1
-      for (int u0 = static_cast<int>(blockIdx.x); u0 < units; u0 += 4 * ctas) {
-        const float4* src[4][3];
-        float gate[4][3];
-        float4 v[4][3];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const bool some = u0 + n * ctas < units;
-          const int u = some ? u0 + n * ctas : u0, t = u / w.KA, col = (u - t * w.KA) * 128 + lane * 4;
-          const bool bad = (c.plan.bad[t >> 5] >> (t & 31)) & 1u;
-#pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            const int j = warp - 2 + 4 * i;
-            const bool has = some && (j < a.k ? !bad : j < picks);
-            const int r = !has ? 0 : (j < a.k ? c.plan.row[t * a.k + j] : t);        // (the shared expert's rows are the first)
-            gate[n][i] = !has ? 0.0f : (j < a.k ? c.plan.gate[t * a.k + j] : 1.0f);
-            src[n][i] = has ? reinterpret_cast<const float4*>(a.o + static_cast<int64_t>(r) * w.PD * a.d + col) : nullptr;
-            v[n][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          }
-        }
-#pragma unroll 1
-        for (int k = 0; k < w.PD; ++k) {
-          float4 x[4][3];
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int i = 0; i < 3; ++i) {
-              x[n][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (src[n][i] != nullptr) x[n][i] = ld_global_f4(src[n][i] + static_cast<int64_t>(k) * (a.d >> 2));
-            }
-          __syncwarp();                                    // all twelve are issued before the first is added
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-              v[n][i] = make_float4(v[n][i].x + x[n][i].x, v[n][i].y + x[n][i].y, v[n][i].z + x[n][i].z, v[n][i].w + x[n][i].w);
-        }
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            if (src[n][i] != nullptr)
-              y = make_float4(fmaf(gate[n][i], v[n][i].x, y.x), fmaf(gate[n][i], v[n][i].y, y.y), fmaf(gate[n][i], v[n][i].z, y.z),
-                              fmaf(gate[n][i], v[n][i].w, y.w));
-          sums[n][warp - 2][lane] = y;
-        }
-        named_barrier(1, 128);
-        if (u0 + (warp - 2) * ctas < units) {               // a warp finishes a block
-          const int u = u0 + (warp - 2) * ctas, t = u / w.KA, col = (u - t * w.KA) * 128 + lane * 4;
-          // A token without a valid choice: NaN.
-          const float zero = (c.plan.bad[t >> 5] >> (t & 31)) & 1u ? __int_as_float(0x7fffffff) : 0.0f;
-          float4 y = make_float4(zero, zero, zero, zero);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 x = sums[warp - 2][i][lane];
-            y = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
-          }
-          *reinterpret_cast<uint2*>(a.y + static_cast<int64_t>(t) * a.d + col) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-        }
-        named_barrier(1, 128);
-      }
-    }
+    if (ok) sum_y(a, c.plan, reinterpret_cast<float4*>(ring), w.PD, true);   // (every copy into the ring has been used)
   }
   tc_fence_before();
   if (__syncthreads_or(!ok)) drain_pause();
