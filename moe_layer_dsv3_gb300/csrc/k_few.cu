@@ -50,7 +50,6 @@ constexpr int kSmemMax = 232448;
 constexpr int kSfCol = 256;                // TMEM: accumulators below, scales of the ring's stages from here on
 constexpr int kQueue = 4;                  // pieces on their way from the warp that takes them to the others
 constexpr int kUpPieces = 1, kDownPieces = 2;   // pieces of a CTA that K is cut for, where there are fewer
-constexpr int kPrefetch = 16384;           // bytes of a prefetch
 constexpr int kMinSteps = 2;               // fewest 128-wide steps of a part
 static_assert(kMaxT == 64, "a token is a bit of an expert's 64-bit mask");
 
@@ -66,9 +65,7 @@ struct FewArgs {
   float* logits;                           // [T][E]
   uint8_t* xq;                             // [64][d]
   uint8_t* xsf;                            // [d / 128] atoms
-  const uint8_t* w1;                       // weights
-  const uint8_t* w2;
-  const uint8_t* w1sf;                     // and their scales
+  const uint8_t* w1sf;                     // scales of the weights
   const uint8_t* w2sf;
   uint8_t* hq;                             // [rows][I], an expert's tokens one after another
   uint8_t* hsf;                            // [experts in use][I / 128] atoms
@@ -255,7 +252,7 @@ __global__ void __launch_bounds__(kRouteThreads) few_route_kernel(const __grid_c
 // ---------------------------------------------------------------- the experts in use
 // Which tokens chose which expert, made by every CTA for itself from the router's choice: a 64-bit mask of tokens per
 // expert, the experts in use in ascending order, and their tokens' rows one after another. A shared expert is number 0, and
-// expert e number e + n_shared: what is known to be used comes first.
+// expert e number e + n_shared.
 struct FewPlan {
   uint32_t mask[kMaxEp][2];
   uint16_t expert[kMaxEp];                 // of a slot
@@ -392,7 +389,11 @@ template <int IT>
 __device__ __noinline__ void sum_blocks(const FewArgs& a, const FewPlan& p, float4* sums_, int PD, bool real) {
   float4 (*sums)[4][32] = reinterpret_cast<float4 (*)[4][32]>(sums_);
   const int warp = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
-  const int cols = a.d >> 7, ctas = static_cast<int>(gridDim.x), picks = a.k + a.S;
+  // (copies: a reference into the kernel's parameters would be read again after every barrier)
+  const int d = a.d, k0 = a.k, picks = a.k + a.S;
+  const float* o = a.o;
+  __nv_bfloat16* out = a.y;
+  const int cols = d >> 7, ctas = static_cast<int>(gridDim.x);
   const int begin = static_cast<int>(blockIdx.x), units = real ? a.T * cols : begin + 1;
 #pragma unroll 1
   for (int u0 = begin; u0 < units; u0 += IT * ctas) {
@@ -407,10 +408,10 @@ __device__ __noinline__ void sum_blocks(const FewArgs& a, const FewPlan& p, floa
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
         const int j = warp + 4 * i;
-        const bool has = some && (j < a.k ? !bad : j < picks);
-        const int r = !has ? 0 : (j < a.k ? p.row[t * a.k + j] : t);                 // (the shared expert's rows are the first)
-        gate[n][i] = !has ? 0.0f : (j < a.k ? p.gate[t * a.k + j] : 1.0f);
-        src[n][i] = has ? reinterpret_cast<const float4*>(a.o + static_cast<int64_t>(r) * PD * a.d + col) : nullptr;
+        const bool has = some && (j < k0 ? !bad : j < picks);
+        const int r = !has ? 0 : (j < k0 ? p.row[t * k0 + j] : t);                 // (the shared expert's rows are the first)
+        gate[n][i] = !has ? 0.0f : (j < k0 ? p.gate[t * k0 + j] : 1.0f);
+        src[n][i] = has ? reinterpret_cast<const float4*>(o + static_cast<int64_t>(r) * PD * d + col) : nullptr;
         v[n][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
     }
@@ -422,7 +423,7 @@ __device__ __noinline__ void sum_blocks(const FewArgs& a, const FewPlan& p, floa
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
           x[n][i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (src[n][i] != nullptr) x[n][i] = ld_global_f4(src[n][i] + static_cast<int64_t>(k) * (a.d >> 2));
+          if (src[n][i] != nullptr) x[n][i] = ld_global_f4(src[n][i] + static_cast<int64_t>(k) * (d >> 2));
         }
       __syncwarp();                                        // all of them are issued before the first is added
 #pragma unroll
@@ -453,12 +454,13 @@ __device__ __noinline__ void sum_blocks(const FewArgs& a, const FewPlan& p, floa
         y = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
       }
       if (real && u < units)
-        *reinterpret_cast<uint2*>(a.y + static_cast<int64_t>(t) * a.d + col) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+        *reinterpret_cast<uint2*>(out + static_cast<int64_t>(t) * d + col) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
     }
     named_barrier(1, 128);
   }
 }
-// One block at once where there is no more than one a CTA: less code to fetch.
+// One block at once where there is no more than one a CTA: four at once cost 89 us instead of 80 for one token (more code to
+// fetch), and 446 instead of 453 for 64.
 __device__ __forceinline__ void sum_y(const FewArgs& a, const FewPlan& p, float4* sums, int PD, bool real) {
   if (a.T * (a.d >> 7) <= static_cast<int>(gridDim.x)) sum_blocks<1>(a, p, sums, PD, real);
   else sum_blocks<4>(a, p, sums, PD, real);
@@ -499,19 +501,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     tmem_alloc(&c.tmem, 512);
     tmem_relinquish();
-  }
-  // The shared expert's weights are read whatever the router chooses: on their way into L2 while it works.
-  if (a.S > 0 && warp == 0) {
-    const int64_t n1 = static_cast<int64_t>(a.d) * a.I * 2, n2 = n1 / 2, at1 = a.E * n1, at2 = a.E * n2;
-    auto fetch = [&](const uint8_t* p, int64_t n) {
-      for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 32 + lane) * kPrefetch; i < n; i += static_cast<int64_t>(gridDim.x) * 32 * kPrefetch)
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p + i), "r"(static_cast<uint32_t>(n - i < kPrefetch ? n - i : kPrefetch))
-                     : "memory");
-    };
-    fetch(a.w1 + at1, n1);
-    fetch(a.w1sf + at1 / 32, n1 / 32);
-    fetch(a.w2 + at2, n2);
-    fetch(a.w2sf + at2 / 32, n2 / 32);
   }
   if (warp >= 2 && warp < 6) {
     sum_y(a, c.plan, reinterpret_cast<float4*>(ring), 1, false);
@@ -910,13 +899,11 @@ extern "C" int moe_few_forward(const moe_config_t* cfg, const void* x, const voi
   a.y = static_cast<__nv_bfloat16*>(y);
   a.status = reinterpret_cast<int*>(base + L.status);
   const int sms = num_sms() < kMaxSms ? num_sms() : kMaxSms;
-  a.w1 = wq_ptr<uint8_t>(WL, w, MOE_WQ_W1F);
-  a.w2 = wq_ptr<uint8_t>(WL, w, MOE_WQ_W2F);
   a.w1sf = wq_ptr<uint8_t>(WL, w, MOE_WQ_W1F_SF);
   a.w2sf = wq_ptr<uint8_t>(WL, w, MOE_WQ_W2F_SF);
   CUtensorMap tw1, tw2, tx, th;
-  if (!make_tmap(&tw1, a.w1, static_cast<int64_t>(a.Ep) * 2 * a.I, a.d, 128, false) ||
-      !make_tmap(&tw2, a.w2, static_cast<int64_t>(a.Ep) * a.d, a.I, 128, false) ||
+  if (!make_tmap(&tw1, wq_ptr<uint8_t>(WL, w, MOE_WQ_W1F), static_cast<int64_t>(a.Ep) * 2 * a.I, a.d, 128, false) ||
+      !make_tmap(&tw2, wq_ptr<uint8_t>(WL, w, MOE_WQ_W2F), static_cast<int64_t>(a.Ep) * a.d, a.I, 128, false) ||
       !make_tmap(&tx, a.xq, kMaxT, a.d, 16, false) ||
       !make_tmap(&th, a.hq, static_cast<int64_t>(a.T) * (a.k + a.S) + 16, a.I, 16, false))
     return MOE_ERR_CUDA;
@@ -927,7 +914,9 @@ extern "C" int moe_few_forward(const moe_config_t* cfg, const void* x, const voi
     launch_kernel_after("few_route", kern, dim3(static_cast<unsigned>(blocks)), dim3(kRouteThreads), 9 * a.E * sizeof(float), s, a);
   };
   const int per = static_cast<int>(ceil_div(a.E, 32));     // experts a lane of the choosing warp
-  if (a.T == 1) {
+  // A row of Wr for one token, or two rows for eight: 121 and 126 us for the whole call at 2 tokens of 7168 columns and 64
+  // experts, 200 and 197 at 4 tokens, 453 and 446 at 64.
+  if (a.T <= 2) {
     if (per <= 2) route(few_route_kernel<1, 1, 2>, 1, 1);
     else if (per <= 4) route(few_route_kernel<1, 1, 4>, 1, 1);
     else if (per <= 8) route(few_route_kernel<1, 1, 8>, 1, 1);
