@@ -29,7 +29,7 @@
 // advance, in a kernel for each projection, left some SMs 15 % behind the others (HBM does
 // not serve all alike), and HBM idle for 9 us between the kernels: 106 us for one
 // token of 9 such experts, 403 for 16 tokens and 47 experts, 544 for 64 and 61, where the list takes
-// 77, 339 and 416: 5.3, 6.3 and 6.7 TB/s of the weights read.
+// 76, 330 to 339 and 416 to 425: 5.4, 6.4 and 6.6 TB/s of the weights read.
 #include <cudaTypedefs.h>
 
 #include "gemm.cuh"
@@ -44,12 +44,14 @@ constexpr int kMaxT = MOE_FEW_MAX_T;
 constexpr int kMaxEp = 513;                // experts, a shared one included
 constexpr int kMaxPicks = kMaxT * 8;       // routed (token, expert) pairs
 constexpr int kThreads = 224;
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 12;            // of the ring: 6 fit at 16 tokens, 5 at 64 (4 cost 1 to 2 %, 2 cost 10)
 constexpr int kTileBytes = 128 * 128;      // a weight tile: 128 rows x 128 values
 constexpr int kSmemMax = 232448;
 constexpr int kSfCol = 256;                // TMEM: accumulators below, scales of the ring's stages from here on
 constexpr int kQueue = 4;                  // pieces on their way from the warp that takes them to the others
-constexpr int kUpPieces = 1, kDownPieces = 2;   // pieces of a CTA that K is cut for, where there are fewer
+// Pieces of a CTA that K is cut for, where there are fewer. More of them (4 and 8) balance better and cost the joining of
+// parts: 83.1 and 80.5 us for one token of 9 wide experts, 58.0 and 55.9 for 5 tokens of 38 narrow ones, nothing elsewhere.
+constexpr int kUpPieces = 1, kDownPieces = 2;
 constexpr int kMinSteps = 2;               // fewest 128-wide steps of a part
 static_assert(kMaxT == 64, "a token is a bit of an expert's 64-bit mask");
 
@@ -384,7 +386,7 @@ __device__ __forceinline__ Piece piece_of(const Work& w, int id) {
 // y from the rows of o, by the epilogue's four warps: blocks of 128 columns of a token, IT at once. A warp adds every fourth of the
 // token's experts, and the four sums (in `sums`, shared memory) are added in order.
 // Not inlined, so that a first call which only goes through it (`real` false: it reads and writes no global memory) fetches
-// the code while the router works: at the end of the list, one miss after another, that took 6 of few_small's 54 us.
+// the code while the router works: at the end of the list, one miss after another, that took 6 of 54 us at 5 tokens.
 template <int IT>
 __device__ __noinline__ void sum_blocks(const FewArgs& a, const FewPlan& p, float4* sums_, int PD, bool real) {
   float4 (*sums)[4][32] = reinterpret_cast<float4 (*)[4][32]>(sums_);

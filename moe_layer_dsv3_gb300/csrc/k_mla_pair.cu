@@ -458,8 +458,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int blk = q >> 1;                                // this thread's tokens: 32 sub .. of this block
     const int hl = (q & 1) * 32 + lane;                    // and head of the CTA
     const int head0 = static_cast<int>(rank) * a.hg;       // first head of the CTA
-    // heads that a CTA whose first is h0 has of an item
-    auto heads_of = [&](const Item& it, int h0) { return max(0, it.rows - h0 < a.hg ? it.rows - h0 : a.hg); };
+    // heads that a CTA whose first is h0 has of an item (a sequence's last row group may be small)
+    auto heads_of = [&](const Item& it, int h0) {
+      const int n = it.rows - h0 < a.hg ? it.rows - h0 : a.hg;
+      return TREE && n < 0 ? 0 : n;
+    };
     const int tl = sub * 128 + q * 32 + lane;              // a head's four threads: tl with bits 6 and 7 free
     const bool first = blk == 0 && sub == 0;               // the one that speaks for the head
     const uint32_t se0 = pair::map_rank(smem_u32(&c.se), 0), pf0 = pair::map_rank(smem_u32(&c.pf), 0);

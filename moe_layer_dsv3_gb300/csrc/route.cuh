@@ -54,8 +54,9 @@ __device__ __forceinline__ void warp_best(float& v, int& e) {
   }
 }
 
-// The best pair of a warp, in every lane's e, by shuffles or by warp-wide integer reductions: the same choice among numbers. The
-// reductions take a third of the latency, which is what a kernel with few tokens waits for.
+// The best pair of a warp, in every lane's e, by shuffles or by warp-wide integer reductions: the same choice among numbers. A
+// kernel with few tokens waits for the choice: with reductions, in a loop, compiled for the experts a lane has, it takes 3 us
+// from the last logit, where shuffles unrolled for 512 experts took 8.6.
 struct BestByShuffles {
   static constexpr int kRounds = 8;        // selection rounds unrolled
   static __device__ __forceinline__ void of(float& v, int& e) { warp_best(v, e); }
