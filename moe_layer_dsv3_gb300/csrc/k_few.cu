@@ -44,7 +44,7 @@ constexpr int kMaxT = MOE_FEW_MAX_T;
 constexpr int kMaxEp = 513;                // experts, a shared one included
 constexpr int kMaxPicks = kMaxT * 8;       // routed (token, expert) pairs
 constexpr int kThreads = 224;
-constexpr int kMaxStages = 12;            // of the ring: 6 fit at 16 tokens, 5 at 64 (4 cost 1 to 2 %, 2 cost 10)
+constexpr int kMaxStages = 6;             // of the ring: 6 fit at 16 tokens, 5 at 64 (4 cost 1 to 2 %, 2 cost 10)
 constexpr int kTileBytes = 128 * 128;      // a weight tile: 128 rows x 128 values
 constexpr int kSmemMax = 232448;
 constexpr int kSfCol = 256;                // TMEM: accumulators below, scales of the ring's stages from here on
@@ -93,15 +93,6 @@ __device__ __forceinline__ int cut_at(int steps, int i, int n) {
   return at < steps ? at : steps;
 }
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int site) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, site));
 }
@@ -120,14 +111,6 @@ __device__ __forceinline__ bool epilogue_or(bool flag) {
 }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// After a wait that gave up, products and copies that nobody waits for may be under way.
-__device__ __forceinline__ void drain_pause() {
-  const uint64_t t0 = global_timer_ns();
-#pragma unroll 1
-  while (global_timer_ns() - t0 < 100000) {
-  }
-}
 
 // One column of two accumulators, and four.
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
@@ -269,12 +252,25 @@ struct FewPlan {
 
 __device__ __forceinline__ void make_plan(const FewArgs& a, FewPlan& p, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // This thread's picks: expert and gate, read together.
+  constexpr int kPicks = (kMaxPicks + kThreads - 1) / kThreads;
+  const int n = a.T * a.k;
+  int pick[kPicks];
+  float gate[kPicks];
+#pragma unroll
+  for (int j = 0; j < kPicks; ++j) {
+    const int i = tid + j * kThreads;
+    pick[j] = i < n ? ld_global_s32(a.idx + i) : 0;
+    gate[j] = i < n ? __int_as_float(ld_global_s32(reinterpret_cast<const int*>(a.w + i))) : 0.0f;
+  }
   for (int i = tid; i < a.Ep; i += kThreads) p.mask[i][0] = p.mask[i][1] = 0;
   if (tid < 2) p.bad[tid] = 0;
   __syncthreads();
-  const int n = a.T * a.k;
-  for (int i = tid; i < n; i += kThreads) {
-    const int e = ld_global_s32(a.idx + i), t = i / a.k;
+#pragma unroll
+  for (int j = 0; j < kPicks; ++j) {
+    const int i = tid + j * kThreads;
+    if (i >= n) break;
+    const int e = pick[j], t = i / a.k;
     const bool ok = e >= 0 && e < a.E;
     atomicOr(ok ? &p.mask[e + a.S][t >> 5] : &p.bad[t >> 5], 1u << (t & 31));
     if (!ok && report) report_error(a.status, kErrBounds, 200);
@@ -318,13 +314,16 @@ __device__ __forceinline__ void make_plan(const FewArgs& a, FewPlan& p, bool rep
     p.first[all >> 16] = static_cast<uint16_t>(all & 0xffffu);
   }
   __syncthreads();
-  for (int i = tid; i < n; i += kThreads) {
-    const int e = ld_global_s32(a.idx + i), t = i / a.k;
+#pragma unroll
+  for (int j = 0; j < kPicks; ++j) {
+    const int i = tid + j * kThreads;
+    if (i >= n) break;
+    const int e = pick[j], t = i / a.k;
     if (e < 0 || e >= a.E) continue;
     const uint32_t* m = p.mask[e + a.S];
     const uint32_t below = t < 32 ? __popc(m[0] & ((1u << t) - 1u)) : __popc(m[0]) + __popc(m[1] & ((1u << (t - 32)) - 1u));
     p.row[i] = static_cast<uint16_t>(p.first[p.slot[e + a.S]] + below);
-    p.gate[i] = __int_as_float(ld_global_s32(reinterpret_cast<const int*>(a.w + i)));
+    p.gate[i] = gate[j];
   }
   __syncthreads();
 }

@@ -264,17 +264,6 @@ __device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint2* 
       : "memory");
 }
 
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
 // mbar_wait in few instructions. Seven warps run five different loops here, and
 // with mbar_wait's unrolled polls at every wait the kernel was 150 KB of code:
 // its instruction-cache misses set the pace of every warp.
@@ -293,16 +282,6 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int* st
 // bar_wait by a whole warp: the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int site) {
   return __all_sync(0xffffffffu, bar_wait(bar, parity, status, site));
-}
-
-// How long a CTA whose wait gave up stays before it leaves: copies, products and words of the other CTA that nobody
-// waits for any more take a few microseconds.
-constexpr uint64_t kDrainNs = 100000;
-__device__ __forceinline__ void drain_pause() {
-  const uint64_t t0 = global_timer_ns();
-#pragma unroll 1
-  while (global_timer_ns() - t0 < kDrainNs) {
-  }
 }
 
 // Barrier over the NT softmax threads that also gives the OR of their flags.

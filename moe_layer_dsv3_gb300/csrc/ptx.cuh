@@ -322,6 +322,27 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// How long a CTA whose wait gave up stays before it leaves: copies, products and words of the other CTA that nobody
+// waits for any more take a few microseconds.
+constexpr uint64_t kDrainNs = 100000;
+__device__ __forceinline__ void drain_pause() {
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  while (global_timer_ns() - t0 < kDrainNs) {
+  }
+}
+
 // ----------------------------------------------------------------- CTA pairs (cluster of 2)
 // The CTA-pair MMA (tcgen05 .cta_group::2) computes a 256-row tile on two SMs:
 // the even CTA of the cluster issues every MMA, each CTA holds half of A and

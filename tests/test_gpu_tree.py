@@ -217,3 +217,71 @@ def test_captured_and_replayed(lib):
         s.check(s.att.tree_out, s.att.tree_lse)
         s.rows = Setup([200, 90, 64], 5, 16, seed=9).rows
     assert s.att.status() == (0, 0)
+
+
+def test_pages_past_32_bits(lib):
+    """Drafted tokens whose pages lie past 2^32 bytes and 2^31 elements of the cache."""
+    from moe_layer_dsv3_gb300.attention import LatentAttention
+    latent, rope, page = 512, 64, 64
+    pool = 2 ** 31 // (page * (latent + rope)) + 40        # 4.3 GB
+    g = torch.Generator(device="cuda").manual_seed(1)
+    cache = torch.empty(pool, page, latent + rope, dtype=torch.bfloat16, device="cuda")
+    lens, n, H = [130, 64, 200], 3, 16
+    table = torch.full((3, 5), -1, dtype=torch.int32)
+    rows = []
+    at = pool - 1
+    for b, L in enumerate(lens):
+        r = torch.randn(L, latent + rope, generator=g, device="cuda").to(torch.bfloat16)
+        for i in range(-(-L // page)):
+            table[b, i] = at
+            part = r[i * page:(i + 1) * page]
+            cache[at].fill_(float("nan"))
+            cache[at, :len(part)] = part
+            at -= 1
+        rows.append(r)
+    s = Setup.__new__(Setup)
+    s.lens, s.n, s.H, s.latent, s.rope, s.scale = lens, n, H, latent, rope, 192 ** -0.5
+    s.drafts, s.masks, s.rows = [3, 2, 3], [[1, 3, 5]] * 3, rows
+    s.cache, s.table, s.tree = cache, table.cuda(), words(s.masks)
+    s.lens_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    s.drafts_t = torch.tensor(s.drafts, dtype=torch.int32, device="cuda")
+    s.q = torch.randn(3, n, H, latent + rope, generator=g, device="cuda").to(torch.bfloat16)
+    s.att = LatentAttention(3, H, latent, rope, page, pool, 5, s.scale, drafts=n)
+    s.check()
+
+
+def test_many_row_groups(lib):
+    """The most rows a sequence can have (64 tokens of 128 heads: 64 groups of 128), and groups that are not full."""
+    Setup([70, 66], 64, 128, seed=10).check()
+    Setup([140], 43, 3, seed=11).check()                   # 129 rows: groups of 65 and 64
+    Setup([90, 200], 37, 7, seed=12).check()               # 259 rows: 87, 87 and 85
+    Setup([90, 200], 13, 5, latent=384, seed=13).check()   # 65 rows in groups of up to 64
+
+
+def test_refused_tensors(lib):
+    s = Setup([70, 66], 4, 4, seed=14)
+    f = s.att.decode_tree
+    bad = lambda *a, **k: pytest.raises(lib.MoeError, f, *a, **k)
+    ok = (s.q, s.cache, s.table, s.lens_t)
+    bad(s.q.float(), *ok[1:])
+    bad(s.q[:1], *ok[1:])
+    bad(s.q[..., :512], *ok[1:])
+    bad(s.q.flatten(1, 2), *ok[1:])
+    bad(s.q.transpose(1, 2).contiguous().transpose(1, 2), *ok[1:])         # a token's heads apart, tokens between them
+    bad(*ok, tree=s.tree.int())
+    bad(*ok, tree=s.tree[:, :3])
+    bad(*ok, drafts=s.drafts_t.long())
+    bad(*ok, out=torch.empty(2, 4, 4, 512, device="cuda"))
+    bad(torch.zeros(2, 5, 4, 576, dtype=torch.bfloat16, device="cuda"), *ok[1:])      # more drafted tokens than the buffers hold
+    with pytest.raises(lib.MoeError):
+        s.att.decode_tree(torch.zeros(2, 65, 4, 576, dtype=torch.bfloat16, device="cuda"), *ok[1:],
+                          out=torch.empty(2, 65, 4, 512, dtype=torch.bfloat16, device="cuda"),
+                          lse=torch.empty(2, 65, 4, device="cuda"))
+
+
+@pytest.mark.parametrize("lens,n,H,latent,page", [
+    ([30000], 3, 16, 512, 64), ([26000], 4, 32, 256, 64), ([12000, 3, 9000], 5, 7, 384, 16), ([700 + 13 * i for i in range(40)], 7, 18, 512, 64),
+    ([9000 + i for i in range(7)], 2, 100, 512, 128), ([20001], 9, 40, 512, 48)])
+def test_long_lists(lib, lens, n, H, latent, page):
+    """Sequences cut into long lists of pieces, and many short ones, in one and in several row groups."""
+    Setup(lens, n, H, latent, page=page, seed=15).check()
