@@ -29,7 +29,7 @@
 // advance, in a kernel for each projection, left some SMs 15 % behind the others (HBM does
 // not serve all alike), and HBM idle for 9 us between the kernels: 106 us for one
 // token of 9 such experts, 403 for 16 tokens and 47 experts, 544 for 64 and 61, where the list takes
-// 76, 330 to 339 and 416 to 425: 5.4, 6.4 and 6.6 TB/s of the weights read.
+// 75, 320 to 330 and 413 to 424: 5.5, 6.6 and 6.6 TB/s of the weights read.
 #include <cudaTypedefs.h>
 
 #include "gemm.cuh"
