@@ -134,7 +134,7 @@ __device__ __forceinline__ int atom_add_acq_rel(int* p, int v) {
 // fp32 on the CUDA cores: two rounds of loads at 7168 columns, where the tensor cores would wait for
 // one CTA's chain of 112 stages. One token, 64 experts: logits after 2.0 us, the last CTA found after 3.2, the choice
 // written after 5.3. The CTA that finishes a group of tokens last
-// chooses for them. Further CTAs quantise x and clear the counters of the kernels that follow.
+// chooses for them. Further CTAs quantise x and clear the counters of the kernel that follows.
 constexpr int kRouteThreads = 256;
 constexpr int kRowWarps = kRouteThreads / 32;
 
