@@ -18,12 +18,15 @@
 // for 512 of which some grow and some shrink, 7 for 37 prompts of 524288 tokens; called from
 // Python the host's 7 to 8 us bound it.
 #include "moe_internal.h"
+#include "pages_sums.h"
 #include "prof.h"
 #include "ptx.cuh"
 
 namespace moe {
 
 namespace {
+
+using pages::Sums;
 
 constexpr int kThreads = 256;
 constexpr int kTokens = 4;                 // consecutive tokens of a thread: their stores are 16 bytes wide
@@ -43,18 +46,6 @@ struct PagesArgs {
   int32_t* slot;
   int32_t* starts;
   int* ws;                                 // {code, site, -, CTAs done}
-};
-
-// Sums over sequences. Lengths may be anything, so a sum stays at kMost once it gets there: past every buffer, and two of
-// them still fit in 32 bits.
-constexpr int kMost = 1 << 30;
-struct Sums {
-  int add, grow, drop;
-  __device__ __forceinline__ void operator+=(const Sums& o) {
-    add = min(add + o.add, kMost);
-    grow = min(grow + o.grow, kMost);
-    drop = min(drop + o.drop, kMost);
-  }
 };
 
 // Index of the sequence that holds number i: the largest b with first[b] <= i (first[n] > i).
@@ -89,16 +80,12 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
     len[b] = n;
     want[b] = m;
   }
-  auto pages_of = [&](int n) { return (n + a.page - 1) / a.page; };   // (cap + page is below 2^31)
+  auto pages_of = [&](int n) { return pages::pages_of(n, a.page); };
   bad = __syncthreads_or(bad);
   Sums mine{0, 0, 0};
   const int per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  auto sums_of = [&](int b) {
-    const int n = len[b], m = want[b], o = pages_of(n), w = pages_of(m);
-    return Sums{m > n ? min(m - n, kMost) : 0, max(w - o, 0), max(o - w, 0)};
-  };
   if (!bad)
-    for (int b = b0; b < b1; ++b) mine += sums_of(b);
+    for (int b = b0; b < b1; ++b) mine += pages::sums_of(len[b], want[b], a.page);
   Sums at = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -107,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
     if (lane >= o) at += v;
   }
   if (lane == 31) scan[warp] = at;
-  // (before this thread's run, within its warp; only used when no sum has reached kMost)
+  // (before this thread's run, within its warp; only used when no sum was cut)
   at = Sums{at.add - mine.add, at.grow - mine.grow, at.drop - mine.drop};
   __syncthreads();
   Sums all{0, 0, 0};
@@ -117,20 +104,18 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
     all += scan[i];
   }
   // A step that cannot be made as a whole is not made at all.
-  int code = MOE_OK;
-  if (bad || all.add > a.max_new || all.drop > a.num_pages - count) code = MOE_ERR_BOUNDS;
-  else if (all.grow > count + all.drop) code = MOE_ERR_PAGES;
+  const int code = bad ? MOE_ERR_BOUNDS : pages::step_code(all, count, a.num_pages, a.max_new);
   if (code != MOE_OK) {
     if (blockIdx.x == 0 && tid == 0) report_error(a.ws, code, 220);
     at = all = Sums{0, 0, 0};
   }
   for (int b = b0; b < b1; ++b) {
-    starts[b] = at.add;
-    taken[b] = at.grow;
-    left[b] = at.drop;
-    if (code == MOE_OK) at += sums_of(b);
+    starts[b] = static_cast<int>(at.add);
+    taken[b] = static_cast<int>(at.grow);
+    left[b] = static_cast<int>(at.drop);
+    if (code == MOE_OK) at += pages::sums_of(len[b], want[b], a.page);
   }
-  const int N = all.add, G = all.grow, F = all.drop;
+  const int N = static_cast<int>(all.add), G = static_cast<int>(all.grow), F = static_cast<int>(all.drop);
   if (tid == 0) {
     starts[a.B] = N;
     taken[a.B] = G;
@@ -226,7 +211,7 @@ extern "C" int moe_pages_update(int batch, int page_size, int num_pages, int max
                                 int32_t* starts, void* ws, moe_stream_t stream) {
   const int64_t lim = (1LL << 31) - 1;
   if (batch < 0 || batch > MOE_PAGES_MAX_BATCH || page_size < 1 || num_pages < 1 || max_pages < 1 || max_new < 0 ||
-      max_new >= kMost || num_pages >= kMost)
+      static_cast<uint32_t>(max_new) >= pages::kMost || static_cast<uint32_t>(num_pages) >= pages::kMost)
     return MOE_ERR_INVALID_ARG;
   if (static_cast<int64_t>(num_pages) * page_size >= lim || static_cast<int64_t>(max_pages + 1LL) * page_size >= lim)
     return MOE_ERR_INVALID_ARG;
