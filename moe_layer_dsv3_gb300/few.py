@@ -26,6 +26,8 @@ class FewTokenMoE:
             wq = torch.zeros(n, dtype=torch.uint8, device=dev)
         else:
             check_tensor("wq", wq, torch.uint8, (n,))
+            if wq.device != self.ws.device:
+                raise MoeError("wq: weights of %s for a layer on %s" % (wq.device, self.ws.device), MOE_ERR_INVALID_ARG)
         self.wq = wq
         self.topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
         self.topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
@@ -40,6 +42,7 @@ class FewTokenMoE:
                 raise MoeError("ws_gu, ws_d: the shared expert's weights are wanted", MOE_ERR_INVALID_ARG)
             check_tensor("ws_gu", ws_gu, torch.bfloat16, (self.S, 2 * self.I, self.d))
             check_tensor("ws_d", ws_d, torch.bfloat16, (self.S, self.d, self.I))
+        check_device(w_gu, w_d, *((ws_gu, ws_d) if self.S else ()), self.wq)
         moe_quantize_weights(self.cfg, w_gu.data_ptr(), w_d.data_ptr(), ws_gu.data_ptr() if self.S else 0,
                              ws_d.data_ptr() if self.S else 0, self.wq.data_ptr(), stream)
 
@@ -56,7 +59,7 @@ class FewTokenMoE:
         if y is None:
             y = self.y[:t]
         check_tensor("y", y, torch.bfloat16, (t, self.d))
-        check_device(x, w_router, bias, y, self.ws)
+        check_device(x, w_router, bias, y, self.wq, self.ws)
         cfg = self._cfgs.get(t)
         if cfg is None:
             cfg = self._cfgs[t] = config(t, *self._shape)
