@@ -6,6 +6,8 @@ a block table, each with a cache of its own).
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import (MOE_ERR_INVALID_ARG, MoeError, mla_config, moe_mla_append, moe_mla_decode, moe_mla_decode_tree,
@@ -80,15 +82,16 @@ class LatentAttention:
 
         q [batch][n][heads][latent + rope]: dense rows, any pitch, a token's heads as far apart as its neighbours' (q of
         shape [batch][n * heads][..], viewed). tree int64 [batch][n]: bit j of word i: token i sees drafted token j (None: a
-        chain). drafts int32 [batch]: drafted tokens of each sequence (None: n each)."""
-        out = self.tree_out if out is None else out
-        lse = self.tree_lse if lse is None else lse
+        chain). drafts int32 [batch]: drafted tokens of each sequence (None: n each). out and lse default to tree_out and
+        tree_lse: with fewer tokens than those hold, to [batch][n].. lying dense at their front."""
         row = self.latent + self.rope
         n = q.shape[1] if q.dim() == 4 else 0
         if not q.is_cuda or q.dtype is not torch.bfloat16 or n < 1 or q.shape != (self.batch, n, self.heads, row) or \
                 (q.numel() and q.stride(3) != 1):
             raise MoeError("q: a CUDA bfloat16 tensor of shape %s with dense rows is wanted" %
                            ((self.batch, "n", self.heads, row),), MOE_ERR_INVALID_ARG)
+        out = self._front(self.tree_out, n) if out is None else out
+        lse = self._front(self.tree_lse, n) if lse is None else lse
         # the stride of a dimension of one is arbitrary
         sh = q.stride(2) if self.heads > 1 else (q.stride(1) if n > 1 else row)
         if self.heads > 1 and n > 1 and q.stride(1) != self.heads * sh:
@@ -107,6 +110,14 @@ class LatentAttention:
                             drafts.data_ptr() if drafts is not None else 0, tree.data_ptr() if tree is not None else 0,
                             out.data_ptr(), lse.data_ptr(), self.ws.data_ptr(), stream)
         return out
+
+    @staticmethod
+    def _front(t, n):
+        """The front of the buffer t [batch][drafts].. as [batch][n].. (t itself where it does not hold as much)."""
+        if n >= t.shape[1]:
+            return t
+        shape = (t.shape[0], n, *t.shape[2:])
+        return t.view(-1)[:math.prod(shape)].view(shape)
 
     def status(self, clear=True, stream=0):
         return moe_mla_status(self.cfg, self.ws.data_ptr(), clear, stream)
