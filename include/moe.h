@@ -539,7 +539,10 @@ MOE_API int moe_mla_status(const moe_mla_config_t* cfg, void* ws, int* code, int
  * [0, max_pages * page_size], more than max_new new tokens, a count outside [0, num_pages],
  * more pages left than the pool has room for: MOE_ERR_BOUNDS) changes nothing and writes
  * no tokens; the status tells. A page out of range in the table or the pool sets the
- * status to MOE_ERR_BOUNDS; its tokens get slot -1. Pages must not be shared by sequences
+ * status to MOE_ERR_BOUNDS in every step that reads it; its tokens get slot -1. Such a step is
+ * made all the same, and the entry moves as it is: left, it goes on the pool, and taken, into
+ * the table. So after this status both hold what the caller wrote there, and have
+ * to be put right before the entry's next use. Pages must not be shared by sequences
  * that may leave them. Everything is read on the device, so a captured call replays.
  * batch 0..MOE_PAGES_MAX_BATCH; num_pages and max_new below 2^30, num_pages * page_size and
  * (max_pages + 1) * page_size below 2^31 - 1; seq, pos, slot and ws on 16-byte boundaries. ws: 16 bytes, zero before the

@@ -38,3 +38,29 @@ def test_sums_past_32_bits_are_refused(lib, page, lens):
     plan.update(now, i32([1] + [0] * (B - 1)), table, free, count)
     torch.cuda.synchronize()
     assert plan.status() == (0, 0) and count.tolist() == [4] and table[0, 0].item() == 5 and plan.slot[0].item() == 5 * page
+
+
+def test_bad_pages_stay_and_are_told_again(lib):
+    """A page out of range moves as it is, from the table to the pool and back, and every step that meets it says so."""
+    from moe_layer_dsv3_gb300.pages import PagePlan
+    for bad in (6, -1, 2 ** 31 - 1, -2 ** 31):
+        plan = PagePlan(2, 8, 6, 4, 32)
+        table, free, count, lens = plan.new_pool()
+
+        def step(*target):
+            plan.update(lens, i32(target), table, free, count)
+            torch.cuda.synchronize()
+            assert lens.tolist() == list(target)
+            return plan.status()
+        assert step(24, 3) == (0, 0) and table[0].tolist() == [0, 1, 2, -1] and table[1].tolist() == [3, -1, -1, -1]
+        table[0, 2] = bad
+        assert step(9, 3)[0] == lib.MOE_ERR_BOUNDS           # left by a sequence that shrinks: the pool holds it
+        assert count.tolist() == [3] and free.tolist()[:3] == [5, 4, bad]
+        assert step(9, 3) == (0, 0)                          # a step that does not meet it
+        assert step(9, 20)[0] == lib.MOE_ERR_BOUNDS          # popped by the other sequence: the table holds it
+        assert table[1].tolist() == [3, bad, 4, -1] and count.tolist() == [1]
+        # the tokens of that page have no row, the others have theirs
+        assert plan.slot.tolist()[:17] == [3 * 8 + i for i in range(3, 8)] + [-1] * 8 + [4 * 8 + i for i in range(4)]
+        assert step(9, 20) == (0, 0)
+        table[1, 1] = 2                                      # mended in the table, it serves again
+        assert step(9, 0) == (0, 0) and sorted(free.tolist()[:4]) == [2, 3, 4, 5]
