@@ -472,7 +472,7 @@ MOE_API int moe_mla_append(const moe_mla_config_t* cfg, int n, const void* kv, i
 
 /* Attention of one new token a sequence over its cached tokens.
  *   q: bf16, element (b, h, c) at b * q_stride_b + h * q_stride_h + c, c < latent + rope
- *      (strides in elements, multiples of 8).
+ *      (strides in elements, multiples of 8, latent + rope at least: sequences may share rows).
  *   seq_lens int32 [batch] (device): tokens of each sequence, the new one included.
  *   out bf16 [batch][heads][latent] = sum_j p_j k_j[0:latent], p = softmax over
  *      j < seq_lens[b] of softmax_scale q . k_j.
@@ -497,7 +497,8 @@ MOE_API int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_t q
  * sees all tokens before the drafted ones and those drafted tokens that its mask names.
  *   drafts: most drafted tokens of a sequence, 1..MOE_MLA_MAX_DRAFTS.
  *   q: bf16, element (b, i, h, c) of drafted token i at b * q_stride_b +
- *      (i * heads + h) * q_stride_h + c (strides in elements, multiples of 8).
+ *      (i * heads + h) * q_stride_h + c (strides in elements, multiples of 8, latent + rope
+ *      at least: sequences may share rows).
  *   seq_lens int32 [batch]: tokens of each sequence, the drafted ones included.
  *   draft_lens int32 [batch]: drafted tokens of each sequence, or NULL: `drafts` each
  *      (0 of an empty sequence).

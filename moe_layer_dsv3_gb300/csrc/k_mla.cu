@@ -943,13 +943,13 @@ int decode(const moe_mla_config_t* cfg, MlaArgs a, const void* q, int64_t q_stri
 
 // What the two calls refuse alike.
 int refuse_decode(const moe_mla_config_t* cfg, const void* q, int64_t q_stride_b, int64_t q_stride_h, const void* cache,
-                  const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse, void* ws, int64_t least_b) {
+                  const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse, void* ws) {
   const int row = cfg->latent + cfg->rope;
   if (cache == nullptr || ws == nullptr) return MOE_ERR_INVALID_ARG;
   if (cfg->batch > 0 && (q == nullptr || block_table == nullptr || seq_lens == nullptr || out == nullptr))
     return MOE_ERR_INVALID_ARG;
-  // strides in elements; a TMA dimension's pitch is below 2^40 bytes
-  if (q_stride_h < row || q_stride_b < least_b || q_stride_h % 8 || q_stride_b % 8 || q_stride_h >= (1LL << 38) ||
+  // strides in elements; a TMA dimension's pitch is below 2^40 bytes. (Sequences may share rows of q: it is only read.)
+  if (q_stride_h < row || q_stride_b < row || q_stride_h % 8 || q_stride_b % 8 || q_stride_h >= (1LL << 38) ||
       q_stride_b >= (1LL << 38))
     return MOE_ERR_INVALID_ARG;
   if (mis(q, 16) || mis(cache, 16) || mis(out, 16) || mis(ws, 16) || mis(lse, 4) || mis(block_table, 4) || mis(seq_lens, 4))
@@ -1014,7 +1014,7 @@ extern "C" int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_
                               const void* cache, const int32_t* block_table, const int32_t* seq_lens, void* out,
                               float* lse, void* ws, moe_stream_t stream) {
   if (int r = validate_mla(cfg)) return r;
-  if (int r = refuse_decode(cfg, q, q_stride_b, q_stride_h, cache, block_table, seq_lens, out, lse, ws, cfg->latent + cfg->rope))
+  if (int r = refuse_decode(cfg, q, q_stride_b, q_stride_h, cache, block_table, seq_lens, out, lse, ws))
     return r;
   if (!arch_ok()) return MOE_ERR_UNSUPPORTED_ARCH;
   if (cfg->batch == 0) return MOE_OK;
@@ -1031,7 +1031,7 @@ extern "C" int moe_mla_decode_tree(const moe_mla_config_t* cfg, int drafts, cons
                                    moe_stream_t stream) {
   if (int r = validate_mla(cfg)) return r;
   if (drafts < 1 || drafts > MOE_MLA_MAX_DRAFTS || mis(draft_lens, 4) || mis(tree, 8)) return MOE_ERR_INVALID_ARG;
-  if (int r = refuse_decode(cfg, q, q_stride_b, q_stride_h, cache, block_table, seq_lens, out, lse, ws, cfg->latent + cfg->rope))
+  if (int r = refuse_decode(cfg, q, q_stride_b, q_stride_h, cache, block_table, seq_lens, out, lse, ws))
     return r;
   // A sequence's rows in groups that one worker takes: up to 128 where the pair form does, else up to 64. Pairs also where they are
   // not full: 48 x ~8192 tokens with 80 rows take 109 us on pairs and 156 in two groups of 40 on single CTAs.

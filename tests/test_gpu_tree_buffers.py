@@ -58,3 +58,32 @@ def test_no_sequences(lib):
     i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
     out = att.decode_tree(torch.zeros(0, 5, 4, 576, dtype=torch.bfloat16, device="cuda"), att.new_cache(), i32(0, 1), i32(0))
     assert out.shape == (0, 5, 4, 512)
+
+
+@pytest.mark.parametrize("H,latent", [(4, 512), (20, 512), (16, 384)])
+def test_sequences_that_share_rows_of_q(lib, H, latent):
+    """A batch stride of one head: sequence b's rows are those of the first one, b heads on."""
+    lens, n = [70, 200, 64, 3], 3
+    s = Setup(lens, n, H, latent, seed=31)
+    row = latent + s.rope
+    rows = torch.randn(n * H + len(lens) - 1, row, device="cuda").to(torch.bfloat16)
+    s.q = rows.as_strided((len(lens), n, H, row), (row, H * row, row, 1))
+    s.check()
+
+
+@pytest.mark.parametrize("H,latent", [(4, 512), (20, 512), (16, 384)])
+def test_heads_farther_apart_than_sequences(lib, H, latent):
+    """q with the sequences inside: a batch stride of one row, heads a batch apart."""
+    lens, n = [70, 200, 64, 3, 1], 3
+    s = Setup(lens, n, H, latent, seed=32)
+    row, B = latent + s.rope, len(lens)
+    inner = s.q.flatten(1, 2).transpose(0, 1).contiguous()                  # [n * H][B][row]
+    q = inner.as_strided((B, n, H, row), (row, H * B * row, B * row, 1))
+    assert torch.equal(q, s.q)
+    s.check(*s.run(q=q))
+    one = Setup(lens, 1, H, latent, masks=[[1]] * B, seed=33)
+    out, lse = one.run()
+    inner = one.q[:, 0].transpose(0, 1).contiguous()
+    got = one.att.decode(inner.transpose(0, 1), one.cache, one.table, one.lens_t)
+    torch.cuda.synchronize()
+    assert torch.equal(got, out[:, 0]) and torch.equal(one.att.lse, lse[:, 0])
