@@ -32,6 +32,7 @@
 // 75, 320 to 330 and 413 to 424: 5.5, 6.6 and 6.6 TB/s of the weights read.
 #include <cudaTypedefs.h>
 
+#include "few_pieces.h"
 #include "gemm.cuh"
 #include "prof.h"
 #include "route.cuh"
@@ -39,6 +40,9 @@
 namespace moe {
 
 namespace {
+
+using few::Piece;
+using few::Work;
 
 constexpr int kMaxT = MOE_FEW_MAX_T;
 constexpr int kMaxEp = 513;                // experts, a shared one included
@@ -49,10 +53,6 @@ constexpr int kTileBytes = 128 * 128;      // a weight tile: 128 rows x 128 valu
 constexpr int kSmemMax = 232448;
 constexpr int kSfCol = 256;                // TMEM: accumulators below, scales of the ring's stages from here on
 constexpr int kQueue = 4;                  // pieces on their way from the warp that takes them to the others
-// Pieces of a CTA that K is cut for, where there are fewer. More of them (4 and 8) balance better and cost the joining of
-// parts: 83.1 and 80.5 us for one token of 9 wide experts, 58.0 and 55.9 for 5 tokens of 38 narrow ones, nothing elsewhere.
-constexpr int kUpPieces = 1, kDownPieces = 2;
-constexpr int kMinSteps = 2;               // fewest 128-wide steps of a part
 static_assert(kMaxT == 64, "a token is a bit of an expert's 64-bit mask");
 
 struct FewArgs {
@@ -79,19 +79,6 @@ struct FewArgs {
   __nv_bfloat16* y;
   int* status;
 };
-
-// Parts that K (`steps` steps) of `units` units is cut into, so that each of `ctas` CTAs gets `want` pieces.
-__host__ __device__ __forceinline__ int parts_of(int units, int steps, int ctas, int want) {
-  const int most = steps / kMinSteps > 1 ? steps / kMinSteps : 1;
-  const int n = (ctas * want + units - 1) / units;
-  return n < most ? n : most;
-}
-
-// First step of part i of n: an even one, since two steps of a row (256 bytes) come from HBM together.
-__device__ __forceinline__ int cut_at(int steps, int i, int n) {
-  const int at = ((steps + 1) >> 1) * i / n * 2;
-  return at < steps ? at : steps;
-}
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, int site) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, site));
@@ -352,37 +339,6 @@ struct Stage {
   }
 };
 
-// The list of pieces.
-struct Work {
-  int KA, KI, NB, RP, slots;               // steps of d and of I, blocks of 256 up and of 256 down rows, experts in use
-  int PU, PD, nup, total;                  // parts, pieces
-};
-struct Piece {
-  bool up;
-  int s, b, part, k0, k1;                  // expert slot, block of rows, part of K, its steps
-};
-__device__ __forceinline__ Piece piece_of(const Work& w, int id) {
-  Piece p;
-  p.up = id < w.nup;
-  if (p.up) {
-    const int u = id / w.PU;
-    p.part = id - u * w.PU;
-    p.s = u / w.NB;
-    p.b = u - p.s * w.NB;
-    p.k0 = cut_at(w.KA, p.part, w.PU);
-    p.k1 = cut_at(w.KA, p.part + 1, w.PU);
-  } else {
-    // (parts of the same rows side by side: with all CTAs on the same quarter of every 2 KB row HBM gave 4.3 TB/s)
-    const int q = id - w.nup, u = q / w.PD;
-    p.part = q - u * w.PD;
-    p.s = u / w.RP;
-    p.b = u - p.s * w.RP;
-    p.k0 = cut_at(w.KI, p.part, w.PD);
-    p.k1 = cut_at(w.KI, p.part + 1, w.PD);
-  }
-  return p;
-}
-
 // y from the rows of o, by the epilogue's four warps: blocks of 128 columns of a token, IT at once. A warp adds every fourth of the
 // token's experts, and the four sums (in `sums`, shared memory) are added in order.
 // Not inlined, so that a first call which only goes through it (`real` false: it reads and writes no global memory) fetches
@@ -518,17 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   make_plan(a, c.plan, blockIdx.x == 0);                   // (ends with a barrier)
   tc_fence_after();
   const uint32_t tmem = c.tmem;
-  Work w;
-  w.KA = a.d >> 7;
-  w.KI = a.I >> 7;
-  w.NB = a.I >> 7;
-  w.RP = ((a.d >> 7) + 1) >> 1;
-  w.slots = c.plan.slots;
-  const int ctas = static_cast<int>(gridDim.x);
-  w.PU = w.slots > 0 ? parts_of(w.slots * w.NB, w.KA, ctas, kUpPieces) : 1;
-  w.PD = w.slots > 0 ? parts_of(w.slots * w.RP, w.KI, ctas, kDownPieces) : 1;
-  w.nup = w.slots * w.NB * w.PU;
-  w.total = w.nup + w.slots * w.RP * w.PD;
+  const Work w = few::work_of(a.d, a.I, c.plan.slots, static_cast<int>(gridDim.x));
   int* done = a.cnt + 1;
   int* ready = a.cnt + 2;
   int* parts = ready + w.slots;
@@ -571,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       q.step(kQueue);
       if (!more) break;
-      const Piece p = piece_of(w, id);
+      const Piece p = few::piece_of(w, id);
       const int n = c.plan.expert[p.s], e = n < a.S ? a.E : n - a.S, K = p.up ? w.KA : w.KI;   // (e: its place in the weights)
       const int row = __shfl_sync(0xffffffffu, p.up ? e * 2 * a.I + p.b * 256 : e * a.d + p.b * 256, 0);
       const int tiles = p.up || 2 * p.b + 1 < w.KA ? 2 : 1;
@@ -603,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int issued = 0;
     int have = -1;                                         // the last expert whose h was found complete
     for (int id; ok && (id = next_piece()) >= 0;) {
-      const Piece p = piece_of(w, id);
+      const Piece p = few::piece_of(w, id);
       const int row = p.up ? 0 : c.plan.first[p.s];
       const int boxes = p.up ? a.N >> 4 : (c.plan.first[p.s + 1] - row + 15) >> 4;
       const CUtensorMap* map = p.up ? &tma_x : &tma_h;
@@ -636,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Stage st, acc;
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sf0 = smem_u32(scales);
     for (int id; ok && (id = next_piece()) >= 0;) {
-      const Piece p = piece_of(w, id);
+      const Piece p = few::piece_of(w, id);
       const int tiles = p.up || 2 * p.b + 1 < w.KA ? 2 : 1;
       const int cols = __shfl_sync(0xffffffffu, p.up ? a.N : (c.plan.first[p.s + 1] - c.plan.first[p.s] + 15) & ~15, 0);
       const uint32_t idesc = idesc_mxf8(128, 0) | (static_cast<uint32_t>(cols >> 3) << 17);
@@ -686,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = !epilogue_or(!ok);
       if (!ok || id < 0) break;
       tc_fence_after();
-      const Piece p = piece_of(w, id);
+      const Piece p = few::piece_of(w, id);
       const int row0 = c.plan.first[p.s], n = c.plan.first[p.s + 1] - row0;
       const uint32_t tacc = tmem + (static_cast<uint32_t>(lq * 32) << 16) + acc.i * 128;
       if (p.up) {
@@ -790,7 +736,7 @@ struct FewLayout {
   int64_t ncnt;
 };
 
-// Most and fewest experts in use.
+// Most experts in use.
 int64_t most_slots(const moe_config_t* c) {
   const int64_t chosen = static_cast<int64_t>(c->T) * c->k;
   return (chosen < c->E ? chosen : c->E) + c->n_shared;
@@ -814,15 +760,9 @@ FewLayout few_layout(const moe_config_t* c) {
   L.xsf = add(d / 128 * 512);
   L.hq = add((rows + 16) * I);
   L.hsf = add(slots * (I / 128) * 512);
-  // Rows times parts are bounded whatever the choice: with s experts in use rows are at most T min(s, k + n_shared), and
-  // parts at most ctas want / (s blocks) + 1.
-  const size_t I128 = I / 128, d128 = d / 128;
-  auto bound = [&](size_t steps, size_t blocks, size_t want) {
-    const size_t most = steps / kMinSteps > 1 ? steps / kMinSteps : 1;
-    const size_t all = T * (ceil_div(kMaxSms * want, blocks) + c->k + c->n_shared);
-    return all < rows * most ? all : rows * most;
-  };
-  const size_t gu = bound(d128, I128, kUpPieces), o = bound(I128, (d128 + 1) / 2, kDownPieces);
+  const int64_t I128 = c->I / 128, d128 = c->d / 128, picks = c->k + c->n_shared;
+  const size_t gu = few::parts_room(c->T, picks, kMaxSms, d128, I128, few::kUpPieces);
+  const size_t o = few::parts_room(c->T, picks, kMaxSms, I128, (d128 + 1) / 2, few::kDownPieces);
   L.gu = add(gu * I128 * 256 * sizeof(float));
   L.o = add(o * d * sizeof(float));
   L.total = cur;
