@@ -32,23 +32,24 @@ MOE_HD int cut_at(int steps, int i, int n) {
   return at < steps ? at : steps;
 }
 
-// The list: `slots` experts in use, d and I columns, `ctas` CTAs.
+// The list of a layer's d and I columns, the `slots` experts in use and `ctas` CTAs.
 struct Work {
   int KA, KI, NB, RP, slots;               // steps of d and of I, blocks of 256 up and of 256 down rows, experts in use
   int PU, PD, nup, total;                  // parts, pieces
 };
-MOE_HD Work work_of(int d, int I, int slots, int ctas) {
-  Work w;
-  w.KA = d >> 7;
-  w.KI = I >> 7;
-  w.NB = I >> 7;
-  w.RP = ((d >> 7) + 1) >> 1;
-  w.slots = slots;
-  w.PU = slots > 0 ? parts_of(slots * w.NB, w.KA, ctas, kUpPieces) : 1;
-  w.PD = slots > 0 ? parts_of(slots * w.RP, w.KI, ctas, kDownPieces) : 1;
-  w.nup = slots * w.NB * w.PU;
-  w.total = w.nup + slots * w.RP * w.PD;
-  return w;
+// (Filled in place from the kernel's own arguments and plan: with numbers for arguments the compiler makes 2.7 KB more code of the
+// kernel, and every call takes 0.2 to 0.8 % longer.)
+template <typename Args, typename Plan>
+MOE_HD void work_of(Work& w, const Args& a, const Plan& p, int ctas) {
+  w.KA = a.d >> 7;
+  w.KI = a.I >> 7;
+  w.NB = a.I >> 7;
+  w.RP = ((a.d >> 7) + 1) >> 1;
+  w.slots = p.slots;
+  w.PU = w.slots > 0 ? parts_of(w.slots * w.NB, w.KA, ctas, kUpPieces) : 1;
+  w.PD = w.slots > 0 ? parts_of(w.slots * w.RP, w.KI, ctas, kDownPieces) : 1;
+  w.nup = w.slots * w.NB * w.PU;
+  w.total = w.nup + w.slots * w.RP * w.PD;
 }
 struct Piece {
   bool up;

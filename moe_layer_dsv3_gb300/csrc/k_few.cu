@@ -474,7 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   make_plan(a, c.plan, blockIdx.x == 0);                   // (ends with a barrier)
   tc_fence_after();
   const uint32_t tmem = c.tmem;
-  const Work w = few::work_of(a.d, a.I, c.plan.slots, static_cast<int>(gridDim.x));
+  Work w;
+  few::work_of(w, a, c.plan, static_cast<int>(gridDim.x));
   int* done = a.cnt + 1;
   int* ready = a.cnt + 2;
   int* parts = ready + w.slots;

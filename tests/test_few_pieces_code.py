@@ -15,15 +15,22 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 CODE = """
 #include "few_pieces.h"
 using namespace moe::few;
+struct Args { int d, I; };
+struct Plan { int slots; };
+static Work list_of(int d, int I, int slots, int ctas) {
+  Work w;
+  work_of(w, Args{d, I}, Plan{slots}, ctas);
+  return w;
+}
 extern "C" {
 int consts(int i) { const int c[] = {kUpPieces, kDownPieces, kMinSteps}; return c[i]; }
 void work(int d, int I, int slots, int ctas, int* out) {
-  const Work w = work_of(d, I, slots, ctas);
+  const Work w = list_of(d, I, slots, ctas);
   const int c[] = {w.KA, w.KI, w.NB, w.RP, w.PU, w.PD, w.nup, w.total};
   for (int i = 0; i < 8; ++i) out[i] = c[i];
 }
 void pieces(int d, int I, int slots, int ctas, int from, int n, int* out) {
-  const Work w = work_of(d, I, slots, ctas);
+  const Work w = list_of(d, I, slots, ctas);
   for (int i = 0; i < n; ++i) {
     const Piece p = piece_of(w, from + i);
     const int c[] = {p.up, p.s, p.b, p.part, p.k0, p.k1};
