@@ -14,8 +14,10 @@
 namespace moe {
 namespace few {
 
-// Pieces of a CTA that K is cut for, where there are fewer. More of them (4 and 8) balance better and cost the joining of
-// parts: 83.1 and 80.5 us for one token of 9 wide experts, 58.0 and 55.9 for 5 tokens of 38 narrow ones, nothing elsewhere.
+// Pieces of a CTA that K is cut for, where there are fewer, up and down. More of them balance better and cost the joining of
+// parts. One token of 9 wide experts: 74.9 us with 1 and 2, 78.4 with 1 and 1, 76.4 with 1 and 4, 77.5 with 2 and 4, 79.1 with 4
+// and 8. Five tokens of 37 narrow ones: 47.1, 47.2, 47.0, 49.2, 50.7. From 16 tokens on within 1 %, but for narrow experts with 4
+// and 8 (80 instead of 77).
 constexpr int kUpPieces = 1, kDownPieces = 2;
 constexpr int kMinSteps = 2;               // fewest 128-wide steps of a part
 

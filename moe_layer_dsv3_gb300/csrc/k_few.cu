@@ -25,11 +25,11 @@
 // CTA that runs and waits for nothing later, so no wait needs all CTAs to be resident. Which CTA
 // takes a piece changes no result: parts and sums have a fixed order.
 //
-// Taken from a list, pieces keep every SM loading to the end. Equal ranges fixed in
-// advance, in a kernel for each projection, left some SMs 15 % behind the others (HBM does
-// not serve all alike), and HBM idle for 9 us between the kernels: 106 us for one
-// token of 9 such experts, 403 for 16 tokens and 47 experts, 544 for 64 and 61, where the list takes
-// 75, 320 to 330 and 413 to 424: 5.5, 6.6 and 6.6 TB/s of the weights read.
+// Taken from a list, pieces keep every SM loading to the end: 75 us for one token of 9 such
+// experts, 320 to 330 for 16 tokens and 47 experts, 413 to 426 for 64 and 61 (5.5, 6.6 and 6.6 TB/s of the
+// weights read). Behind a router of 256 experts: 81 us for one token, 448 for 16 and 67 experts, 748 for 64 and 110.
+// The first build of this file, equal ranges fixed in advance in a kernel for each projection, left some SMs
+// 15 % behind the others (HBM does not serve all alike) and HBM idle for 9 us between the kernels: 106, 403 and 544 us.
 #include <cudaTypedefs.h>
 
 #include "few_pieces.h"
@@ -118,8 +118,8 @@ __device__ __forceinline__ int atom_add_acq_rel(int* p, int v) {
 
 // ---------------------------------------------------------------- route
 // Logits: the eight warps of a CTA share the columns of ER rows of Wr, for TG tokens, in
-// fp32 on the CUDA cores: two rounds of loads at 7168 columns, where the tensor cores would wait for
-// one CTA's chain of 112 stages. One token, 64 experts: logits after 2.0 us, the last CTA found after 3.2, the choice
+// fp32 on the CUDA cores: one round of loads at 7168 columns for one token, two for eight, where the tensor cores would wait
+// for one CTA's chain of 112 stages. One token, 64 experts: logits after 2.0 us, the last CTA found after 3.2, the choice
 // written after 5.3. The CTA that finishes a group of tokens last
 // chooses for them. Further CTAs quantise x and clear the counters of the kernel that follows.
 constexpr int kRouteThreads = 256;
@@ -342,7 +342,8 @@ struct Stage {
 // y from the rows of o, by the epilogue's four warps: blocks of 128 columns of a token, IT at once. A warp adds every fourth of the
 // token's experts, and the four sums (in `sums`, shared memory) are added in order.
 // Not inlined, so that a first call which only goes through it (`real` false: it reads and writes no global memory) fetches
-// the code while the router works: at the end of the list, one miss after another, that took 6 of 54 us at 5 tokens.
+// the code while the router works: at the end of the list, one miss after another, that took 6 of 54 us at 5 tokens (in the
+// build before this).
 template <int IT>
 __device__ __noinline__ void sum_blocks(const FewArgs& a, const FewPlan& p, float4* sums_, int PD, bool real) {
   float4 (*sums)[4][32] = reinterpret_cast<float4 (*)[4][32]>(sums_);
@@ -417,8 +418,9 @@ __device__ __noinline__ void sum_blocks(const FewArgs& a, const FewPlan& p, floa
     named_barrier(1, 128);
   }
 }
-// One block at once where there is no more than one a CTA: four at once cost 89 us instead of 80 for one token (more code to
-// fetch), and 446 instead of 453 for 64.
+// One block at once where there is no more than one a CTA. With four throughout (more code to fetch) one token takes 75.7 us
+// instead of 74.9 and five of narrow experts 49.4 instead of 47.1; with one throughout 64 tokens take 431 instead of 417. Between
+// them one would do a little better (4 tokens 173 instead of 175, 16 of narrow experts 75.4 instead of 77.0).
 __device__ __forceinline__ void sum_y(const FewArgs& a, const FewPlan& p, float4* sums, int PD, bool real) {
   if (a.T * (a.d >> 7) <= static_cast<int>(gridDim.x)) sum_blocks<1>(a, p, sums, PD, real);
   else sum_blocks<4>(a, p, sums, PD, real);
@@ -617,7 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const int lq = warp & 3, row = lq * 32 + lane;
     Stage acc;
-    // MX(h) of a token: its 32 values lie in the warp's lanes.
+    // MX(h) of a token: its 32 values lie in the warp's lanes. silu by the fast exponential and quotient, as in the layer's own
+    // epilogue: off by about (6 + 1.2 |g|) 2^-23 of itself, where the E4M3 code that h is rounded to has a half step of 2^-4.
     auto emit = [&](int s, int r, int b, float g, float u) {
       const float h = __fdividef(g, 1.0f + __expf(-g)) * u;
       const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(h)));
@@ -857,8 +860,9 @@ extern "C" int moe_few_forward(const moe_config_t* cfg, const void* x, const voi
     launch_kernel_after("few_route", kern, dim3(static_cast<unsigned>(blocks)), dim3(kRouteThreads), 9 * a.E * sizeof(float), s, a);
   };
   const int per = static_cast<int>(ceil_div(a.E, 32));     // experts a lane of the choosing warp
-  // A row of Wr for one token, or two rows for eight: 121 and 126 us for the whole call at 2 tokens of 7168 columns and 64
-  // experts, 200 and 197 at 4 tokens, 453 and 446 at 64.
+  // A row of Wr for one token, or two rows for eight. Whole calls of 7168 columns, in us: with 64 experts 75 and 77 for 1 token,
+  // 120 and 122 for 2, 171 and 175 for 4, 327 and 330 for 16, 425 and 417 for 64; with 256 experts 80 and 84, 127 and 130, 194
+  // and 197, 452 and 447, 773 and 748. (So the border could lie a little higher, at 4 to 16 tokens as the experts are.)
   if (a.T <= 2) {
     if (per <= 2) route(few_route_kernel<1, 1, 2>, 1, 1);
     else if (per <= 4) route(few_route_kernel<1, 1, 4>, 1, 1);

@@ -1034,7 +1034,9 @@ extern "C" int moe_mla_decode_tree(const moe_mla_config_t* cfg, int drafts, cons
   if (int r = refuse_decode(cfg, q, q_stride_b, q_stride_h, cache, block_table, seq_lens, out, lse, ws))
     return r;
   // A sequence's rows in groups that one worker takes: up to 128 where the pair form does, else up to 64. Pairs also where they are
-  // not full: 48 x ~8192 tokens with 80 rows take 109 us on pairs and 156 in two groups of 40 on single CTAs.
+  // not full. In us, after a flushed L2, on pairs and in groups of up to 64 on single CTAs: 48 x ~8192 tokens with 80 rows 108 and
+  // 156, 64 x ~1000 with 80 44 and 56, 4 x ~1500 with 80 27 and 31, 16 x ~4000 with 160 53 and 58. Of ten sizes one is the other
+  // way round: 23 x ~700 with 140 rows, two groups of 70 or three of 47, 37.5 and 36.
   MlaArgs a{};
   a.H = drafts * cfg->heads;
   a.V = static_cast<int>(ceil_div(a.H, cfg->latent % 256 == 0 ? 2 * kMaxHeadsCta : kMaxHeadsCta));

@@ -14,9 +14,9 @@
 // 6 MB, 1 us at the copy rate). So it is one launch, in which every CTA makes
 // the prefix sums for itself; lengths and count are stored by the CTA that
 // arrives last, when every other has read them, so that they may be updated in place.
-// Measured in a graph of such calls: 5.0 us a call for 96 sequences with a token each, 7.6
-// for 512 of which some grow and some shrink, 7 for 37 prompts of 524288 tokens; called from
-// Python the host's 7 to 8 us bound it.
+// Measured in a graph of such calls: 4.5 to 5.7 us a call for 96 sequences with a token each, 7.1 to 8.8
+// for 512 of which some grow and some shrink, 8.0 for 37 prompts of 524288 tokens; called from
+// Python the host's 8 to 9 us bound it.
 #include "moe_internal.h"
 #include "pages_sums.h"
 #include "prof.h"
