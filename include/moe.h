@@ -509,7 +509,8 @@ MOE_API int moe_mla_decode(const moe_mla_config_t* cfg, const void* q, int64_t q
  *      for moe_mla_decode, over the tokens that are seen. Rows of tokens past
  *      the sequence's drafted ones, and rows that see nothing, get zeros and -inf.
  * With one drafted token a sequence this is moe_mla_decode. A cached row that is not
- * finite reaches every drafted token of its sequence: its column is NaN also where p is 0.
+ * finite reaches every drafted token of its sequence that sees anything: its column is NaN also
+ * where p is 0.
  * A count outside [0, min(drafts, seq_lens)] is clamped and sets the status to
  * MOE_ERR_BOUNDS; everything else is as for moe_mla_decode, the workspace too. */
 #define MOE_MLA_MAX_DRAFTS 64

@@ -602,8 +602,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t w[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                w[k] = pack_bf16x2(__uint_as_float(o[4 * i + 2 * k]) * f[i + (k >> 1)].x,
-                                   __uint_as_float(o[4 * i + 2 * k + 1]) * f[i + (k >> 1)].y);
+                w[k] = pack_bf16x2(normed<TREE>(__uint_as_float(o[4 * i + 2 * k]), f[i + (k >> 1)].x),
+                                   normed<TREE>(__uint_as_float(o[4 * i + 2 * k + 1]), f[i + (k >> 1)].y));
               const int h = 8 * (i + (lane >> 4)) + (lane & 7);
               stmatrix_x4_trans(smem_u32(stage) + h * 32 + ((((lane >> 3) ^ (h >> 2)) & 1) << 4), w[0], w[1], w[2], w[3]);
             }

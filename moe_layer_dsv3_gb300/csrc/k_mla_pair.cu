@@ -680,10 +680,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 f0 = f[4 * i], f1 = f[4 * i + 4];
             const int h = 8 * (i + (lane >> 4)) + (lane & 7);
             stmatrix_x4_trans(smem_u32(stage) + h * 32 + ((((lane >> 3) ^ (h >> 2)) & 1) << 4),
-                              pack_bf16x2(__uint_as_float(o[4 * i]) * f0.x, __uint_as_float(o[4 * i + 1]) * f0.y),
-                              pack_bf16x2(__uint_as_float(o[4 * i + 2]) * f0.x, __uint_as_float(o[4 * i + 3]) * f0.y),
-                              pack_bf16x2(__uint_as_float(o[4 * i + 4]) * f1.x, __uint_as_float(o[4 * i + 5]) * f1.y),
-                              pack_bf16x2(__uint_as_float(o[4 * i + 6]) * f1.x, __uint_as_float(o[4 * i + 7]) * f1.y));
+                              pack_bf16x2(normed<TREE>(__uint_as_float(o[4 * i]), f0.x), normed<TREE>(__uint_as_float(o[4 * i + 1]), f0.y)),
+                              pack_bf16x2(normed<TREE>(__uint_as_float(o[4 * i + 2]), f0.x), normed<TREE>(__uint_as_float(o[4 * i + 3]), f0.y)),
+                              pack_bf16x2(normed<TREE>(__uint_as_float(o[4 * i + 4]), f1.x), normed<TREE>(__uint_as_float(o[4 * i + 5]), f1.y)),
+                              pack_bf16x2(normed<TREE>(__uint_as_float(o[4 * i + 6]), f1.x), normed<TREE>(__uint_as_float(o[4 * i + 7]), f1.y)));
           }
           __syncwarp();
           const int g0 = grp * a.hg, gn = heads_of(item, g0);

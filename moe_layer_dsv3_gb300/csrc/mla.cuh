@@ -109,6 +109,14 @@ __device__ __forceinline__ uint64_t sees(const Sight& s, int prefix, int at) {
   return before > -64 ? s.mask >> -before : 0;
 }
 
+// An output's sum times its row's factor, the reciprocal of the row's sum of P. (TREE) A row that sees nothing has a factor of 0 and
+// is zero whatever the cache holds: its P are all 0, and the product gave NaN where a cached row is not finite.
+template <bool TREE>
+__device__ __forceinline__ float normed(float o, float f) {
+  if constexpr (TREE) return f == 0.0f ? 0.0f : o * f;
+  else return o * f;
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -552,7 +560,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) mla_join_kernel(const __grid_
       for (int k = 0; k < 4; ++k) {
         const float got = __shfl_xor_sync(0xffffffffu, odd ? x[k] : y[k], 4);
         const uint32_t v = odd ? pack_bf16x2(got, y[k]) : pack_bf16x2(x[k], got);
-        if (hl + odd < nh) *reinterpret_cast<uint32_t*>(out + c * 128 + 8 * k) = v;
+        // (a row that sees nothing: see normed, which took 0.06 us more here than one choice a store)
+        if (hl + odd < nh) *reinterpret_cast<uint32_t*>(out + c * 128 + 8 * k) = TREE && (odd ? iy : ix) == 0.0f ? 0u : v;
       }
     }
   };
