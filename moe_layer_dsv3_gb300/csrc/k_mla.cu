@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (active) {
           if constexpr (TREE) {
             const int t64 = (wk.t0 + ti) * kTile;
-            if (t64 + kTile > prefix || !sight[0].live || !sight[1].live) {
+            if (prefix - t64 < kTile || !sight[0].live || !sight[1].live) {
               uint64_t see[2];
 #pragma unroll
               for (int k = 0; k < 2; ++k) see[k] = sees(sight[k], prefix, t64) >> (2 * (lane & 3));

@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive(se0);
         if constexpr (TREE) {
           const int at = (wk.t0 + ti) * kTile + blk * kBlock + sub * 32;
-          if (at + 32 > prefix || !sight.live) {
+          if (prefix - at < 32 || !sight.live) {
             const uint32_t see = static_cast<uint32_t>(sees(sight, prefix, at));
 #pragma unroll
             for (int i = 0; i < 32; ++i)
