@@ -157,10 +157,10 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
         if (i0 + k >= N) continue;
         while (starts[b + 1] <= i) ++b;    // (sequences without new tokens lie between)
         s[k] = b;
-        p[k] = len[b] + i - starts[b];
+        p[k] = pages::nth(len[b], i, starts[b]);
         const int j = p[k] / a.page, old = pages_of(len[b]);
         in[k] = p[k] - j * a.page;
-        at_page[k] = j < old ? a.table + static_cast<int64_t>(b) * a.max_pages + j : taken_at(taken[b] + j - old);
+        at_page[k] = j < old ? a.table + static_cast<int64_t>(b) * a.max_pages + j : taken_at(pages::nth(taken[b], j, old));
       }
       int page[kTokens];
 #pragma unroll

@@ -32,6 +32,9 @@ struct Sums {
 
 MOE_HD int pages_of(int tokens, int page) { return (tokens + page - 1) / page; }   // (capacity + page is below 2^31)
 
+// Number i of a list whose number `first` is `base`. (base + i may pass 2^31, the result does not.)
+MOE_HD int nth(int base, int i, int first) { return base + (i - first); }
+
 // What a sequence that goes from n to m tokens, both in [0, capacity], adds to them.
 MOE_HD Sums sums_of(int n, int m, int page) {
   const int o = pages_of(n, page), w = pages_of(m, page);
