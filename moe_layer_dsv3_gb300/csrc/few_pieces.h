@@ -79,6 +79,25 @@ MOE_HD Piece piece_of(const Work& w, int id) {
   return p;
 }
 
+// Accumulators. The tensor core truncates when it adds into TMEM: with products of one sign the sums of 448 additions (14336 columns)
+// were 67 x 2^-23 of themselves too small, and with random ones over 7168 columns 5 of 295000 values of h took the neighbouring code
+// of MX(h), or a block's scale the neighbouring power of two (which moved a token's y by up to 2 %), where sums rounded to nearest
+// give 1. So K of an up piece is cut into chunks with accumulators of their own, which the epilogue adds: up to four, as TMEM has room
+// for them and for the next piece's first. That leaves 7 x 2^-23, and 2 values of 295000. It costs 0.3 to 0.6 us for one token and for
+// five of narrow experts, 0.7 of 317 for 16 and 0.3 of 416 for 64. (A down piece's sums are rounded, not quantised.)
+constexpr int kAccCols = 440;              // TMEM columns of accumulators, two tiles of N columns each
+constexpr int kMaxChunks = 4;
+constexpr int kMinChunkSteps = 14;
+MOE_HD int acc_slots(int N) { return kAccCols / (2 * N); }   // 13, 6, 4 and 3 for 16 to 64 columns
+constexpr int kMaxSlots = kAccCols / 32;
+MOE_HD int chunks_of(const Piece& p, int N) {
+  if (!p.up) return 1;
+  const int fit = acc_slots(N) - 1, most = fit < kMaxChunks ? fit : kMaxChunks, n = (p.k1 - p.k0) / kMinChunkSteps;
+  return n < 1 ? 1 : n < most ? n : most;
+}
+// First step of chunk i of n.
+MOE_HD int chunk_at(const Piece& p, int i, int n) { return p.k0 + (p.k1 - p.k0) * i / n; }
+
 // Rows times parts of a product of `steps` steps over `blocks` blocks of rows an expert, whatever T tokens choose of `picks` experts
 // each (a shared one among them) on up to `ctas` CTAs: with s experts in use rows are at most T min(s, picks), and parts at
 // most ctas want / (s blocks) + 1.

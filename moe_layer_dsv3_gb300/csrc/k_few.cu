@@ -51,7 +51,8 @@ constexpr int kThreads = 224;
 constexpr int kMaxStages = 6;             // of the ring: 6 fit at 16 tokens, 5 at 64 (4 cost 1 to 2 %, 2 cost 10)
 constexpr int kTileBytes = 128 * 128;      // a weight tile: 128 rows x 128 values
 constexpr int kSmemMax = 232448;
-constexpr int kSfCol = 256;                // TMEM: accumulators below, scales of the ring's stages from here on
+constexpr int kSfCol = few::kAccCols;      // TMEM: accumulators below, scales of the ring's stages from here on
+static_assert(kSfCol + 12 * kMaxStages <= 512, "TMEM columns");
 constexpr int kQueue = 4;                  // pieces on their way from the warp that takes them to the others
 static_assert(kMaxT == 64, "a token is a bit of an expert's 64-bit mask");
 
@@ -318,7 +319,7 @@ __device__ __forceinline__ void make_plan(const FewArgs& a, FewPlan& p, bool rep
 
 struct FewSmem {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t accf[2], acce[2];
+  uint64_t accf[few::kMaxSlots], acce[few::kMaxSlots];   // of accumulator slots: a piece that ends there is done; read
   uint64_t qf[kQueue], qe[kQueue];
   int queue[kQueue];                       // pieces, -1 after the last
   uint32_t tmem;
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c.full[i], 2);                            // the two loading warps
       mbar_init(&c.empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < few::kMaxSlots; ++i) {
       mbar_init(&c.accf[i], 1);
       mbar_init(&c.acce[i], 128);
     }
@@ -481,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* done = a.cnt + 1;
   int* ready = a.cnt + 2;
   int* parts = ready + w.slots;
+  const int slots = few::acc_slots(a.N);                   // of accumulators
   bool ok = true;
   // The next piece, for the warps that follow warp 0.
   Stage q;
@@ -582,43 +584,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     land(st, issued);
   } else if (warp == 1) {
-    Stage st, acc;
+    Stage st;
+    int slot = 0;                                          // of the next chunk
+    uint32_t used = 0;                                     // bit s: parity of slot s's uses
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), sf0 = smem_u32(scales);
     for (int id; ok && (id = next_piece()) >= 0;) {
       const Piece p = few::piece_of(w, id);
       const int tiles = p.up || 2 * p.b + 1 < w.KA ? 2 : 1;
       const int cols = __shfl_sync(0xffffffffu, p.up ? a.N : (c.plan.first[p.s + 1] - c.plan.first[p.s] + 15) & ~15, 0);
       const uint32_t idesc = idesc_mxf8(128, 0) | (static_cast<uint32_t>(cols >> 3) << 17);
-      ok = warp_wait(&c.acce[acc.i], acc.phase ^ 1u, a.status, 207);
-      const uint32_t d = tm + acc.i * 128;
+      const int chunks = few::chunks_of(p, a.N);
+      int k = p.k0;
 #pragma unroll 1
-      for (int k = p.k0; k < p.k1 && ok; ++k) {
-        ok = warp_wait(&c.full[st.i], st.phase, a.status, 208);
-        tc_fence_after();
-        if (ok && elect_one()) {
-          const uint32_t base = smem_u32(ring + st.i * a.stage_bytes), sf = tm + kSfCol + st.i * 12, sfs = sf0 + st.i * (3 * 512);
-          tc_cp_sf(sf + 8, desc_sf_chunk(sfs + 1024));
+      for (int chunk = 0; chunk < chunks && ok; ++chunk) {
+        ok = warp_wait(&c.acce[slot], (used >> slot & 1u) ^ 1u, a.status, 207);
+        used ^= 1u << slot;
+        const uint32_t d = tm + slot * 2 * a.N;
+        const int end = few::chunk_at(p, chunk + 1, chunks);
+        uint32_t more = 0;                                 // the chunk's first product starts its sums
+#pragma unroll 1
+        for (; k < end && ok; ++k) {
+          ok = warp_wait(&c.full[st.i], st.phase, a.status, 208);
+          tc_fence_after();
+          if (ok && elect_one()) {
+            const uint32_t base = smem_u32(ring + st.i * a.stage_bytes), sf = tm + kSfCol + st.i * 12, sfs = sf0 + st.i * (3 * 512);
+            tc_cp_sf(sf + 8, desc_sf_chunk(sfs + 1024));
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (j < tiles) {
-              tc_cp_sf(sf + 4 * j, desc_sf_chunk(sfs + 512 * j));
+            for (int j = 0; j < 2; ++j)
+              if (j < tiles) {
+                tc_cp_sf(sf + 4 * j, desc_sf_chunk(sfs + 512 * j));
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma_mxf8(d + 64 * j, desc_kmajor_sw128(base + j * kTileBytes + kk * 32),
-                            desc_kmajor_sw128(base + 2 * kTileBytes + kk * 32), idesc_mxf8_sf(idesc, kk, kk), sf + 4 * j, sf + 8,
-                            k > p.k0 || kk > 0);
-            }
-          tc_commit(&c.empty[st.i]);
-          if (k == p.k1 - 1) tc_commit(&c.accf[acc.i]);
+                for (int kk = 0; kk < 4; ++kk)
+                  tc_mma_mxf8(d + a.N * j, desc_kmajor_sw128(base + j * kTileBytes + kk * 32),
+                              desc_kmajor_sw128(base + 2 * kTileBytes + kk * 32), idesc_mxf8_sf(idesc, kk, kk), sf + 4 * j, sf + 8,
+                              more | (kk > 0));
+              }
+            tc_commit(&c.empty[st.i]);
+            if (k == p.k1 - 1) tc_commit(&c.accf[slot]);
+          }
+          __syncwarp();
+          st.step(a.nst);
+          more = 1;
         }
-        __syncwarp();
-        st.step(a.nst);
+        if (++slot == slots) slot = 0;
       }
-      acc.step(2);
     }
   } else {
     const int lq = warp & 3, row = lq * 32 + lane;
-    Stage acc;
+    int slot = 0;                                          // of the next piece's first chunk
+    uint32_t seen = 0;                                     // bit s: parity of the pieces that ended in slot s
     // MX(h) of a token: its 32 values lie in the warp's lanes. silu by the fast exponential and quotient, as in the layer's own
     // epilogue: off by about (6 + 1.2 |g|) 2^-23 of itself, where the E4M3 code that h is rounded to has a half step of 2^-4.
     auto emit = [&](int s, int r, int b, float g, float u) {
@@ -631,14 +645,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     while (true) {
       const int id = next_piece();
-      if (id >= 0) ok = mbar_wait(&c.accf[acc.i], acc.phase, a.status, 209);
+      const Piece p = few::piece_of(w, id >= 0 ? id : 0);
+      const int chunks = few::chunks_of(p, a.N);
+      const int first = slot;
+      slot += chunks;
+      const int last = slot - 1 < slots ? slot - 1 : slot - 1 - slots;
+      if (slot >= slots) slot -= slots;
+      if (id >= 0) ok = mbar_wait(&c.accf[last], seen >> last & 1u, a.status, 209);
+      seen ^= 1u << last;
       // Whether a wait gave up is the answer of all four warps, which meet at barriers below.
       ok = !epilogue_or(!ok);
       if (!ok || id < 0) break;
       tc_fence_after();
-      const Piece p = few::piece_of(w, id);
       const int row0 = c.plan.first[p.s], n = c.plan.first[p.s + 1] - row0;
-      const uint32_t tacc = tmem + (static_cast<uint32_t>(lq * 32) << 16) + acc.i * 128;
+      // The piece's accumulators have been read.
+      auto give_back = [&]() {
+        tc_fence_before();
+#pragma unroll 1
+        for (int j = 0, s = first; j < chunks; ++j) {
+          mbar_arrive(&c.acce[s]);
+          if (++s == slots) s = 0;
+        }
+      };
+      const uint32_t tacc = tmem + (static_cast<uint32_t>(lq * 32) << 16) + first * 2 * a.N;
       if (p.up) {
         const int e = c.plan.expert[p.s];
         const bool whole = w.PU == 1;
@@ -650,23 +679,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int r = 0; m != 0; ++r, m &= m - 1) {
           const int t = __ffsll(static_cast<long long>(m)) - 1;
-          uint32_t g, u;
-          tmem_ld1(tacc + t, g);
-          tmem_ld1(tacc + 64 + t, u);
-          tmem_wait_ld();
-          reg_fence(g);
-          reg_fence(u);
+          float g = 0.0f, u = 0.0f;
+#pragma unroll 1
+          for (int j = 0; j < chunks; ++j) {
+            const int back = first + j < slots ? j : j - slots;
+            uint32_t x[2];
+            tmem_ld1(tacc + back * 2 * a.N + t, x[0]);
+            tmem_ld1(tacc + (back * 2 + 1) * a.N + t, x[1]);
+            tmem_wait_ld();
+            reg_fence(x[0]);
+            reg_fence(x[1]);
+            g += __uint_as_float(x[0]);
+            u += __uint_as_float(x[1]);
+          }
           if (whole) {
-            emit(p.s, r, p.b, __uint_as_float(g), __uint_as_float(u));
+            emit(p.s, r, p.b, g, u);
           } else {
             float* to = gu + r * gu_step + p.part * 256;
-            to[0] = __uint_as_float(g);
-            to[128] = __uint_as_float(u);
+            to[0] = g;
+            to[128] = u;
           }
         }
-        tc_fence_before();
-        mbar_arrive(&c.acce[acc.i]);
-        acc.step(2);
+        give_back();
         if (!whole) {
           // The CTA that stores a block's last part adds all of them.
           named_barrier(1, 128);
@@ -701,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c0 = 0; c0 < n; c0 += 4) {
           uint32_t v[2][4];
           tmem_ld4(tacc + c0, v[0]);
-          tmem_ld4(tacc + 64 + c0, v[1]);
+          tmem_ld4(tacc + a.N + c0, v[1]);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 2; ++j)
@@ -711,9 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (j < tiles && c0 + i < n) o[(c0 + i) * o_step + j * 128] = __uint_as_float(v[j][i]);
             }
         }
-        tc_fence_before();
-        mbar_arrive(&c.acce[acc.i]);
-        acc.step(2);
+        give_back();
         named_barrier(1, 128);
         if (tid == 64) red_release_add(done, 1);
       }

@@ -37,6 +37,13 @@ void pieces(int d, int I, int slots, int ctas, int from, int n, int* out) {
     for (int k = 0; k < 6; ++k) out[6 * i + k] = c[k];
   }
 }
+int slots_of(int N) { return acc_slots(N); }
+int chunks(int up, int k0, int k1, int N, int* at) {
+  const Piece p{up != 0, 0, 0, 0, k0, k1};
+  const int n = chunks_of(p, N);
+  for (int i = 0; i <= n; ++i) at[i] = chunk_at(p, i, n);
+  return n;
+}
 long long room(long long T, long long picks, long long ctas, long long steps, long long blocks, long long want) {
   return parts_room(T, picks, ctas, steps, blocks, want);
 }
@@ -105,6 +112,23 @@ def test_ends_of_the_range(code):
                 assert end == steps
             code.pieces(d, inner, slots, ctas, w["total"] - 1, 1, out)
             assert list(out)[:4] == [0, slots - 1, (KA + 1) // 2 - 1, pd - 1] and out[5] == KI
+
+
+def test_chunks_of_a_piece(code):
+    """A piece's chunks are its steps in order, none empty, and leave an accumulator for the next piece's first one."""
+    at = (ctypes.c_int * 8)()
+    for N in (16, 32, 48, 64):
+        slots = code.slots_of(N)
+        assert slots * 2 * N <= 512 - 72 and slots <= 32    # (scales of six stages lie behind them; parities are bits)
+        for k0 in (0, 2, 28):
+            for steps in list(range(1, 60)) + [1000, 1 << 17]:
+                n = code.chunks(1, k0, k0 + steps, N, at)
+                assert 1 <= n <= min(4, slots - 1)
+                cuts = list(at)[:n + 1]
+                assert cuts[0] == k0 and cuts[-1] == k0 + steps and all(a < b for a, b in zip(cuts, cuts[1:]))
+                assert n == 1 or min(b - a for a, b in zip(cuts, cuts[1:])) >= 14
+                assert code.chunks(0, k0, k0 + steps, N, at) == 1 and list(at)[:2] == [k0, k0 + steps]
+        assert code.chunks(1, 0, 56, N, at) == min(4, slots - 1)
 
 
 def test_the_code_s_parts_fit(code):

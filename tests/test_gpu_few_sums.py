@@ -1,0 +1,48 @@
+"""The sums of g and u of moe_few_forward over long rows: short chains of additions in the tensor core, joined in fp32.
+
+An addition into TMEM may truncate: it is off by 2^-23 of the running sum at most, always towards zero, so with products of one
+sign a chain of n additions is off by up to sum_k 2^-23 k / n = (n + 1) / 2 * 2^-23 of its sum. A product of 32 columns adds
+once. 224 steps of 128 columns are two parts of 112 here, and those four chunks of 28: n = 112. The chunks are joined by three
+additions rounded to nearest, 2^-24 each; one more 2^-23 each for the products that an addition lines up. Values of several
+magnitudes, blocks of 32 in turn eight (so that sums do not fit 24 bits): running sums are up to eight additions ahead.
+"""
+import pytest
+import torch
+
+from tests.test_gpu_few import F, mx
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import moe_layer_dsv3_gb300 as m
+    return m
+
+
+def test_sums_of_long_rows(lib):
+    from moe_layer_dsv3_gb300.few import FewTokenMoE
+    d, I = 128 * 224, 128 * 100
+    g = torch.Generator(device="cuda").manual_seed(70)
+    rnd = lambda *s: torch.rand(*s, generator=g, device="cuda", dtype=torch.float32)
+    few = FewTokenMoE(1, d, 1, 1, I=I)
+    some = lambda *s: (1.0 + rnd(*s)) * torch.exp2(-torch.floor(4.0 * rnd(*s)))
+    gu = (some(1, 2 * I, d) * 2.0 ** -12).to(torch.bfloat16)
+    down = torch.zeros(1, d, I, dtype=torch.bfloat16, device="cuda")
+    few.quantize_weights(gu, down)
+    x = (some(1, d).view(-1, 32) * torch.exp2(-torch.arange(d // 32, device="cuda").remainder(8).float())[:, None]).view(1, d)
+    x = x.to(torch.bfloat16)
+    few.forward(x, torch.zeros(1, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, device="cuda"))
+    torch.cuda.synchronize()
+    assert few.status() == (0, 0)
+    up = lambda n: -(-n // 1024) * 1024                     # the workspace: what lies before the parts
+    at = sum(up(n) for n in (16 + 4 * 64, 4 * (2 + 1 + I // 128), 4, 64 * d, d // 128 * 512, (1 + 16) * I, I // 128 * 512))
+    got = few.ws[at:at + 100 * 2 * 256 * 4].view(torch.float32).view(100, 2, 2, 128).to(F)       # [block][part][g, u][row]
+    xq = mx(x.to(F))[0].view(2, d // 2)
+    want = torch.stack([torch.stack([mx(gu[0, r:r + 128].to(F)).view(128, 2, d // 2)[:, p] @ xq[p] for r in range(0, 2 * I, 128)])
+                        for p in range(2)])                 # [part][g blocks, then u blocks][row]
+    want = torch.stack([want[:, :100], want[:, 100:]], 2).permute(1, 0, 2, 3)
+    rel = (got - want).abs() / want
+    assert rel.max() <= ((112 + 1) / 2 + 8 + 1 + 3 / 2) * 2.0 ** -23, rel.max().item() * 2 ** 23
