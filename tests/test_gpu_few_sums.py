@@ -9,7 +9,7 @@ magnitudes, blocks of 32 in turn eight (so that sums do not fit 24 bits): runnin
 import pytest
 import torch
 
-from tests.test_gpu_few import F, mx
+from tests.test_gpu_few import Case, F, mx
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +46,13 @@ def test_sums_of_long_rows(lib):
     want = torch.stack([want[:, :100], want[:, 100:]], 2).permute(1, 0, 2, 3)
     rel = (got - want).abs() / want
     assert rel.max() <= ((112 + 1) / 2 + 8 + 1 + 3 / 2) * 2.0 ** -23, rel.max().item() * 2 ** 23
+
+
+@pytest.mark.parametrize("T", [1, 16, 17, 32, 40, 48, 56, 64])
+def test_chunks_of_every_width(lib, T):
+    """Several pieces a CTA whose rows are cut into chunks: the accumulators are walked around more than once."""
+    c = Case(T, 7168, 40, 4, 1, 1, 2048, 1, seed=80 + T, xgain=0.25, bias=0.05)
+    y = c.run().clone()
+    c.check(y)
+    for i in range(5):
+        assert torch.equal(c.run(), y)
