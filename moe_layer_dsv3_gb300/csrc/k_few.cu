@@ -26,7 +26,7 @@
 // takes a piece changes no result: parts and sums have a fixed order.
 //
 // Taken from a list, pieces keep every SM loading to the end: 75 us for one token of 9 such
-// experts, 320 to 330 for 16 tokens and 47 experts, 413 to 426 for 64 and 61 (5.5, 6.6 and 6.6 TB/s of the
+// experts, 312 to 340 for 16 tokens and 47 experts, 413 to 426 for 64 and 61 (5.5, 6.6 and 6.6 TB/s of the
 // weights read). Behind a router of 256 experts: 81 us for one token, 448 for 16 and 67 experts, 748 for 64 and 110.
 // The first build of this file, equal ranges fixed in advance in a kernel for each projection, left some SMs
 // 15 % behind the others (HBM does not serve all alike) and HBM idle for 9 us between the kernels: 106, 403 and 544 us.
